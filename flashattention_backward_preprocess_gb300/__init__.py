@@ -31,3 +31,9 @@ from .binding import (  # noqa: F401
     load_library,
 )
 from .autograd import FlashAttentionFunction, flash_attention  # noqa: F401
+from .packed import (  # noqa: F401
+    fa_page_slots,
+    fa_paged_fwd,
+    fa_paged_write,
+    fa_varlen_fwd,
+)

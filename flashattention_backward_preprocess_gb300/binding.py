@@ -30,7 +30,9 @@ _lib = None
 EXPORTS = ("fa_bwd", "fa_bwd_ex", "fa_bwd_noalloc", "fa_bwd_preprocess", "fa_fwd", "fa_fwd_ex", "fa_bwd_host",
            "fa_bwd_workspace_bytes",
            "fa_check_device", "fa_profile", "fa_profile_read", "fa_selftest_timeout",
-           "fa_last_error", "fa_shutdown", "fa_version")
+           "fa_last_error", "fa_shutdown", "fa_version",
+           "fa_varlen_fwd", "fa_varlen_workspace_bytes", "fa_paged_fwd", "fa_paged_workspace_bytes",
+           "fa_page_slots", "fa_paged_write")
 
 
 class FaError(RuntimeError):
@@ -79,6 +81,19 @@ def load_library(path: str | None = None):
         lib.fa_profile_read.restype = I
         lib.fa_selftest_timeout.argtypes = [ctypes.c_ulonglong, V]
         lib.fa_selftest_timeout.restype = I
+        Z = ctypes.c_size_t
+        lib.fa_varlen_fwd.argtypes = [V] * 7 + [I] * 6 + [V, F, I, I, I, I, V, Z, V]
+        lib.fa_varlen_fwd.restype = I
+        lib.fa_varlen_workspace_bytes.argtypes = [I] * 8
+        lib.fa_varlen_workspace_bytes.restype = Z
+        lib.fa_paged_fwd.argtypes = [V] * 8 + [I] * 8 + [V, F, I, I, I, I, V, Z, V]
+        lib.fa_paged_fwd.restype = I
+        lib.fa_paged_workspace_bytes.argtypes = [I] * 7
+        lib.fa_paged_workspace_bytes.restype = Z
+        lib.fa_page_slots.argtypes = [V] * 9 + [I] * 5 + [V]
+        lib.fa_page_slots.restype = I
+        lib.fa_paged_write.argtypes = [V] * 5 + [I] * 5 + [V, I, V]
+        lib.fa_paged_write.restype = I
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_version.restype = ctypes.c_char_p
         lib.fa_shutdown.restype = None

@@ -19,7 +19,8 @@ LIB = os.path.join(BUILD, "libfa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "preprocess.cu", "bwd_simt.cu", "fwd_simt.cu", "fwd_sm103.cu", "bwd_sm103.cu", "bwd_d256.cu",
-           "noalloc.cu", "selftest.cu"]
+           "noalloc.cu", "selftest.cu", "packed_api.cu", "packed_plan.cu", "packed_fwd.cu", "packed_simt.cu",
+           "paged_cache.cu"]
 
 
 def _nvcc() -> str:

@@ -16,6 +16,7 @@
 #include <utility>
 
 #include "fa_internal.cuh"
+#include "packed.cuh"
 
 namespace fa {
 namespace {
@@ -561,10 +562,21 @@ int fa_check_device(void* stream) {
     }
     // fa_bwd_noalloc records its timeouts in its own scratch, shared by every stream
     unsigned int na_word = 0;
-    const int rc = noalloc_take_error_word(&na_word);
+    int rc = noalloc_take_error_word(&na_word);
     if (rc != FA_OK) return rc;
+    // so do the packed and paged calls, in one word per device
+    unsigned int packed_word = 0;
+    rc = packed_take_error_word(&packed_word);
+    if (rc != FA_OK) return rc;
+    na_word |= packed_word;
     const int status = status_from_error_words(words[0], na_word);
     if (status == FA_ERR_TIMEOUT) return fail(FA_ERR_TIMEOUT, "device", "a bounded wait in a kernel timed out");
+    if (status == FA_ERR_INVALID_ARG)
+        return fail(status, "device",
+                    std::string("a packed or paged call was given") +
+                        (na_word & kErrLengths ? " sequence lengths that do not fit its tensors;" : "") +
+                        (na_word & kErrPage ? " a page or slot outside the cache;" : "") +
+                        (na_word & kErrPool ? " too few free pages or table columns;" : ""));
     if (status != FA_OK)
         return fail(status, "device", "kernel error word " + std::to_string(words[0] | na_word));
     return FA_OK;

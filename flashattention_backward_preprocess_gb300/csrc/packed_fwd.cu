@@ -1,0 +1,618 @@
+// packed_fwd.cu -- attention forward over packed sequences or a paged key/value cache for
+// GB300 (sm_103a), f16 / bf16, on the 5th-generation tensor cores.
+//
+//   s_ij = scale <q_i, k_j> over the keys j of i's own sequence that it sees (key_visible)
+//   O_i  = sum_j exp(s_ij) v_j / sum_j exp(s_ij),   LSE_i = log sum_j exp(s_ij)
+// with one pass over the keys (running max and sum per row); a row that sees no key gets
+// O = 0 and LSE = -inf.
+//
+// Design:
+//   * a tile packs tpt = 128 / g query tokens with the g query heads of one key/value head
+//     (one TMA box [64 columns, g heads, tpt tokens]), so keys and values are read once per
+//     group: a single-token step reads its cache once, whatever the number of query heads;
+//   * the plan kernel lays all (unit, key/value head, key tile) triples on one axis and gives
+//     each of the CTAs (one per SM) the same number of them.  One long request is spread over
+//     the whole grid by the same rule that packs a thousand short ones.  Items that a share's
+//     border cuts leave fp32 parts in the workspace; the CTA whose part arrives last joins
+//     them in order of the keys, so the result does not depend on which one that is;
+//   * K / V tiles come through a TMA ring.  Paged: one box per page, 128-byte swizzle, each
+//     lane of the producer warp looks up and issues its own boxes one tile ahead.  The rows of
+//     V behind the sequence's last key (another sequence's, or whatever a page holds) are
+//     zeroed in shared memory before the P V product: P is 0 there, but 0 * inf is not;
+//   * S = Q K^T and O += P V with tcgen05.mma, P as the TMEM A operand; three S buffers
+//     (two at d = 256); warps 0-3 softmax and epilogue (one row per thread), warp 4 TMA,
+//     warp 5 S products, warp 6 P V products.  The next item's loads and S products overlap
+//     this item's epilogue.  Softmax warps whose rows are all padding (single-token steps fill
+//     g of 128 rows) only pass the barriers on;
+//   * P is rounded to the inputs' 16-bit type for the product (the tensor core's operand type);
+//     the row sum adds the unrounded fp32 values;
+//   * every wait is bounded: a timeout records an error word, the roles drop out, TMEM is freed.
+#include <math.h>
+
+#include "bounded_wait.cuh"
+#include "packed.cuh"
+#include "tma_map.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int BM = 128;  // rows per tile
+constexpr int kThreads = 224;
+constexpr int kWarpTma = 4, kWarpMma = 5, kWarpPv = 6;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;  // move the running max only past this margin
+constexpr uint32_t kSoftBarrier = 1;
+
+template <int D>
+struct PCfg {
+    static constexpr int BN = D <= 128 ? 128 : 64;
+    static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 2);
+    static constexpr int NBUF = D <= 128 ? 3 : 2;
+    static constexpr int BOXES = D / 64;
+    static constexpr uint32_t kTileQ_B = BM * D * 2;
+    static constexpr uint32_t kTileKV_B = BN * D * 2;
+    static constexpr uint32_t kBoxQ_B = BM * 128;
+    static constexpr uint32_t kBoxKV_B = BN * 128;
+    static constexpr uint32_t OFF_Q = 0;
+    static constexpr uint32_t OFF_K = OFF_Q + kTileQ_B;
+    static constexpr uint32_t OFF_V = OFF_K + STAGES * kTileKV_B;
+    static constexpr uint32_t OFF_BAR = OFF_V + STAGES * kTileKV_B;
+    static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
+    // boxes of one K / V tile per producer lane (pages of 8 rows are the smallest)
+    static constexpr int PIECES = (BN / 8 * 2 * BOXES + 31) / 32;
+    static_assert(TM_O + D <= 512, "TMEM columns");
+};
+
+enum {
+    P_Q = 0,               // Q tile landed (TMA)
+    P_S0,                  // S in buffer b (MMA commit), three slots
+    P_P0 = P_S0 + 3,       // P packed in buffer b (4 softmax warps), three slots
+    P_PV0 = P_P0 + 3,      // P V product of buffer b done (MMA commit), three slots
+    P_FINAL = P_PV0 + 3,   // every product done
+    P_QE,                  // the item's S products are done: the Q tile may be reloaded
+    P_OFULL,               // O of an item complete
+    P_OFREE,               // O of an item read (4 softmax warps)
+    P_STAGE0               // STAGES "full", then STAGES "empty"
+};
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+template <bool kBF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (kBF16) {
+        __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t*>(&v);
+    }
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+template <typename T, int D, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const PackedFwd a, const FwdPlan plan, int tpt) {
+    using C = PCfg<D>;
+    constexpr int BN = C::BN, NB = C::NBUF;
+    constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
+    constexpr int kNumBars = P_STAGE0 + 2 * C::STAGES;
+    constexpr uint32_t OFF_MISC = C::OFF_BAR + kNumBars * 8;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC + 4);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
+    auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
+    auto bar_full = [&](int s) { return bar(P_STAGE0 + s); };
+    auto bar_empty = [&](int s) { return bar(P_STAGE0 + C::STAGES + s); };
+    const int g = a.H / a.H_kv;
+    unsigned int* err = a.err;
+
+    if (threadIdx.x == 0) {
+        if ((sbase & 1023u) != 0) atomicOr(err, kErrSmemAlign);
+        *abort_flag = (sbase & 1023u) != 0;
+        for (int i = 0; i < kNumBars; ++i)
+            ptx::mbar_init(bar(i), ((i >= P_P0 && i < P_P0 + 3) || i == P_OFREE) ? 4u : 1u);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(sbase + OFF_MISC + 4, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();  // the plan
+
+    // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
+    // CTA (jg), per-item ones its segments with work (ka).
+    if (warp == kWarpTma) {
+        // ------------------------------------------------------------ producer
+        // Two streams over the same segments, polled in turn: the Q tile (once the previous
+        // item's S products are done) and the K / V ring.  Lane 0 polls; every lane issues its
+        // own boxes of a K / V tile.
+        if (!*abort_flag) {
+            FwdWalk wq, wk;
+            bool q_more = wq.init(plan, blockIdx.x, a.H_kv), kv_more = wk.init(plan, blockIdx.x, a.H_kv);
+            while (q_more && wq.tiles() == 0) q_more = wq.next(plan);
+            while (kv_more && wk.tiles() == 0) kv_more = wk.next(plan);
+            int q_act = 0, jg = 0, kj = kv_more ? wk.j0 : 0;
+            const int pr = kPaged ? min(a.page_size, BN) : BN;  // rows per box
+            int page[C::PIECES];                                // paged: page of this lane's boxes of the next tile
+            uint32_t bytes = 2 * C::kTileKV_B;
+            auto look_up = [&]() {
+                if constexpr (kPaged) {
+                    const int n0 = (wk.t.n_first + kj) * BN;
+                    const int live = min((wk.t.S_k - n0 + pr - 1) / pr, BN / pr);  // boxes that hold a key
+                    bytes = (uint32_t)(live * pr) * 128u * 2u * C::BOXES;
+                    const int* row = a.table + (size_t)wk.t.n * a.max_pages;
+                    // keys before the window of the unit's first row may have lost their pages:
+                    // they are masked, and read as zeros (page `pages`) without a look-up
+                    const int k_lo = a.window > 0 ? wk.t.pos0 - a.window + 1 : 0;
+                    bool bad = false;
+#pragma unroll
+                    for (int i = 0; i < C::PIECES; ++i) {
+                        const int b = (lane + 32 * i) / (2 * C::BOXES), j = n0 + b * pr;
+                        page[i] = b >= live         ? -1
+                                  : j + pr <= k_lo ? a.pages
+                                                    : page_of(row, j, a.page_size, a.max_pages, a.pages, &bad);
+                    }
+                    if (bad) atomicOr(err, kErrPage);
+                }
+            };
+            if (kv_more) look_up();
+            uint64_t t0 = ptx::globaltimer();
+            uint32_t spins = 0;
+            while (q_more || kv_more) {
+                int act = 0;
+                if (lane == 0) {
+                    if (q_more && (q_act == 0 || ptx::mbar_test_wait(bar(P_QE), (q_act - 1) & 1))) act |= 1;
+                    if (kv_more && (jg < C::STAGES ||
+                                    ptx::mbar_test_wait(bar_empty(jg % C::STAGES), ((jg / C::STAGES) - 1) & 1)))
+                        act |= 2;
+                }
+                act = __shfl_sync(0xffffffffu, act, 0);
+                if (act & 1) {
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(tpt * g) * 128u * C::BOXES);
+                        for (int x = 0; x < C::BOXES; ++x)
+                            ptx::tma_load_3d(sbase + C::OFF_Q + x * C::kBoxQ_B, &tmQ, x * 64, wq.hd * g, wq.t.q_tok,
+                                             bar(P_Q));
+                    }
+                    ++q_act;
+                    do q_more = wq.next(plan);
+                    while (q_more && wq.tiles() == 0);
+                }
+                if (act & 2) {
+                    const int s = jg % C::STAGES;
+                    const int n0 = (wk.t.n_first + kj) * BN;
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full(s), bytes);
+                    __syncwarp();
+                    if constexpr (kPaged) {
+#pragma unroll
+                        for (int i = 0; i < C::PIECES; ++i) {
+                            const int e = lane + 32 * i, b = e / (2 * C::BOXES), x = (e >> 1) % C::BOXES;
+                            if (b < BN / pr && page[i] >= 0)
+                                tma_load_4d(sbase + ((e & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B +
+                                                x * C::kBoxKV_B + b * pr * 128,
+                                            (e & 1) ? &tmV : &tmK, x * 64, wk.hd, (n0 + b * pr) % a.page_size,
+                                            page[i], bar_full(s));
+                        }
+                    } else if (lane < 2 * C::BOXES) {
+                        const int x = lane >> 1;
+                        ptx::tma_load_3d(sbase + ((lane & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B +
+                                             x * C::kBoxKV_B,
+                                         (lane & 1) ? &tmV : &tmK, x * 64, wk.hd, wk.t.k_base + n0, bar_full(s));
+                    }
+                    ++jg;
+                    if (++kj == wk.j1) {
+                        do kv_more = wk.next(plan);
+                        while (kv_more && wk.tiles() == 0);
+                        kj = wk.j0;
+                    }
+                    if (kv_more) look_up();
+                }
+                int stop = 0;
+                if (lane == 0) {
+                    if (act) {
+                        t0 = ptx::globaltimer();
+                    } else if (++spins % 64 == 0) {
+                        if (*abort_flag) stop = 1;
+                        if (ptx::globaltimer() - t0 > kWaitLimitNs) {
+                            *abort_flag = 1;
+                            atomicOr(err, kErrTimeout);
+                            stop = 1;
+                        }
+                    }
+                }
+                if (__shfl_sync(0xffffffffu, stop, 0)) break;
+            }
+            // never leave copies in flight into shared memory that is about to be released
+            if (lane == 0) {
+                if (q_act > 0) drain_wait(bar(P_Q), (q_act - 1) & 1);
+                for (int j = jg - C::STAGES < 0 ? 0 : jg - C::STAGES; j < jg; ++j)
+                    drain_wait(bar_full(j % C::STAGES), (j / C::STAGES) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma || warp == kWarpPv) {
+        // ------------------------------------------------------------ MMA issuers
+        // Warp 5 issues S = Q K^T, warp 6 O += P V, so that each hides the other's waits.  S
+        // of tile jg goes into buffer jg % NB once the P V product of tile jg - NB has read P
+        // out of it; the P V product runs once the softmax has packed P.
+        if (lane == 0 && !*abort_flag) {
+            constexpr uint32_t ID_S = ptx::idesc_f16(BM, BN, kBF16, false, false);
+            constexpr uint32_t ID_PV = ptx::idesc_f16(BM, D, kBF16, false, true);
+            auto desc_add = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
+            bool ok = true;
+            int jg = 0, ka = 0;
+            FwdWalk w;
+            bool more = w.init(plan, blockIdx.x, a.H_kv);
+            if (warp == kWarpMma) {
+                const uint64_t dQ_k = ptx::sw128_desc(sbase + C::OFF_Q, 16, 1024);
+                const uint64_t dK_k = ptx::sw128_desc(sbase + C::OFF_K, 16, 1024);
+                for (; ok && more; more = w.next(plan)) {
+                    const int nt = w.tiles();
+                    if (nt == 0) continue;
+                    if (!(ok = wait_bar(bar(P_Q), ka & 1, abort_flag, err))) break;
+                    for (int j = 0; j < nt; ++j, ++jg) {
+                        const int s = jg % C::STAGES;
+                        if (!(ok = wait_bar(bar_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
+                        if (jg >= NB && !(ok = wait_bar(bar(P_PV0 + jg % NB), (jg / NB - 1) & 1, abort_flag, err)))
+                            break;
+                        ptx::tc_fence_after();
+                        const uint32_t so = (uint32_t)s * C::kTileKV_B;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t kq = (kk / 4) * C::kBoxQ_B + (kk % 4) * 32;
+                            const uint32_t kv = (kk / 4) * C::kBoxKV_B + (kk % 4) * 32;
+                            ptx::mma_ss(tmem + C::TM_S + (jg % NB) * 128, desc_add(dQ_k, kq), desc_add(dK_k, so + kv),
+                                        ID_S, kk > 0);
+                        }
+                        ptx::mma_commit(bar(P_S0 + jg % NB));
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit(bar(P_QE));
+                    ++ka;
+                }
+                // every S product is read by a P V product, so all are complete once the other
+                // issuer has drained
+            } else {
+                const uint64_t dV_mn = ptx::sw128_desc(sbase + C::OFF_V, C::kBoxKV_B, 1024);
+                for (; ok && more; more = w.next(plan)) {
+                    const int nt = w.tiles();
+                    if (nt == 0) continue;
+                    for (int j = 0; j < nt; ++j, ++jg) {
+                        const int s = jg % C::STAGES;
+                        if (!(ok = wait_bar(bar(P_P0 + jg % NB), (jg / NB) & 1, abort_flag, err))) break;
+                        // the first product of an item overwrites O: the epilogue of the
+                        // previous item must have read it
+                        if (j == 0 && ka > 0 && !(ok = wait_bar(bar(P_OFREE), (ka - 1) & 1, abort_flag, err))) break;
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            ptx::mma_ts(tmem + C::TM_O, tmem + C::TM_S + (jg % NB) * 128 + kk * 8,
+                                        desc_add(dV_mn, (uint32_t)s * C::kTileKV_B + kk * 2048), ID_PV,
+                                        (j > 0 || kk > 0) ? 1u : 0u);
+                        ptx::mma_commit(bar(P_PV0 + jg % NB));
+                        ptx::mma_commit(bar_empty(s));
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit(bar(P_OFULL));
+                    ++ka;
+                }
+                ptx::mma_commit(bar(P_FINAL));  // no MMA may still write TMEM when it is released
+                drain_wait(bar(P_FINAL), 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax + epilogue
+        const int t = warp * 32 + lane;  // TMEM lane == row of the tile
+        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        const int ti = t / g, th = t - ti * g;  // token and head of the row
+        const float scale_log2 = a.scale * 1.4426950408889634f;
+        bool ok = !*abort_flag;
+        int jg = 0, ka = 0;
+        FwdWalk w;
+        bool more = w.init(plan, blockIdx.x, a.H_kv);
+        for (; ok && more; more = w.next(plan)) {
+            const int rows = w.t.n_tok * g;
+            const bool row_valid = t < rows;
+            const bool warp_live = warp * 32 < rows;
+            const int nt = w.tiles();
+            float m_run = -INFINITY;  // running max of s * log2(e), moved lazily
+            float l_run = 0.f;        // sum of exp2(x - m_run)
+            for (int j = 0; ok && j < nt; ++j, ++jg) {
+                const uint32_t buf = tmem + C::TM_S + (jg % NB) * 128 + lane_off;
+                const int n0 = (w.t.n_first + w.j0 + j) * BN;
+                const int k_live = w.t.S_k - n0;  // keys of the sequence from this tile on
+                int c_lo, c_hi;
+                visible_keys(w.t.pos0 + ti - n0, a.causal, a.window, c_lo, c_hi);
+                c_lo = max(c_lo, 0);
+                c_hi = min(c_hi, k_live);
+                const unsigned c_span = c_hi > c_lo ? (unsigned)(c_hi - c_lo) : 0u;
+                const bool masked = __any_sync(0xffffffffu, !(c_lo <= 0 && c_hi >= BN));
+                if (!(ok = wait_bar_warp(bar(P_S0 + jg % NB), (jg / NB) & 1, abort_flag, err))) break;
+                if (k_live < BN) {
+                    // V rows behind the last key: zeros (this wait only orders the zeros after
+                    // the loads; S could not be complete before them)
+                    const int s = jg % C::STAGES;
+                    if (!(ok = wait_bar_warp(bar_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
+                    if (t < BN && t >= k_live) {
+#pragma unroll
+                        for (int x = 0; x < C::BOXES; ++x)
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::kTileKV_B + x * C::kBoxKV_B +
+                                                          t * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                ptx::tc_fence_after();
+                if (warp_live) {
+                    uint32_t r[BN];
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) ptx::tmem_ld32p(buf + c * 32, r + c * 32);
+                    ptx::tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < BN; ++c)
+                            r[c] = (unsigned)(c - c_lo) < c_span ? r[c] : __float_as_uint(-INFINITY);
+                    }
+                    float mx8[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < BN; c += 2)
+                        mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                    float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                     fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                    mx = mx == -INFINITY ? -INFINITY : mx * scale_log2;
+                    float alpha = 1.f;
+                    const bool rescale = mx > m_run + kRescaleLog2;
+                    if (rescale) {
+                        alpha = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - mx);
+                        m_run = mx;
+                    }
+                    const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                    const float2 sc2 = make_float2(scale_log2, scale_log2);
+                    const float2 nm2 = make_float2(-m_use, -m_use);
+                    float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                      make_float2(0.f, 0.f)};
+                    uint32_t Pp[BN / 2];
+#pragma unroll
+                    for (int c = 0; c < BN; c += 2) {
+                        const float2 x =
+                            __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nm2);
+                        const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                        sum2[(c >> 1) & 3] = __fadd2_rn(sum2[(c >> 1) & 3], pp);
+                        Pp[c / 2] = pack2<kBF16>(pp.x, pp.y);
+                    }
+                    const float2 s2 = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
+                    l_run = l_run * alpha + (s2.x + s2.y);
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) ptx::tmem_st32(buf + c * 32, Pp + c * 32);
+                    // rescale the O row before the next P V product accumulates into it
+                    if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+                        if (!(ok = wait_bar_warp(bar(P_PV0 + (jg - 1) % NB), ((jg - 1) / NB) & 1, abort_flag, err))) {
+                            ptx::tmem_wait_st();  // no TMEM store in flight at the release
+                            break;
+                        }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32p(tmem + C::TM_O + lane_off + c * 32, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int kk = 0; kk < 32; ++kk) o[kk] = __float_as_uint(__uint_as_float(o[kk]) * alpha);
+                            ptx::tmem_st32(tmem + C::TM_O + lane_off + c * 32, o);
+                        }
+                    }
+                    ptx::tmem_wait_st();
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(P_P0 + jg % NB));
+            }
+            if (!ok) break;
+            // ---- epilogue: O = acc / l and LSE = (m + log2 l) ln 2 of a whole item, the raw
+            // accumulator with (m, l) of a cut one
+            const bool has = nt > 0;
+            const bool whole = w.whole();
+            if (has && !(ok = wait_bar_warp(bar(P_OFULL), ka & 1, abort_flag, err))) break;
+            ptx::tc_fence_after();
+            const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+            const int tok = w.t.q_tok + ti, head = w.hd * g + th;
+            const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
+            if (warp_live) {
+                T* Orow = static_cast<T*>(a.O) + (long long)tok * a.o.tok + (long long)head * a.o.head;
+                float* Prow = plan.part_o + ((size_t)slot * BM + t) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (has) {
+                        ptx::tmem_ld32p(tmem + C::TM_O + lane_off + c * 32, o);
+                        ptx::tmem_wait_ld();
+                        if (c == D / 32 - 1) {  // O read: the next item may overwrite it
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bar(P_OFREE));
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 32; ++kk) o[kk] = 0u;
+                    }
+                    if (row_valid && whole) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t w4[4];
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                w4[kk] = pack2<kBF16>(__uint_as_float(o[u * 8 + 2 * kk]) * inv_l,
+                                                      __uint_as_float(o[u * 8 + 2 * kk + 1]) * inv_l);
+                            if (c * 32 + u * 8 < a.d)
+                                *reinterpret_cast<uint4*>(Orow + c * 32 + u * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                        }
+                    } else if (row_valid) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            *reinterpret_cast<uint4*>(Prow + c * 32 + u * 4) =
+                                make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (row_valid) {
+                    if (whole)
+                        a.LSE[(size_t)head * a.T_q + tok] =
+                            l_run > 0.f ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+                    else
+                        plan.part_ml[(size_t)slot * BM + t] = make_float2(m_run, l_run);
+                }
+            } else if (has && lane == 0) {
+                ptx::mbar_arrive(bar(P_OFREE));
+            }
+            if (!whole) {
+                // the last part to arrive joins the item
+                int first, count;
+                w.parts(first, count);
+                __threadfence();
+                ptx::named_bar_sync(kSoftBarrier, 128);
+                if (t == 0) *last_flag = atomicAdd(&plan.done[first], 1u) == (unsigned)(count - 1);
+                ptx::named_bar_sync(kSoftBarrier, 128);
+                if (*last_flag) {
+                    __threadfence();
+                    join_parts<T>(a, plan, w.t, w.hd * g, g, rows, BM, D, first, count, t, 128);
+                }
+            }
+            if (has) ++ka;
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kWarpMma) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- host side
+bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+    TmaEncodeTiledFn enc = tma_encode_fn();
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    return enc && enc(m, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms > 0 ? sms : 148;
+}
+
+template <typename T, int D, bool kPaged>
+cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+    using C = PCfg<D>;
+    constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16;
+    static_assert(kSmem <= 232448, "shared memory budget");
+    const int g = a.H / a.H_kv;
+    FwdGeom geo;
+    geo.rows = BM;
+    geo.tpt = BM / g;
+    geo.bn = C::BN;
+    geo.heads = a.H_kv;
+    geo.ctas = sm_count();
+    geo.D = D;
+    geo.min_chunk = 2;
+    FwdPlan plan;
+    *bytes = fwd_plan_layout(a, geo, ws, &plan);
+    if (ws == nullptr) return cudaSuccess;
+    const CUtensorMapDataType dt =
+        TypeTraits<T>::kId == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tq, tk, tv;
+    bool ok;
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.T_q};
+        const cuuint64_t str[2] = {(cuuint64_t)a.q.head * 2, (cuuint64_t)a.q.tok * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)geo.tpt};
+        ok = encode(&tq, a.Q, dt, 3, dims, str, box);
+    }
+    const struct {
+        CUtensorMap* m;
+        const void* p;
+        RowStride s;
+        long long page;
+    } kv[2] = {{&tk, a.K, a.k, a.k_page}, {&tv, a.V, a.v, a.v_page}};
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (kPaged) {
+            const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.H_kv, (cuuint64_t)a.page_size,
+                                        (cuuint64_t)a.pages};
+            const cuuint64_t str[3] = {(cuuint64_t)kv[i].s.head * 2, (cuuint64_t)kv[i].s.tok * 2,
+                                       (cuuint64_t)kv[i].page * 2};
+            const cuuint32_t box[4] = {64, 1, (cuuint32_t)(a.page_size < C::BN ? a.page_size : C::BN), 1};
+            ok = ok && encode(kv[i].m, kv[i].p, dt, 4, dims, str, box);
+        } else {
+            const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H_kv, (cuuint64_t)(a.T_k > 0 ? a.T_k : 1)};
+            const cuuint64_t str[2] = {(cuuint64_t)kv[i].s.head * 2, (cuuint64_t)kv[i].s.tok * 2};
+            const cuuint32_t box[3] = {64, 1, (cuuint32_t)C::BN};
+            ok = ok && encode(kv[i].m, a.T_k > 0 ? kv[i].p : a.Q, dt, 3, dims, str, box);
+        }
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    cudaError_t e = launch_fwd_plan(a, geo, plan, st);
+    if (e != cudaSuccess) return e;
+    auto kern = packed_fwd_kernel<T, D, kPaged>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    // programmatic dependent launch: barriers and TMEM are set up while the plan is made
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)geo.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, plan, geo.tpt);
+}
+
+template <typename T>
+cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+    const int D = a.d == 256 ? 256 : tc_head_dim(a.d);
+    if (a.paged()) {
+        if (D == 64) return launch_t<T, 64, true>(a, ws, bytes, st);
+        if (D == 128) return launch_t<T, 128, true>(a, ws, bytes, st);
+        if (D == 256) return launch_t<T, 256, true>(a, ws, bytes, st);
+    } else {
+        if (D == 64) return launch_t<T, 64, false>(a, ws, bytes, st);
+        if (D == 128) return launch_t<T, 128, false>(a, ws, bytes, st);
+        if (D == 256) return launch_t<T, 256, false>(a, ws, bytes, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+    return a.dtype == FA_F16 ? launch_d<__half>(a, ws, bytes, st) : launch_d<__nv_bfloat16>(a, ws, bytes, st);
+}
+
+}  // namespace fa

@@ -190,10 +190,116 @@ int fa_bwd_noalloc(const void* dO, const void* Q, const void* K, const void* V, 
  * copies, the fp32 dQ accumulator and the deterministic mode's turn counters. */
 size_t fa_bwd_workspace_bytes(int B, int H, int S_q, int d);
 
+/*
+ * ---- Packed sequences and paged caches -----------------------------------
+ *
+ * Packed tensors hold N sequences of different lengths one after another, token
+ * major: Q, O [T_q, H, d], K, V [T_k, H_kv, d]; sequence n owns query rows
+ * [cu_q[n], cu_q[n+1]) and key rows [cu_k[n], cu_k[n+1]) (int32 device arrays
+ * of N + 1 non-decreasing entries).  LSE is [H, T_q] float32.  Attention runs
+ * inside each sequence, with the alignment, causal mask and window of fa_fwd_ex
+ * for that sequence's S_q and S_k.  Sequences may be empty on either side: a
+ * query that sees no key gets O = 0 and LSE = -inf.  The pages have no
+ * counterpart of these entry points.
+ *
+ *   strides    : element strides in host memory, or NULL for dense tensors; the
+ *                head dimension itself is contiguous.  Every stride is > 0 and a
+ *                multiple of 16 bytes, every tensor 16-byte aligned, so the
+ *                slices of a joint QKV projection can be passed as they are.
+ *   fill       : rows of no sequence (before cu_q[0], from cu_q[N] on) are
+ *                0 = left as they were, 1 = set to O = 0 and LSE = -inf.
+ *   workspace  : caller's scratch, 256-byte aligned, of at least the bytes that
+ *                the matching *_workspace_bytes function gives.  It needs no
+ *                initialisation and must not be shared by calls whose GPU work
+ *                may overlap (graphs replayed side by side included).
+ * All lengths are read on the device: no call synchronizes, and a captured call
+ * replays with whatever lengths the arrays hold then.  Lengths that do not fit
+ * the tensors (decreasing, negative, past T_q / T_k or the table) make the call
+ * compute nothing; fa_check_device then reports FA_ERR_INVALID_ARG.
+ */
+
+/*
+ * fa_varlen_fwd -- attention forward over packed sequences.
+ *   strides : {Q token, Q head, K token, K head, V token, V head, O token, O head}
+ * F16/BF16 run a tcgen05 kernel (H / H_kv <= 128), F32 and wider head groups an
+ * FFMA kernel.  The result is bitwise reproducible.
+ */
+int fa_varlen_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,
+                  const int* cu_k, int N, int T_q, int T_k, int H, int H_kv, int d,
+                  const long long* strides, float scale, int causal, int window_size, int fill,
+                  int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_varlen_fwd (backward = 0) or fa_varlen_bwd (backward = 1);
+ * 0 for arguments those calls refuse. */
+size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d, int dtype,
+                                 int backward);
+
+/*
+ * fa_paged_fwd -- attention of each request's newest tokens over its pages of a
+ * key/value cache (one token per request is a decode step, many a chunk of its
+ * prompt; both kinds may share a call).
+ *   K_cache, V_cache : [num_pages, page_size, H_kv, d], holding the new tokens too
+ *   block_table      : [N, max_pages] int32 page numbers; entries behind a
+ *                      request's last page are not read
+ *   cu_q             : [N + 1] int32, the new tokens of request n are rows
+ *                      [cu_q[n], cu_q[n+1]) of Q
+ *   seq_lens         : [N] int32 tokens in the cache, the new ones included;
+ *                      query i sits at position seq_lens[n] - S_q + i
+ *   strides          : {Q token, Q head, K page, K row, K head, V page, V row,
+ *                      V head, O token, O head}
+ * F16/BF16 caches whose page_size is a multiple of 8 that divides 128 or is a
+ * multiple of 128 (64 at d = 256) run the tcgen05 kernel, others an FFMA kernel.
+ * A table entry outside the cache reads as zeros and is reported by
+ * fa_check_device (FA_ERR_INVALID_ARG).  With a window, pages that lie wholly
+ * before it need not be valid any more.  The result is bitwise reproducible.
+ */
+int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* O, float* LSE,
+                 const int* block_table, const int* cu_q, const int* seq_lens, int N, int T_q,
+                 int num_pages, int page_size, int max_pages, int H, int H_kv, int d,
+                 const long long* strides, float scale, int causal, int window_size, int fill,
+                 int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_paged_fwd; 0 for arguments it refuses. */
+size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype);
+
+/*
+ * fa_page_slots -- pages and slots of a step's new tokens, on the device.
+ *   ctx_lens    : [N] int32 tokens each request holds already
+ *   cu_q        : [N + 1] int32 new tokens, as in fa_paged_fwd
+ *   free_pages  : [num_free] int32 numbers of unused pages, taken from
+ *                 free_start[0] on, in request order
+ *   block_table : [N, max_pages] int32, in: the pages held; out: the new pages
+ *                 behind them (other entries are left alone)
+ *   slots       : [T] int64 out, page * page_size + row of each token; -1 for
+ *                 rows of no request
+ *   positions   : [T] int32 out, position of each token in its request, or -1
+ *   seq_lens    : [N] int32 out, ctx_lens plus the new tokens
+ *   free_next   : [1] int32 out, free_start[0] plus the pages taken
+ * When the free list or the table has no room, the entries and slots concerned
+ * are -1 and fa_check_device reports FA_ERR_INVALID_ARG.  The call changes
+ * neither free_pages nor free_start, so running it again gives the same result.
+ */
+int fa_page_slots(const int* ctx_lens, const int* cu_q, const int* free_pages, const int* free_start,
+                  int* block_table, long long* slots, int* positions, int* seq_lens, int* free_next,
+                  int N, int T, int num_free, int page_size, int max_pages, void* stream);
+
+/*
+ * fa_paged_write -- K and V rows [T, H_kv, d] of new tokens to their slots of the
+ * cache.  A negative slot is skipped; one past the cache is skipped and reported
+ * by fa_check_device (FA_ERR_INVALID_ARG).  Slots must differ: of two rows with
+ * the same slot either may be kept.
+ *   strides : {K token, K head, V token, V head, K page, K row, K head of the
+ *             cache, V page, V row, V head of the cache}
+ */
+int fa_paged_write(const void* K, const void* V, const long long* slots, void* K_cache, void* V_cache,
+                   int T, int num_pages, int page_size, int H_kv, int d, const long long* strides,
+                   int dtype, void* stream);
+
 /* Synchronizes `stream`, then returns FA_ERR_TIMEOUT if a kernel of this
  * library on that stream, or an fa_bwd_noalloc call on this device, recorded
  * a bounded-wait timeout since the last check (clearing the record), else
- * FA_OK (or FA_ERR_CUDA). */
+ * FA_ERR_INVALID_ARG if a packed or paged call on this device was given lengths,
+ * pages or slots that do not fit, else FA_OK (or FA_ERR_CUDA). */
 int fa_check_device(void* stream);
 
 /*
