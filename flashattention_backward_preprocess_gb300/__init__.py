@@ -1,5 +1,6 @@
 """GB300 (sm_103a) FlashAttention-2 backward: preprocess D = rowsum(dO * O),
-then dQ, dK, dV from a tcgen05 tensor-core kernel.
+then dQ, dK, dV from a tcgen05 tensor-core kernel; the same over packed sequences of
+different lengths, and the forward over paged key/value caches (``packed``).
 
 The compute lives in the C-ABI library ``_build/libfa.so`` (include/fa.h);
 this package is the thin Python binding over it (argument marshalling only,
@@ -30,10 +31,16 @@ from .binding import (  # noqa: F401
     library_path,
     load_library,
 )
-from .autograd import FlashAttentionFunction, flash_attention  # noqa: F401
+from .autograd import (  # noqa: F401
+    FlashAttentionFunction,
+    FlashAttentionVarlenFunction,
+    flash_attention,
+    flash_attention_varlen,
+)
 from .packed import (  # noqa: F401
     fa_page_slots,
     fa_paged_fwd,
     fa_paged_write,
+    fa_varlen_bwd,
     fa_varlen_fwd,
 )

@@ -31,7 +31,7 @@ EXPORTS = ("fa_bwd", "fa_bwd_ex", "fa_bwd_noalloc", "fa_bwd_preprocess", "fa_fwd
            "fa_bwd_workspace_bytes",
            "fa_check_device", "fa_profile", "fa_profile_read", "fa_selftest_timeout",
            "fa_last_error", "fa_shutdown", "fa_version",
-           "fa_varlen_fwd", "fa_varlen_workspace_bytes", "fa_paged_fwd", "fa_paged_workspace_bytes",
+           "fa_varlen_fwd", "fa_varlen_bwd", "fa_varlen_workspace_bytes", "fa_paged_fwd", "fa_paged_workspace_bytes",
            "fa_page_slots", "fa_paged_write")
 
 
@@ -84,6 +84,8 @@ def load_library(path: str | None = None):
         Z = ctypes.c_size_t
         lib.fa_varlen_fwd.argtypes = [V] * 7 + [I] * 6 + [V, F, I, I, I, I, V, Z, V]
         lib.fa_varlen_fwd.restype = I
+        lib.fa_varlen_bwd.argtypes = [V] * 11 + [I] * 6 + [V, F, I, I, I, I, I, V, Z, V]
+        lib.fa_varlen_bwd.restype = I
         lib.fa_varlen_workspace_bytes.argtypes = [I] * 8
         lib.fa_varlen_workspace_bytes.restype = Z
         lib.fa_paged_fwd.argtypes = [V] * 8 + [I] * 8 + [V, F, I, I, I, I, V, Z, V]

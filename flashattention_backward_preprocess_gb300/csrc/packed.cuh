@@ -206,6 +206,96 @@ cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaS
 // packed_simt.cu: CUDA cores (f32, and layouts that TMA cannot address)
 cudaError_t launch_packed_fwd_simt(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 
+// ---------------------------------------------------------------- backward
+struct PackedBwd {
+    const void *dO, *Q, *K, *V, *O;
+    const float* LSE;  // [H, T_q]
+    void *dQ, *dK, *dV;
+    const int *cu_q, *cu_k;
+    int N, T_q, T_k, H, H_kv, d;
+    RowStride sdo, sq, sk, sv, so, sdq, sdk, sdv;
+    float scale;
+    int causal, window, deterministic, fill, dtype;
+    unsigned int* err;
+};
+
+constexpr int kBwdTile = 128;  // query rows and key rows of a plan tile
+
+// A 128-row query tile: rows q_tok .. q_tok + rows - 1 of Q; its place in the list is its place
+// in the padded rows of the accumulator, D and the LSE copy.
+struct QueryTile {
+    int q_tok, rows;
+};
+// A 128-row key tile of a sequence.
+struct alignas(16) KeyTile {
+    int n;      // sequence
+    int k_tok;  // first key row of the tile (row of K)
+    int n0;     // the same within the sequence
+    int S_q, S_k;
+    int unit0;  // first query tile of the sequence
+    int its;    // query tiles that see a key of this tile
+    int pad;
+};
+
+struct BwdPlan {
+    long long* head;      // [0] query tiles, [1] key tiles
+    QueryTile* query;     // [max_units]
+    KeyTile* key;         // [max_keys], in sequence order
+    int* order;           // [max_keys] key tiles, most query tiles first
+    int *seq_q, *seq_k;   // [N + 1] first query / key tile of each sequence
+    CUtensorMap* maps;    // [N][4] of each sequence: Q, dO, K, V (tensor-core kernel)
+    unsigned *sem, *ticket;  // deterministic: turn counters [H][max_units], start-order ticket
+    float *lse2, *D;      // [H][rows]
+    float* dqacc;         // [rows][H][d] fp32, not scaled
+    long long rows;       // max_units * 128
+    int max_units, max_keys;
+};
+
+inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, BwdPlan* p) {
+    char* b = static_cast<char*>(ws);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* r = b + at;
+        at = packed_align(at + bytes);
+        return r;
+    };
+    BwdPlan q;
+    q.max_units = a.T_q / kBwdTile + (a.N < a.T_q ? a.N : a.T_q);
+    q.max_keys = a.T_k / kBwdTile + (a.N < a.T_k ? a.N : a.T_k);
+    q.rows = (long long)q.max_units * kBwdTile;
+    q.head = reinterpret_cast<long long*>(take(16));
+    q.ticket = reinterpret_cast<unsigned*>(take(4));
+    q.sem = reinterpret_cast<unsigned*>(take(a.deterministic ? (size_t)a.H * q.max_units * 4 : 0));
+    q.query = reinterpret_cast<QueryTile*>(take((size_t)q.max_units * sizeof(QueryTile)));
+    q.key = reinterpret_cast<KeyTile*>(take((size_t)q.max_keys * sizeof(KeyTile)));
+    q.order = reinterpret_cast<int*>(take((size_t)q.max_keys * 4));
+    q.seq_q = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
+    q.seq_k = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
+    q.maps = reinterpret_cast<CUtensorMap*>(take(tensor_cores ? (size_t)a.N * 4 * sizeof(CUtensorMap) : 0));
+    q.lse2 = reinterpret_cast<float*>(take((size_t)q.rows * a.H * 4));
+    q.D = reinterpret_cast<float*>(take((size_t)q.rows * a.H * 4));
+    q.dqacc = reinterpret_cast<float*>(take((size_t)q.rows * a.H * a.d * 4));
+    if (p) *p = q;
+    return at;
+}
+
+// packed_plan.cu: tiles, order, maps, counters; with a.fill the gradient rows of no sequence
+cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_cores, cudaStream_t st);
+// packed_simt.cu: D, the LSE copy and a zeroed accumulator; dQ from the accumulator
+cudaError_t launch_packed_preprocess(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
+cudaError_t launch_packed_dq(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
+// packed_bwd.cu (f16 / bf16, head dim <= 128) and packed_bwd_simt.cu (f32, head dim 256)
+cudaError_t launch_packed_bwd(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
+cudaError_t launch_packed_bwd_simt(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
+
+// Map of the fp32 accumulator [rows][H][d]: boxes of 32 columns, one head, 128 rows.
+bool bwd_acc_map(CUtensorMap* m, const PackedBwd& a, const BwdPlan& p);
+
+// Orders this thread's later uses of a tensor map after its writes (by an earlier kernel).
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // packed_api.cu: reads the error word of the packed and paged calls on the current device into
 // *word and clears it.  Returns an fa_status.
 int packed_take_error_word(unsigned int* word);

@@ -36,6 +36,9 @@ int err_word(unsigned int** out) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_bad("cudaGetDevice", e);
     if (dev < 0 || dev >= kMaxDevices) return set_error(FA_ERR_UNSUPPORTED, "device", "device index too large");
+    // a thread's first call (an autograd worker's, say) makes tensor maps before it launches
+    // anything: the driver refuses that until the device's context is current in the thread
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) return cuda_bad("cudaSetDevice", e);
     std::lock_guard<std::mutex> lk(g_mu);
     if (g_err_ptr[dev] == nullptr) {
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
@@ -102,6 +105,8 @@ bool use_tensor_cores(const PackedFwd& a) {
     return a.page_size % 8 == 0 && (bn % a.page_size == 0 || a.page_size % bn == 0);
 }
 
+bool bwd_tensor_cores(const PackedBwd& a) { return a.dtype != FA_F32 && tc_head_dim(a.d) != 0; }
+
 size_t fwd_bytes(const PackedFwd& a) {
     size_t n = 0;
     if (use_tensor_cores(a))
@@ -152,7 +157,11 @@ extern "C" {
 
 size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d, int dtype, int backward) {
     if (check_common(N, H, H_kv, d, 1.f, 0, 0, 0, dtype) != FA_OK || T_q < 0 || T_k < 0) return 0;
-    (void)backward;
+    if (backward) {
+        PackedBwd b = {};
+        b.N = N, b.T_q = T_q, b.T_k = T_k, b.H = H, b.H_kv = H_kv, b.d = d, b.dtype = dtype, b.deterministic = 1;
+        return bwd_plan_layout(b, bwd_tensor_cores(b), nullptr, nullptr);
+    }
     PackedFwd a = {};
     static const int some = 0;
     a.cu_k = &some;  // packed
@@ -187,6 +196,55 @@ int fa_varlen_fwd(const void* Q, const void* K, const void* V, void* O, float* L
     a.q = {s[0], s[1]}, a.k = {s[2], s[3]}, a.v = {s[4], s[5]}, a.o = {s[6], s[7]};
     a.scale = scale, a.causal = causal, a.window = window_size, a.fill = fill, a.dtype = dtype;
     return run_fwd(a, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, const void* O, const float* LSE, void* dQ,
+                  void* dK, void* dV, const int* cu_q, const int* cu_k, int N, int T_q, int T_k, int H, int H_kv, int d,
+                  const long long* strides, float scale, int causal, int window_size, int deterministic, int fill,
+                  int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    clear_error();
+    int rc;
+    if ((rc = check_common(N, H, H_kv, d, scale, causal, window_size, fill, dtype))) return rc;
+    if (deterministic != 0 && deterministic != 1) return bad("deterministic", "must be 0 or 1");
+    if ((rc = check_count("T_q", T_q, 0, kMaxTokens)) || (rc = check_count("T_k", T_k, 0, kMaxTokens))) return rc;
+    if ((rc = check_ptr(cu_q, "cu_q", 4)) || (rc = check_ptr(cu_k, "cu_k", 4))) return rc;
+    if (T_q == 0 && T_k == 0) return FA_OK;
+    if (T_q > 0 && ((rc = check_ptr(dO, "dO", 16)) || (rc = check_ptr(Q, "Q", 16)) || (rc = check_ptr(O, "O", 16)) ||
+                    (rc = check_ptr(LSE, "LSE", 4)) || (rc = check_ptr(dQ, "dQ", 16))))
+        return rc;
+    if (T_k > 0 && ((rc = check_ptr(K, "K", 16)) || (rc = check_ptr(V, "V", 16)) || (rc = check_ptr(dK, "dK", 16)) ||
+                    (rc = check_ptr(dV, "dV", 16))))
+        return rc;
+    const long long qr = (long long)H * d, kr = (long long)H_kv * d;
+    const long long dense[16] = {qr, d, qr, d, kr, d, kr, d, qr, d, qr, d, kr, d, kr, d};
+    const long long* s = strides ? strides : dense;
+    if ((rc = check_strides(s, 16, dtype))) return rc;
+    PackedBwd a = {};
+    a.dO = dO, a.Q = Q, a.K = K, a.V = V, a.O = O, a.LSE = LSE, a.dQ = dQ, a.dK = dK, a.dV = dV;
+    a.cu_q = cu_q, a.cu_k = cu_k, a.N = N, a.T_q = T_q, a.T_k = T_k, a.H = H, a.H_kv = H_kv, a.d = d;
+    a.sdo = {s[0], s[1]}, a.sq = {s[2], s[3]}, a.sk = {s[4], s[5]}, a.sv = {s[6], s[7]}, a.so = {s[8], s[9]};
+    a.sdq = {s[10], s[11]}, a.sdk = {s[12], s[13]}, a.sdv = {s[14], s[15]};
+    a.scale = scale, a.causal = causal, a.window = window_size > kOpen ? kOpen : window_size;
+    a.deterministic = deterministic, a.fill = fill, a.dtype = dtype;
+    if ((rc = err_word(&a.err))) return rc;
+    const bool tc = bwd_tensor_cores(a);
+    BwdPlan p;
+    const size_t need = bwd_plan_layout(a, tc, workspace, &p);
+    if (workspace == nullptr || workspace_bytes < need)
+        return bad("workspace", "needs " + std::to_string(need) + " bytes, got " +
+                                    std::to_string(workspace ? workspace_bytes : 0));
+    if ((rc = check_ptr(workspace, "workspace", 256))) return rc;
+    // the largest grid is one CTA per 16 rows of a query tile or per piece of a key tile and head
+    if ((double)p.max_units * 8 > 2.0e9 || (double)p.max_keys * H_kv * 4 > 2.0e9 || H > 65535)
+        return bad("shape", "tensor too large");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_bwd_plan(a, p, tc, st);
+    if (e != cudaSuccess) return cuda_bad("plan launch", e);
+    if ((e = launch_packed_preprocess(a, p, st)) != cudaSuccess) return cuda_bad("preprocess launch", e);
+    e = tc ? launch_packed_bwd(a, p, st) : launch_packed_bwd_simt(a, p, st);
+    if (e != cudaSuccess) return cuda_bad("main kernel launch", e);
+    if ((e = launch_packed_dq(a, p, st)) != cudaSuccess) return cuda_bad("dq launch", e);
+    return FA_OK;
 }
 
 int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* O, float* LSE, const int* block_table,

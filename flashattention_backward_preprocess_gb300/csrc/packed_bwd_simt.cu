@@ -1,0 +1,531 @@
+// packed_bwd_simt.cu -- the passes around the packed backward's main kernel, and that kernel
+// on CUDA cores (fp32 inputs; head dim 256).
+//
+// Preprocess, per query row and head: D = sum_c dO_c O_c (fp32), LSE * log2 e into rows padded
+// to whole query tiles (+inf on padding rows and rows without keys, so their P is 0), and the
+// row of the fp32 dQ accumulator set to zero.  dQ: scale times the accumulator, rounded once.
+// Both read and write each byte once and are bound by DRAM.
+//
+// Main kernel (the mathematics of bwd_simt.cu): one CTA owns BN key rows of one (sequence, kv
+// head), dK and dV in registers, and walks BM-row query tiles of every query head of the group;
+// every product is a register-tiled block product from shared memory in fp32.  Bound by the
+// FMA pipe and its shared-memory operands.
+#include <math.h>
+
+#include "packed.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+
+constexpr int lanes_per_row(int chunks) {
+    int l = 1;
+    while (l < chunks && l < 32) l *= 2;
+    return l;
+}
+
+constexpr int kRowsPerBlock = 16;  // tile rows of one block; its rows are kRowsPerBlock x H
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_preprocess_kernel(const PackedBwd a, const BwdPlan p) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    constexpr int VEC = 16 / sizeof(T);
+    constexpr int CPR = D / VEC;
+    constexpr int LPR = lanes_per_row(CPR);
+    const int u = blockIdx.x / (kBwdTile / kRowsPerBlock);
+    if (u >= p.head[0]) return;
+    const int r0 = (blockIdx.x % (kBwdTile / kRowsPerBlock)) * kRowsPerBlock;
+    const QueryTile t = p.query[u];
+    const int lane = threadIdx.x % LPR;
+    const int total = kRowsPerBlock * a.H;
+    // whole groups of LPR lanes stay together: total rows are walked in steps of the block's groups
+    for (int e0 = 0; e0 < total; e0 += kThreads / LPR) {
+        const int e = e0 + threadIdx.x / LPR;
+        const int r = r0 + e / a.H, h = e % a.H;
+        const bool in = e < total;
+        const bool valid = in && r < t.rows;
+        float acc = 0.f;
+        if (valid) {
+            const T* dO = static_cast<const T*>(a.dO) + (long long)(t.q_tok + r) * a.sdo.tok + (long long)h * a.sdo.head;
+            const T* O = static_cast<const T*>(a.O) + (long long)(t.q_tok + r) * a.so.tok + (long long)h * a.so.head;
+            float* z = p.dqacc + (((long long)u * kBwdTile + r) * a.H + h) * D;
+#pragma unroll
+            for (int ch = lane; ch < CPR; ch += LPR) {
+                const int4 x = __ldcs(reinterpret_cast<const int4*>(dO) + ch);
+                const int4 y = __ldcs(reinterpret_cast<const int4*>(O) + ch);
+                const T* tx = reinterpret_cast<const T*>(&x);
+                const T* ty = reinterpret_cast<const T*>(&y);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    acc = fmaf(TypeTraits<T>::to_f32(tx[k]), TypeTraits<T>::to_f32(ty[k]), acc);
+#pragma unroll
+                for (int k = 0; k < VEC / 4; ++k)
+                    reinterpret_cast<float4*>(z)[ch * (VEC / 4) + k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o, LPR);
+        if (in && lane == 0) {
+            const long long row = h * p.rows + (long long)u * kBwdTile + r;
+            const float l = valid ? a.LSE[(size_t)h * a.T_q + t.q_tok + r] : -INFINITY;
+            p.D[row] = acc;
+            p.lse2[row] = (l == -INFINITY || isnan(l)) ? INFINITY : l * 1.4426950408889634f;
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedBwd a, const BwdPlan p) {
+    ptx::griddep_wait();
+    constexpr int C8 = D / 8;  // 8-column groups per row
+    const int u = blockIdx.x / (kBwdTile / kRowsPerBlock);
+    if (u >= p.head[0]) return;
+    const int r0 = (blockIdx.x % (kBwdTile / kRowsPerBlock)) * kRowsPerBlock;
+    const QueryTile t = p.query[u];
+    const int rows = min(kRowsPerBlock, t.rows - r0);
+    for (int e = threadIdx.x; e < rows * a.H * C8; e += kThreads) {
+        const int c = e % C8, rh = e / C8;
+        const int r = r0 + rh / a.H, h = rh % a.H;
+        const float4* s = reinterpret_cast<const float4*>(p.dqacc + (((long long)u * kBwdTile + r) * a.H + h) * D) + 2 * c;
+        const float4 x = __ldcs(s), y = __ldcs(s + 1);
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        T* dst = static_cast<T*>(a.dQ) + (long long)(t.q_tok + r) * a.sdq.tok + (long long)h * a.sdq.head + 8 * c;
+        if constexpr (sizeof(T) == 4) {
+            float4* o = reinterpret_cast<float4*>(dst);
+            o[0] = make_float4(v[0] * a.scale, v[1] * a.scale, v[2] * a.scale, v[3] * a.scale);
+            o[1] = make_float4(v[4] * a.scale, v[5] * a.scale, v[6] * a.scale, v[7] * a.scale);
+        } else {
+            alignas(16) T o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = TypeTraits<T>::from_f32(v[k] * a.scale);
+            __stcs(reinterpret_cast<int4*>(dst), *reinterpret_cast<const int4*>(o));
+        }
+    }
+}
+
+template <int D>
+struct SCfg {
+    static constexpr int BN = D <= 128 ? 64 : 32;  // key rows per CTA (shared memory at d = 256)
+    static constexpr int BM = BN;
+    static constexpr int LD = D + 4;
+    static constexpr int LP = BN + 4;
+    static constexpr int TR = BM / 16;
+    static constexpr int TC = BN / 16;
+    static constexpr int NG = (D / 4 + 15) / 16;
+    static constexpr size_t SMEM = sizeof(float) * ((size_t)(2 * BN + 2 * BM) * LD + 2 * BM * LP + 2 * BM);
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float4*>(p);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const T* t = reinterpret_cast<const T*>(&u);
+        return make_float4(TypeTraits<T>::to_f32(t[0]), TypeTraits<T>::to_f32(t[1]), TypeTraits<T>::to_f32(t[2]),
+                           TypeTraits<T>::to_f32(t[3]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float x, float y, float z, float w) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+    } else {
+        alignas(8) T t[4] = {TypeTraits<T>::from_f32(x), TypeTraits<T>::from_f32(y), TypeTraits<T>::from_f32(z),
+                             TypeTraits<T>::from_f32(w)};
+        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
+    }
+}
+
+// rows [0, n) of a tile (row stride `ld` elements) into a padded fp32 shared tile; zeros behind
+template <typename T, int D>
+__device__ __forceinline__ void stage_rows(float* dst, const T* src, long long ld, int n, int rows) {
+    constexpr int LD = D + 4;
+    for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c4 = e % (D / 4);
+        const float4 v = r < n ? load4(src + r * ld + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + r * LD + 4 * c4) = v;
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedBwd a, const BwdPlan p) {
+    using C = SCfg<D>;
+    constexpr int BN = C::BN, BM = C::BM, LD = C::LD, LP = C::LP, TR = C::TR, TC = C::TC, NG = C::NG;
+    constexpr int kPieces = kBwdTile / BN;  // CTAs per plan tile and head
+    extern __shared__ float4 smem4[];
+    float* smem = reinterpret_cast<float*>(smem4);
+    float* sK = smem;
+    float* sV = sK + BN * LD;
+    float* sQ = sV + BN * LD;
+    float* sdO = sQ + BM * LD;
+    float* sP = sdO + BM * LD;
+    float* sdS = sP + BM * LP;
+    float* sL = sdS + BM * LP;
+    float* sDd = sL + BM;
+    ptx::griddep_wait();
+
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int item = blockIdx.x / kPieces;
+    if (item / a.H_kv >= p.head[1]) return;
+    const KeyTile kt = p.key[p.order[item / a.H_kv]];
+    const int hk = item % a.H_kv, g = a.H / a.H_kv;
+    const int sub = (blockIdx.x % kPieces) * BN;  // this CTA's rows within the plan tile
+    const int n0 = kt.n0 + sub, S_q = kt.S_q, S_k = kt.S_k;
+    if (n0 >= S_k) return;
+    const int off = S_k - S_q;
+    const float sc2 = a.scale * 1.4426950408889634f;
+    const int krows = min(BN, S_k - n0);
+    stage_rows<T, D>(sK, static_cast<const T*>(a.K) + (long long)(kt.k_tok + sub) * a.sk.tok + (long long)hk * a.sk.head,
+                     a.sk.tok, krows, BN);
+    stage_rows<T, D>(sV, static_cast<const T*>(a.V) + (long long)(kt.k_tok + sub) * a.sv.tok + (long long)hk * a.sv.head,
+                     a.sv.tok, krows, BN);
+
+    float accV[TC][NG][4], accK[TC][NG][4];
+#pragma unroll
+    for (int r = 0; r < TC; ++r)
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) accV[r][q][u] = accK[r][q][u] = 0.f;
+
+    Shape sh;
+    sh.S_q = S_q;
+    sh.S_k = S_k;
+    sh.causal = a.causal;
+    sh.window = a.window;
+    int i_begin, i_end;
+    query_range(sh, n0, min(n0 + BN, S_k), i_begin, i_end);
+    const int m_first = i_begin / BM * BM;
+    const int nq = i_end > i_begin ? (i_end - m_first + BM - 1) / BM : 0;
+    const long long q_tok0 = nq > 0 ? p.query[kt.unit0].q_tok : 0;  // first query row of the sequence
+    const long long row0 = (long long)kt.unit0 * kBwdTile;          // and in the padded rows
+    for (int it = 0; it < g * nq; ++it) {
+        const int h = hk * g + it / nq;
+        const int m0 = m_first + (it % nq) * BM;
+        const int rows = min(BM, S_q - m0);
+        __syncthreads();  // the previous step's reads are done
+        stage_rows<T, D>(sQ, static_cast<const T*>(a.Q) + (q_tok0 + m0) * a.sq.tok + (long long)h * a.sq.head, a.sq.tok,
+                         rows, BM);
+        stage_rows<T, D>(sdO, static_cast<const T*>(a.dO) + (q_tok0 + m0) * a.sdo.tok + (long long)h * a.sdo.head,
+                         a.sdo.tok, rows, BM);
+        for (int r = tid; r < BM; r += kThreads) {
+            sL[r] = p.lse2[h * p.rows + row0 + m0 + r];  // +inf on padding rows: P = 0
+            sDd[r] = p.D[h * p.rows + row0 + m0 + r];
+        }
+        __syncthreads();
+        // ---- S and dP blocks (rows ty + 16r, keys tx + 16c), 4 head-dim columns a step
+        float accS[TR][TC], accP[TR][TC];
+#pragma unroll
+        for (int r = 0; r < TR; ++r)
+#pragma unroll
+            for (int c = 0; c < TC; ++c) accS[r][c] = accP[r][c] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) {
+            float4 q[TR], o[TR], kk[TC], v[TC];
+#pragma unroll
+            for (int r = 0; r < TR; ++r) {
+                q[r] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * r) * LD + k);
+                o[r] = *reinterpret_cast<const float4*>(sdO + (ty + 16 * r) * LD + k);
+            }
+#pragma unroll
+            for (int c = 0; c < TC; ++c) {
+                kk[c] = *reinterpret_cast<const float4*>(sK + (tx + 16 * c) * LD + k);
+                v[c] = *reinterpret_cast<const float4*>(sV + (tx + 16 * c) * LD + k);
+            }
+#pragma unroll
+            for (int r = 0; r < TR; ++r)
+#pragma unroll
+                for (int c = 0; c < TC; ++c) {
+                    accS[r][c] = fmaf(q[r].x, kk[c].x, accS[r][c]);
+                    accS[r][c] = fmaf(q[r].y, kk[c].y, accS[r][c]);
+                    accS[r][c] = fmaf(q[r].z, kk[c].z, accS[r][c]);
+                    accS[r][c] = fmaf(q[r].w, kk[c].w, accS[r][c]);
+                    accP[r][c] = fmaf(o[r].x, v[c].x, accP[r][c]);
+                    accP[r][c] = fmaf(o[r].y, v[c].y, accP[r][c]);
+                    accP[r][c] = fmaf(o[r].z, v[c].z, accP[r][c]);
+                    accP[r][c] = fmaf(o[r].w, v[c].w, accP[r][c]);
+                }
+        }
+        // ---- P = exp(scale S - LSE) on visible pairs, dS = P (dP - D)
+#pragma unroll
+        for (int r = 0; r < TR; ++r) {
+            const int ri = ty + 16 * r, i = m0 + ri;
+            const float l2 = sL[ri], Di = sDd[ri];
+#pragma unroll
+            for (int c = 0; c < TC; ++c) {
+                const int j = n0 + tx + 16 * c;
+                const bool vis = i < S_q && j < S_k && key_visible(i + off, j, a.causal, a.window);
+                const float pv = vis ? exp2f(fmaf(accS[r][c], sc2, -l2)) : 0.f;
+                sP[ri * LP + tx + 16 * c] = pv;
+                sdS[ri * LP + tx + 16 * c] = pv * (accP[r][c] - Di);
+            }
+        }
+        __syncthreads();
+        // ---- dV += P^T dO, dK += dS^T Q (key rows ty + 16r, column groups tx + 16q)
+#pragma unroll 2
+        for (int i = 0; i < BM; ++i) {
+            float pk[TC], dk[TC];
+#pragma unroll
+            for (int r = 0; r < TC; ++r) {
+                pk[r] = sP[i * LP + ty + 16 * r];
+                dk[r] = sdS[i * LP + ty + 16 * r];
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+                const int f = tx + 16 * q;
+                if (NG * 16 * 4 == D || f < D / 4) {
+                    const float4 o = *reinterpret_cast<const float4*>(sdO + i * LD + 4 * f);
+                    const float4 x = *reinterpret_cast<const float4*>(sQ + i * LD + 4 * f);
+#pragma unroll
+                    for (int r = 0; r < TC; ++r) {
+                        accV[r][q][0] = fmaf(pk[r], o.x, accV[r][q][0]);
+                        accV[r][q][1] = fmaf(pk[r], o.y, accV[r][q][1]);
+                        accV[r][q][2] = fmaf(pk[r], o.z, accV[r][q][2]);
+                        accV[r][q][3] = fmaf(pk[r], o.w, accV[r][q][3]);
+                        accK[r][q][0] = fmaf(dk[r], x.x, accK[r][q][0]);
+                        accK[r][q][1] = fmaf(dk[r], x.y, accK[r][q][1]);
+                        accK[r][q][2] = fmaf(dk[r], x.z, accK[r][q][2]);
+                        accK[r][q][3] = fmaf(dk[r], x.w, accK[r][q][3]);
+                    }
+                }
+            }
+        }
+        // ---- dQacc += dS K (query rows ty + 16r, column groups tx + 16q)
+        if (!a.deterministic) {
+            float accQ[TR][NG][4];
+#pragma unroll
+            for (int r = 0; r < TR; ++r)
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) accQ[r][q][u] = 0.f;
+#pragma unroll 2
+            for (int jj = 0; jj < BN; ++jj) {
+                float ds[TR];
+#pragma unroll
+                for (int r = 0; r < TR; ++r) ds[r] = sdS[(ty + 16 * r) * LP + jj];
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    const int f = tx + 16 * q;
+                    if (NG * 16 * 4 == D || f < D / 4) {
+                        const float4 kv = *reinterpret_cast<const float4*>(sK + jj * LD + 4 * f);
+#pragma unroll
+                        for (int r = 0; r < TR; ++r) {
+                            accQ[r][q][0] = fmaf(ds[r], kv.x, accQ[r][q][0]);
+                            accQ[r][q][1] = fmaf(ds[r], kv.y, accQ[r][q][1]);
+                            accQ[r][q][2] = fmaf(ds[r], kv.z, accQ[r][q][2]);
+                            accQ[r][q][3] = fmaf(ds[r], kv.w, accQ[r][q][3]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < TR; ++r) {
+                const int ri = ty + 16 * r;
+                if (ri < rows) {
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        const int f = tx + 16 * q;
+                        if (NG * 16 * 4 == D || f < D / 4)
+                            ptx::red_add_v4(p.dqacc + ((row0 + m0 + ri) * a.H + h) * D + 4 * f, accQ[r][q][0],
+                                            accQ[r][q][1], accQ[r][q][2], accQ[r][q][3]);
+                    }
+                }
+            }
+        }
+    }
+    // ---- dK (scaled) and dV rows of this tile
+#pragma unroll
+    for (int r = 0; r < TC; ++r) {
+        const int rr = ty + 16 * r;
+        if (rr >= krows) continue;
+        T* dV = static_cast<T*>(a.dV) + (long long)(kt.k_tok + sub + rr) * a.sdv.tok + (long long)hk * a.sdv.head;
+        T* dK = static_cast<T*>(a.dK) + (long long)(kt.k_tok + sub + rr) * a.sdk.tok + (long long)hk * a.sdk.head;
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const int f = tx + 16 * q;
+            if (!(NG * 16 * 4 == D || f < D / 4)) continue;
+            store4<T>(dV + 4 * f, accV[r][q][0], accV[r][q][1], accV[r][q][2], accV[r][q][3]);
+            store4<T>(dK + 4 * f, accK[r][q][0] * a.scale, accK[r][q][1] * a.scale, accK[r][q][2] * a.scale,
+                      accK[r][q][3] * a.scale);
+        }
+    }
+}
+
+// Deterministic dQ: one CTA per (kDqRows query rows, head) forms the accumulator rows itself,
+// visiting the visible keys in index order, so every row is one fixed sequence of additions.
+constexpr int kDqRows = 16;
+constexpr int kDqKeys = 32;
+constexpr int kDqThreads = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kDqThreads) packed_dq_simt_kernel(const PackedBwd a, const BwdPlan p) {
+    extern __shared__ float smem[];
+    float* sQ = smem;
+    float* sdO = sQ + kDqRows * D;
+    float* sK = sdO + kDqRows * D;
+    float* sV = sK + kDqKeys * D;
+    float* sdS = sV + kDqKeys * D;
+    constexpr int kPerThread = kDqRows * D / kDqThreads;
+    const int tid = threadIdx.x;
+    const int u = blockIdx.x / (kBwdTile / kDqRows);
+    if (u >= p.head[0]) return;
+    const QueryTile t = p.query[u];
+    const int r0 = (blockIdx.x % (kBwdTile / kDqRows)) * kDqRows;  // within the query tile
+    const int rows = min(kDqRows, t.rows - r0);
+    if (rows <= 0) return;
+    // the sequence of this query tile
+    int n = 0;
+    for (int hi = a.N; hi - n > 1;) {
+        const int mid = (n + hi) >> 1;
+        if (p.seq_q[mid] <= u)
+            n = mid;
+        else
+            hi = mid;
+    }
+    const int k_tok0 = a.cu_k[n], S_k = a.cu_k[n + 1] - k_tok0;
+    const int S_q = a.cu_q[n + 1] - a.cu_q[n];
+    const int m0 = t.q_tok - a.cu_q[n] + r0;  // first query of this CTA within the sequence
+    const int h = blockIdx.y, hk = h / (a.H / a.H_kv);
+    const int off = S_k - S_q;
+    const float sc2 = a.scale * 1.4426950408889634f;
+    const long long row = (long long)u * kBwdTile + r0;
+    const T* Q = static_cast<const T*>(a.Q) + (long long)(t.q_tok + r0) * a.sq.tok + (long long)h * a.sq.head;
+    const T* dO = static_cast<const T*>(a.dO) + (long long)(t.q_tok + r0) * a.sdo.tok + (long long)h * a.sdo.head;
+    const T* K = static_cast<const T*>(a.K) + (long long)k_tok0 * a.sk.tok + (long long)hk * a.sk.head;
+    const T* V = static_cast<const T*>(a.V) + (long long)k_tok0 * a.sv.tok + (long long)hk * a.sv.head;
+    for (int e = tid; e < kDqRows * D; e += kDqThreads) {
+        const int r = e / D, c = e % D;
+        sQ[e] = r < rows ? TypeTraits<T>::to_f32(Q[r * a.sq.tok + c]) : 0.f;
+        sdO[e] = r < rows ? TypeTraits<T>::to_f32(dO[r * a.sdo.tok + c]) : 0.f;
+    }
+    float acc[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) acc[i] = 0.f;
+    Shape sh;
+    sh.S_q = S_q;
+    sh.S_k = S_k;
+    sh.causal = a.causal;
+    sh.window = a.window;
+    int k_lo, k_hi;
+    key_range(sh, m0, m0 + rows, k_lo, k_hi);
+    for (int n0 = k_lo - k_lo % kDqKeys; n0 < k_hi; n0 += kDqKeys) {
+        __syncthreads();
+        for (int e = tid; e < kDqKeys * D; e += kDqThreads) {
+            const int j = n0 + e / D, c = e % D;
+            sK[e] = j < S_k ? TypeTraits<T>::to_f32(K[j * a.sk.tok + c]) : 0.f;
+            sV[e] = j < S_k ? TypeTraits<T>::to_f32(V[j * a.sv.tok + c]) : 0.f;
+        }
+        __syncthreads();
+        for (int pr = tid; pr < kDqRows * kDqKeys; pr += kDqThreads) {
+            const int r = pr / kDqKeys, jj = pr % kDqKeys;
+            const int j = n0 + jj;
+            float ds = 0.f;
+            if (r < rows && j < S_k && key_visible(m0 + r + off, j, a.causal, a.window)) {
+                float sc = 0.f, dp = 0.f;
+                for (int c = 0; c < D; ++c) {
+                    sc = fmaf(sQ[r * D + c], sK[jj * D + c], sc);
+                    dp = fmaf(sdO[r * D + c], sV[jj * D + c], dp);
+                }
+                const float pv = exp2f(fmaf(sc, sc2, -p.lse2[h * p.rows + row + r]));
+                ds = pv * (dp - p.D[h * p.rows + row + r]);
+            }
+            sdS[pr] = ds;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int e = tid + i * kDqThreads, r = e / D, c = e % D;
+            for (int jj = 0; jj < kDqKeys; ++jj) acc[i] = fmaf(sdS[r * kDqKeys + jj], sK[jj * D + c], acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int e = tid + i * kDqThreads, r = e / D, c = e % D;
+        if (r < rows) p.dqacc[((row + r) * a.H + h) * D + c] = acc[i];
+    }
+}
+
+template <typename... A>
+cudaError_t launch_pdl(void (*k)(A...), long long grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <typename T, int D>
+cudaError_t preprocess_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    return launch_pdl(packed_preprocess_kernel<T, D>, (long long)p.max_units * (kBwdTile / kRowsPerBlock), kThreads, st, a, p);
+}
+
+template <typename T, int D>
+cudaError_t dq_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    return launch_pdl(packed_dq_kernel<T, D>, (long long)p.max_units * (kBwdTile / kRowsPerBlock), kThreads, st, a, p);
+}
+
+template <typename T, int D>
+cudaError_t bwd_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    using C = SCfg<D>;
+    cudaError_t e;
+    if (p.max_keys > 0) {
+        auto kern = packed_bwd_simt_kernel<T, D>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)((long long)p.max_keys * a.H_kv * (kBwdTile / C::BN)), kThreads, C::SMEM, st>>>(a, p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (a.deterministic && p.max_units > 0) {
+        const size_t smem = sizeof(float) * (2 * kDqRows * D + 2 * kDqKeys * D + kDqRows * kDqKeys);
+        auto kern = packed_dq_simt_kernel<T, D>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        kern<<<dim3((unsigned)(p.max_units * (kBwdTile / kDqRows)), (unsigned)a.H), kDqThreads, smem, st>>>(a, p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_packed_preprocess(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    if (p.max_units == 0) return cudaSuccess;
+#define FA_L(T, DD) return preprocess_t<T, DD>(a, p, st)
+    FA_DISPATCH_HEAD_DIM(a.dtype, a.d, FA_L);
+#undef FA_L
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_packed_dq(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    if (p.max_units == 0) return cudaSuccess;
+#define FA_L(T, DD) return dq_t<T, DD>(a, p, st)
+    FA_DISPATCH_HEAD_DIM(a.dtype, a.d, FA_L);
+#undef FA_L
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_packed_bwd_simt(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    if (a.dtype == FA_F32) {
+        switch (a.d) {
+            case 32: return bwd_t<float, 32>(a, p, st);
+            case 64: return bwd_t<float, 64>(a, p, st);
+            case 96: return bwd_t<float, 96>(a, p, st);
+            case 128: return bwd_t<float, 128>(a, p, st);
+            case 256: return bwd_t<float, 256>(a, p, st);
+        }
+    } else if (a.d == 256) {
+        return a.dtype == FA_F16 ? bwd_t<__half, 256>(a, p, st) : bwd_t<__nv_bfloat16, 256>(a, p, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace fa

@@ -146,6 +146,43 @@ def fa_varlen_fwd(Q, K, V, cu_q, cu_k, scale: float | None = None, causal: bool 
     return O, LSE
 
 
+def fa_varlen_bwd(dO, Q, K, V, O, LSE, cu_q, cu_k, scale: float | None = None, causal: bool = False,
+                  window_size: int = 0, deterministic: bool = False, dQ=None, dK=None, dV=None, stream=None):
+    """(dQ, dK, dV) of attention inside each packed sequence; see include/fa.h (fa_varlen_bwd)."""
+    qs = _rows("Q", Q, 3)
+    T_q, H, d = Q.shape
+    ks = _rows("K", K, 3, dtype=Q.dtype)
+    T_k, H_kv, dk = K.shape
+    if dk != d:
+        _refuse("K", f"shape {tuple(K.shape)} incompatible with Q {tuple(Q.shape)}")
+    vs = _rows("V", V, 3, K.shape, Q.dtype)
+    dos = _rows("dO", dO, 3, Q.shape, Q.dtype)
+    os_ = _rows("O", O, 3, Q.shape, Q.dtype)
+    if LSE.shape != (H, T_q) or LSE.dtype != torch.float32 or not LSE.is_contiguous():
+        _refuse("LSE", f"must be contiguous float32 {(H, T_q)}, got {LSE.dtype} {tuple(LSE.shape)}")
+    N = cu_q.numel() - 1
+    _ints("cu_q", cu_q, (N + 1,))
+    _ints("cu_k", cu_k, (N + 1,))
+    dt = _dtype(Q)
+    dev = _device_of(Q, dO, K, V, O, LSE, cu_q, cu_k, dQ, dK, dV)
+    lib = load_library()
+    with _on(dev, stream) as st:
+        fill = int(dQ is None and dK is None and dV is None)
+        new = torch.Tensor.new_empty if fill else torch.Tensor.new_zeros
+        dQ = new(Q, Q.shape) if dQ is None else dQ
+        dK = new(K, K.shape) if dK is None else dK
+        dV = new(V, V.shape) if dV is None else dV
+        dqs, dks, dvs = (_rows(n, t, 3, r.shape, Q.dtype) for n, t, r in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V)))
+        need = _varlen_ws(dev.index, N, T_q, T_k, H, H_kv, d, dt, 1)
+        ws = _workspace(need, dev)
+        _check(lib.fa_varlen_bwd(dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(),
+                                 dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), N, T_q,
+                                 T_k, H, H_kv, d, _strides(dos, qs, ks, vs, os_, dqs, dks, dvs),
+                                 1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
+                                 int(window_size), int(bool(deterministic)), fill, dt, ws.data_ptr(), need, st))
+    return dQ, dK, dV
+
+
 def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float | None = None, causal: bool = True,
                  window_size: int = 0, O=None, LSE=None, stream=None):
     """(O, LSE) of each request's newest tokens over its pages; see include/fa.h (fa_paged_fwd)."""

@@ -235,6 +235,21 @@ size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d
                                  int backward);
 
 /*
+ * fa_varlen_bwd -- dQ, dK, dV of fa_varlen_fwd from dO, O and LSE (fa_bwd_ex inside
+ * each sequence).  Rows of keys that no query sees get 0.
+ *   strides       : {dO token, dO head, then the same of Q, K, V, O, dQ, dK, dV}
+ *   deterministic : as in fa_bwd_ex (0 = dQ reduced with fp32 atomics, 1 =
+ *                   bitwise reproducible dQ); dK and dV are reproducible in both
+ *   fill          : gradient rows of no sequence are 0 = left, 1 = set to 0
+ * F16/BF16 with d <= 128 run a tcgen05 kernel, F32 and d = 256 an FFMA kernel.
+ */
+int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, const void* O,
+                  const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q, const int* cu_k,
+                  int N, int T_q, int T_k, int H, int H_kv, int d, const long long* strides,
+                  float scale, int causal, int window_size, int deterministic, int fill, int dtype,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fa_paged_fwd -- attention of each request's newest tokens over its pages of a
  * key/value cache (one token per request is a decode step, many a chunk of its
  * prompt; both kinds may share a call).

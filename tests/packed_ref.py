@@ -6,7 +6,7 @@ Bounds (u = eps / 2 of the tensors' type, the largest relative error of one roun
     once at the end, so with A_ic = sum_j P_ij |V_jc|
       |O - O64|   <= u (|O64| + A) + e A,
       |dV - dV64| <= u (|dV64| + sum_i P_ij |dO_ic|) + e (...)
-      |dQ - dQ64| <= u (|dQ64| + scale sum_j |dS_ij| |K_jc|) + e (...), dK alike;
+      |dQ - dQ64| <= u (|dQ64| + scale sum_j |dS_ij| |K_jc|) + e (...), dK alike (grads());
     fp32 tensors are not rounded in between: u = 2^-24;
   * e covers fp32 arithmetic: a product of n terms summed in fp32 is off by at most
     n 2^-23 sum |terms| (2^-23 per step: tensor cores may truncate), so a score is off by
@@ -59,45 +59,54 @@ def attend(q, k, v, causal, window, scale):
 
 
 def grads(do, q, k, v, o, lse, causal, window, scale):
-    """fp64 dQ, dK, dV of one sequence, the sums of absolute values, and e."""
+    """fp64 dQ, dK, dV of one sequence; for each the sum of magnitudes that a rounding of dS (P)
+    scales with, and the one that fp32 arithmetic scales with; and e.
+
+    dP and D are d-term fp32 sums and P carries the factor of its score's error, so
+      |error of dS_ij| <= e P_ij (sum_c |dO_ic V_jc| + sum_c |dO_ic O_ic|) = e P_ij M_ij,
+    which does not shrink with dS itself: where dP = D (a query with one key, for which O = V)
+    dS is 0 and only that remains.  It reaches dQ as e scale sum_j P_ij M_ij |K_j|, dK alike.
+    """
     nq, H, d = q.shape
     nk, H_kv, _ = k.shape
     g = H // H_kv
-    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
-    aq, ak, av = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    out = [torch.zeros_like(x) for x in (q, k, v)]
+    mag = [torch.zeros_like(x) for x in (q, k, v)]
+    f32 = [torch.zeros_like(x) for x in (q, k, v)]
     vis = visible(nq, nk, causal, window)
     e = 0.0
     if nk and nq:
         for h in range(H):
-            kh, vh = k[:, h // g], v[:, h // g]
+            c = h // g
+            kh, vh = k[:, c], v[:, c]
             s = (q[:, h] @ kh.T) * scale
             s_err = d * STEP * scale * float((q[:, h].abs() @ kh.abs().T).max())
             L = torch.where(lse[h] == -math.inf, 0.0, lse[h])
             P = torch.exp((s - L[:, None]).masked_fill(~vis, -math.inf))
             D = (do[:, h] * o[:, h]).sum(1)
-            dp = do[:, h] @ vh.T
-            mag = do[:, h].abs() @ vh.abs().T + (do[:, h] * o[:, h]).abs().sum(1)[:, None]
-            dS = P * (dp - D[:, None])
-            dq[:, h] = scale * (dS @ kh)
-            dk[:, h // g] += scale * (dS.T @ q[:, h])
-            dv[:, h // g] += P.T @ do[:, h]
-            # |dS| plus what fp32 may add to it, as sums of absolute terms
-            rel = 2 * math.expm1(s_err) + (nq * g + nk) * STEP + 2.0 ** -21
-            big = dS.abs() + P * mag  # one scale for the rounding of dS and for e
-            aq[:, h] = scale * (dS.abs() @ kh.abs())
-            ak[:, h // g] += scale * (dS.abs().T @ q[:, h].abs())
-            av[:, h // g] += P.T @ do[:, h].abs()
-            # fp32 part: kept apart in e through the ratio of the two sums
-            r = float((big.sum() / dS.abs().sum().clamp(min=1e-30)))
-            e = max(e, (rel + d * STEP) * max(1.0, min(r, 1e4)))
-    return dq, dk, dv, aq, ak, av, e
+            dS = P * (do[:, h] @ vh.T - D[:, None])
+            M = P * (do[:, h].abs() @ vh.abs().T + (do[:, h] * o[:, h]).abs().sum(1)[:, None])
+            out[0][:, h] = scale * (dS @ kh)
+            out[1][:, c] += scale * (dS.T @ q[:, h])
+            out[2][:, c] += P.T @ do[:, h]
+            mag[0][:, h] = scale * (dS.abs() @ kh.abs())
+            mag[1][:, c] += scale * (dS.abs().T @ q[:, h].abs())
+            mag[2][:, c] += P.T @ do[:, h].abs()
+            f32[0][:, h] = scale * (M @ kh.abs())
+            f32[1][:, c] += scale * (M.T @ q[:, h].abs())
+            f32[2][:, c] += P.T @ do[:, h].abs()
+            # LSE is given in fp32 and scaled once more in fp32: 2^-22 |LSE| in the exponent
+            l_err = 2.0 ** -22 * float(L.abs().max())
+            e = max(e, 2 * math.expm1(s_err + l_err) + (d + nq * g + nk) * STEP + 2.0 ** -21)
+    return out, mag, f32, e
 
 
-def check(name, got, want, mag, e, dtype):
-    """got within u (|want| + mag) + e mag of want, elementwise; infinities equal."""
+def check(name, got, want, mag, e, dtype, f32=None):
+    """got within u (|want| + mag + e f32) + e f32 of want, elementwise (f32: mag unless given)."""
     got, want, mag = got.double().cpu(), want.cpu(), mag.cpu()
+    f32 = mag if f32 is None else f32.cpu()
     assert torch.isfinite(got).all(), f"{name}: not finite"
-    tol = U[dtype] * (want.abs() + mag) * 1.001 + e * mag + 1e-30
+    tol = U[dtype] * (want.abs() + mag + e * f32) * 1.001 + e * f32 + 1e-30
     if dtype == torch.float16:
         tol = tol + 2.0 ** -24  # subnormal step
     worst = ((got - want).abs() / tol).max() if want.numel() else 0.0
