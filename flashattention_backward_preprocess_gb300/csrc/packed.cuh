@@ -40,10 +40,12 @@ struct PackedFwd {
 // ---------------------------------------------------------------- forward plan
 // A unit is `tpt` consecutive query tokens of one sequence; the g query heads of a key/value
 // head are packed beside each other, so a tile has tpt * g rows (token major, then head) and
-// reads each key once for the whole group.  A unit costs max(key tiles, 1) per head; the plan
-// lays (unit, head, key tile) out on one axis of W positions and gives every CTA the same
-// number of consecutive ones, so the grid is filled whatever the lengths are.  A (unit, head)
-// item that a CTA boundary cuts is computed in parts and joined by the last CTA to finish.
+// reads each key once for the whole group.  A (unit, head) item takes `overhead` positions for
+// what it costs beside its key tiles (the epilogue), then one per key tile (one if it has none).
+// The plan lays the items out on one axis of W positions and gives every CTA the same number of
+// consecutive ones, so the grid is filled whatever the lengths are.  A tile belongs to the CTA
+// that has its position; an item whose tiles belong to several CTAs is computed in parts and
+// joined by the last of them to finish.
 struct alignas(16) FwdTile {
     int n;        // sequence
     int q_tok;    // first query token (row of Q)
@@ -78,6 +80,7 @@ struct FwdGeom {
     int ctas;       // CTAs of the grid
     int D;          // columns of a part
     int min_chunk;  // positions per CTA at least
+    int overhead;   // positions an item takes beside its key tiles
 };
 
 inline size_t packed_align(size_t x) { return (x + 255) / 256 * 256; }
@@ -109,8 +112,8 @@ inline size_t fwd_plan_layout(const PackedFwd& a, const FwdGeom& g, void* ws, Fw
 
 // A CTA's walk over its positions: segments (unit, head, key tiles [j0, j1)).
 struct FwdWalk {
-    long long pos, end, chunk, base;
-    int u, hd, j0, j1, cc, heads;
+    long long item, start, end, chunk;  // first position of the item's tiles; the CTA's positions
+    int u, hd, j0, j1, cc, heads, overhead;
     FwdTile t;
     __device__ __forceinline__ void load(const FwdPlan& p) {
         const int4* r = reinterpret_cast<const int4*>(p.tile + u);
@@ -119,84 +122,115 @@ struct FwdWalk {
         t.k_base = b.x, t.S_k = b.y, t.n_first = b.z, t.n_cnt = b.w;
         cc = t.n_cnt > 0 ? t.n_cnt : 1;
     }
-    __device__ __forceinline__ void cut() {
-        const long long left = end - pos;
-        j1 = left < cc - j0 ? j0 + (int)left : cc;
-    }
-    __device__ __forceinline__ bool init(const FwdPlan& p, int cta, int heads_) {
-        heads = heads_;
-        const long long W = p.head[0];
-        chunk = p.head[1];
-        pos = chunk * cta;
-        end = pos + chunk < W ? pos + chunk : W;
-        if (pos >= end) return false;
-        u = p.start[cta];
-        load(p);
-        const long long rel = pos - p.base[u];
-        hd = (int)(rel / cc);
-        j0 = (int)(rel - (long long)hd * cc);
-        cut();
+    // tiles of the item that belong to the CTA; false if there are none
+    __device__ __forceinline__ bool cut() {
+        if (item >= end) return false;
+        j0 = start > item ? (int)(start - item) : 0;
+        j1 = end - item < cc ? (int)(end - item) : cc;
         return true;
     }
+    __device__ __forceinline__ bool init(const FwdPlan& p, int cta, int heads_, int overhead_) {
+        heads = heads_;
+        overhead = overhead_;
+        const long long W = p.head[0];
+        chunk = p.head[1];
+        start = chunk * cta;
+        end = start + chunk < W ? start + chunk : W;
+        if (start >= end) return false;
+        u = p.start[cta];
+        load(p);
+        const long long base = p.base[u];
+        hd = (int)((start - base) / (cc + overhead));
+        item = base + (long long)hd * (cc + overhead) + overhead;
+        return cut();
+    }
     __device__ __forceinline__ bool next(const FwdPlan& p) {
-        pos += j1 - j0;
-        if (pos >= end) return false;
-        j0 = 0;
+        item += cc;
+        if (item >= end) return false;  // the next item's first position
         if (++hd == heads) {
             hd = 0;
             ++u;
             load(p);
         }
-        cut();
-        return true;
+        item += overhead;
+        return cut();
     }
     __device__ __forceinline__ int tiles() const { return t.n_cnt > 0 ? j1 - j0 : 0; }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == cc; }
-    // of a cut item: the CTA its first position belongs to, and its number of parts
+    // of a cut item: the CTA its first tile belongs to, and its number of parts
     __device__ __forceinline__ void parts(int& first, int& count) const {
-        const long long s = pos - j0;
-        first = (int)(s / chunk);
-        count = (int)((s + cc - 1) / chunk) - first + 1;
+        first = (int)(item / chunk);
+        count = (int)((item + cc - 1) / chunk) - first + 1;
     }
 };
 
 // packed_plan.cu
 cudaError_t launch_fwd_plan(const PackedFwd& a, const FwdGeom& g, const FwdPlan& p, cudaStream_t st);
 
-// Joins the parts of one cut item (threads tid of nthreads, all of them past the barrier that
-// follows the last part's arrival): O = sum_k O_k 2^(m_k - M) / sum_k l_k 2^(m_k - M).
-template <typename T>
+// Joins the parts of one cut item (kThreads threads, all of them past the barrier that follows
+// the last part's arrival): O = sum_k O_k 2^(m_k - M) / sum_k l_k 2^(m_k - M), parts in the order
+// of their keys.  s_row: `rows` float2 of shared memory; sync: a barrier of those threads.
+template <typename T, int kThreads, int kRowsLd, int kD, typename Sync>
 __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p, const FwdTile& t, int head0, int g,
-                                           int rows, int rows_ld, int D, int first, int count, int tid,
-                                           int nthreads) {
-    const int c4n = a.d / 4;
-    for (int e = tid; e < rows * c4n; e += nthreads) {
-        const int r = e / c4n, c = (e - r * c4n) * 4;
-        float M = -INFINITY;
+                                           int rows, int first, int count, int tid, float2* s_row, Sync sync) {
+    auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * first + 1 : 2 * (first + k)) * kRowsLd; };
+    for (int r = tid; r < rows; r += kThreads) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll 4
         for (int k = 0; k < count; ++k) {
-            const int slot = k == 0 ? 2 * first + 1 : 2 * (first + k);
-            M = fmaxf(M, __ldcg(&p.part_ml[(size_t)slot * rows_ld + r]).x);
+            const float2 ml = __ldcg(&p.part_ml[slot(k) + r]);
+            if (ml.x > M) {
+                L = L * exp2f(M - ml.x) + ml.y;
+                M = ml.x;
+            } else if (ml.x > -INFINITY) {
+                L += ml.y * exp2f(ml.x - M);
+            }
         }
-        float L = 0.f;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < count; ++k) {
-            const int slot = k == 0 ? 2 * first + 1 : 2 * (first + k);
-            const float2 ml = __ldcg(&p.part_ml[(size_t)slot * rows_ld + r]);
-            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-            if (w == 0.f) continue;  // a part in which the row sees no key
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * rows_ld + r) * D + c));
-            L += ml.y * w;
-            s.x += o.x * w, s.y += o.y * w, s.z += o.z * w, s.w += o.w * w;
-        }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int tok = t.q_tok + r / g, h = head0 + r % g;
-        T out[4] = {TypeTraits<T>::from_f32(s.x * inv), TypeTraits<T>::from_f32(s.y * inv),
-                    TypeTraits<T>::from_f32(s.z * inv), TypeTraits<T>::from_f32(s.w * inv)};
-        T* dst = static_cast<T*>(a.O) + tok * a.o.tok + h * a.o.head + c;
+        s_row[r] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
+        a.LSE[(size_t)(head0 + r % g) * a.T_q + t.q_tok + r / g] =
+            L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    }
+    sync();
+    // four columns of a row per thread and step; kBatch steps' loads in flight together
+    constexpr int kBatch = 8, C4 = kD / 4;
+    for (int e0 = tid; e0 < rows * C4; e0 += kBatch * kThreads) {
+        float4 s[kBatch];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) dst[q] = out[q];
-        if (c == 0)
-            a.LSE[(size_t)h * a.T_q + tok] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        for (int b = 0; b < kBatch; ++b) s[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < count; ++k) {
+            float4 o[kBatch];
+            float w[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int e = e0 + b * kThreads, r = e / C4;
+                if (r < rows) {
+                    o[b] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) + r) * kD) + e % C4);
+                    w[b] = __ldcg(&p.part_ml[slot(k) + r]).x;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int r = (e0 + b * kThreads) / C4;
+                // a part in which the row sees no key adds nothing
+                if (r < rows && w[b] > -INFINITY) {
+                    const float f = exp2f(w[b] - s_row[r].x);
+                    s[b].x += o[b].x * f, s[b].y += o[b].y * f, s[b].z += o[b].z * f, s[b].w += o[b].w * f;
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + b * kThreads, r = e / C4, c = e % C4 * 4;
+            if (r >= rows || c >= a.d) continue;
+            const float inv = s_row[r].y;
+            T* dst = static_cast<T*>(a.O) + (t.q_tok + r / g) * a.o.tok + (head0 + r % g) * a.o.head + c;
+            alignas(16) T out[4] = {TypeTraits<T>::from_f32(s[b].x * inv), TypeTraits<T>::from_f32(s[b].y * inv),
+                                    TypeTraits<T>::from_f32(s[b].z * inv), TypeTraits<T>::from_f32(s[b].w * inv)};
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<float4*>(dst) = *reinterpret_cast<const float4*>(out);
+            else
+                *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(out);
+        }
     }
 }
 

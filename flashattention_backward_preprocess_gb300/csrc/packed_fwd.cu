@@ -98,10 +98,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// 32 bytes per thread (32-byte aligned): a row per thread makes every store of a warp touch 32
+// lines, so the widest store has the fewest of them
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const PackedFwd a, const FwdPlan plan, int tpt) {
+                      const __grid_constant__ CUtensorMap tmV, const PackedFwd a, const FwdPlan plan, int tpt, int overhead) {
     using C = PCfg<D>;
     constexpr int BN = C::BN, NB = C::NBUF;
     constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
@@ -146,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // own boxes of a K / V tile.
         if (!*abort_flag) {
             FwdWalk wq, wk;
-            bool q_more = wq.init(plan, blockIdx.x, a.H_kv), kv_more = wk.init(plan, blockIdx.x, a.H_kv);
+            bool q_more = wq.init(plan, blockIdx.x, a.H_kv, overhead),
+                 kv_more = wk.init(plan, blockIdx.x, a.H_kv, overhead);
             while (q_more && wq.tiles() == 0) q_more = wq.next(plan);
             while (kv_more && wk.tiles() == 0) kv_more = wk.next(plan);
             int q_act = 0, jg = 0, kj = kv_more ? wk.j0 : 0;
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             int jg = 0, ka = 0;
             FwdWalk w;
-            bool more = w.init(plan, blockIdx.x, a.H_kv);
+            bool more = w.init(plan, blockIdx.x, a.H_kv, overhead);
             if (warp == kWarpMma) {
                 const uint64_t dQ_k = ptx::sw128_desc(sbase + C::OFF_Q, 16, 1024);
                 const uint64_t dK_k = ptx::sw128_desc(sbase + C::OFF_K, 16, 1024);
@@ -325,10 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
         const int ti = t / g, th = t - ti * g;  // token and head of the row
         const float scale_log2 = a.scale * 1.4426950408889634f;
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.O) | (a.o.tok * 2) | (a.o.head * 2)) & 31) == 0;
         bool ok = !*abort_flag;
         int jg = 0, ka = 0;
         FwdWalk w;
-        bool more = w.init(plan, blockIdx.x, a.H_kv);
+        bool more = w.init(plan, blockIdx.x, a.H_kv, overhead);
         for (; ok && more; more = w.next(plan)) {
             const int rows = w.t.n_tok * g;
             const bool row_valid = t < rows;
@@ -458,21 +468,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int kk = 0; kk < 32; ++kk) o[kk] = 0u;
                     }
                     if (row_valid && whole) {
+                        if (c * 32 < a.d) {
+                            uint32_t w[16];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            uint32_t w4[4];
+                            for (int kk = 0; kk < 16; ++kk)
+                                w[kk] = pack2<kBF16>(__uint_as_float(o[2 * kk]) * inv_l,
+                                                     __uint_as_float(o[2 * kk + 1]) * inv_l);
+                            if (wide) {
+                                st_global_v8(Orow + c * 32, w);
+                                st_global_v8(Orow + c * 32 + 16, w + 8);
+                            } else {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                w4[kk] = pack2<kBF16>(__uint_as_float(o[u * 8 + 2 * kk]) * inv_l,
-                                                      __uint_as_float(o[u * 8 + 2 * kk + 1]) * inv_l);
-                            if (c * 32 + u * 8 < a.d)
-                                *reinterpret_cast<uint4*>(Orow + c * 32 + u * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                                for (int u = 0; u < 4; ++u)
+                                    *reinterpret_cast<uint4*>(Orow + c * 32 + u * 8) =
+                                        make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                            }
                         }
                     } else if (row_valid) {
 #pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            *reinterpret_cast<uint4*>(Prow + c * 32 + u * 4) =
-                                make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+                        for (int u = 0; u < 4; ++u) st_global_v8(Prow + c * 32 + u * 8, o + u * 8);
                     }
                     __syncwarp();
                 }
@@ -496,7 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::named_bar_sync(kSoftBarrier, 128);
                 if (*last_flag) {
                     __threadfence();
-                    join_parts<T>(a, plan, w.t, w.hd * g, g, rows, BM, D, first, count, t, 128);
+                    join_parts<T, 128, BM, D>(a, plan, w.t, w.hd * g, g, rows, first, count, t,
+                                              reinterpret_cast<float2*>(smem + OFF_MISC + 16),
+                                              [] { ptx::named_bar_sync(kSoftBarrier, 128); });
                 }
             }
             if (has) ++ka;
@@ -529,7 +545,7 @@ int sm_count() {
 template <typename T, int D, bool kPaged>
 cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     using C = PCfg<D>;
-    constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16;
+    constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16 + BM * 8;
     static_assert(kSmem <= 232448, "shared memory budget");
     const int g = a.H / a.H_kv;
     FwdGeom geo;
@@ -540,6 +556,7 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     geo.ctas = sm_count();
     geo.D = D;
     geo.min_chunk = 2;
+    geo.overhead = 3;
     FwdPlan plan;
     *bytes = fwd_plan_layout(a, geo, ws, &plan);
     if (ws == nullptr) return cudaSuccess;
@@ -591,7 +608,7 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, plan, geo.tpt);
+    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, plan, geo.tpt, geo.overhead);
 }
 
 template <typename T>

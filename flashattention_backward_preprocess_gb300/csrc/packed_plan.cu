@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) fwd_plan_kernel(const PackedFwd 
             t.n_first = hi > lo ? lo / g.bn : 0;
             t.n_cnt = hi > lo ? (hi + g.bn - 1) / g.bn - t.n_first : 0;
             p.tile[u] = t;
-            cost = (long long)max(t.n_cnt, 1) * g.heads;
+            cost = (long long)(max(t.n_cnt, 1) + g.overhead) * g.heads;
         }
         long long total;
         const long long at = block_excl_scan(cost, s_lsum, &total);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) fwd_plan_kernel(const PackedFwd 
     for (int c = tid; c < g.ctas; c += kPlanThreads) p.done[c] = 0u;
     for (int u = tid; u < U; u += kPlanThreads) {
         const long long b = p.base[u];
-        const long long e = b + (long long)max(p.tile[u].n_cnt, 1) * g.heads;
+        const long long e = b + (long long)(max(p.tile[u].n_cnt, 1) + g.overhead) * g.heads;
         for (long long c = (b + chunk - 1) / chunk; c * chunk < e; ++c) p.start[c] = u;
     }
 }

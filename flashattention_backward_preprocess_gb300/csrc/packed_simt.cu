@@ -13,12 +13,14 @@ namespace {
 constexpr int BM = 64, BN = 64;
 constexpr int kThreads = 256;
 constexpr int KT_LD = BN + 4;
+constexpr int kOverhead = 1;  // a tile takes longer than the rest of its item
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-    packed_fwd_simt_kernel(const PackedFwd a, const FwdPlan plan, int tpt, int hsub) {
+    packed_fwd_simt_kernel(const PackedFwd a, const FwdPlan plan, int hsub) {
     extern __shared__ float smem[];
     __shared__ int s_last;
+    __shared__ float2 s_row[BM];
     float* sQ = smem;             // [BM][D]
     float* sKt = sQ + BM * D;     // [D][KT_LD]
     float* sV = sKt + D * KT_LD;  // [BN][D]
@@ -31,7 +33,7 @@ __global__ void __launch_bounds__(kThreads)
     const T* K = static_cast<const T*>(a.K);
     const T* V = static_cast<const T*>(a.V);
     FwdWalk w;
-    for (bool more = w.init(plan, blockIdx.x, a.H_kv * hsub); more; more = w.next(plan)) {
+    for (bool more = w.init(plan, blockIdx.x, a.H_kv * hsub, kOverhead); more; more = w.next(plan)) {
         // groups of more heads than a tile has rows are cut into hsub pieces of up to 64
         const int hk = w.hd / hsub, h0 = (w.hd % hsub) * BM;
         const int gh = min(g - h0, BM);      // heads of this item
@@ -176,7 +178,8 @@ __global__ void __launch_bounds__(kThreads)
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join_parts<T>(a, plan, w.t, head0, gh, rows, BM, D, first, count, tid, kThreads);
+                join_parts<T, kThreads, BM, D>(a, plan, w.t, head0, gh, rows, first, count, tid, s_row,
+                                               [] { __syncthreads(); });
             }
         }
     }
@@ -199,6 +202,7 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     geo.ctas = (sms > 0 ? sms : 148) * (D <= 96 ? 2 : 1);  // resident CTAs by shared memory
     geo.D = D;
     geo.min_chunk = 2;
+    geo.overhead = kOverhead;
     FwdPlan plan;
     *bytes = fwd_plan_layout(a, geo, ws, &plan);
     if (ws == nullptr) return cudaSuccess;
@@ -206,7 +210,7 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<geo.ctas, kThreads, smem, st>>>(a, plan, geo.tpt, hsub);
+    kern<<<geo.ctas, kThreads, smem, st>>>(a, plan, hsub);
     return cudaGetLastError();
 }
 
