@@ -48,6 +48,8 @@ def library_path() -> str:
 def load_library(path: str | None = None):
     """Load libfa.so (built by flashattention_backward_preprocess_gb300.build)."""
     global _lib
+    if _lib is not None and path is None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

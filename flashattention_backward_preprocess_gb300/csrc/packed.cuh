@@ -12,6 +12,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "fa_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -63,8 +65,12 @@ struct FwdPlan {
     long long* base;  // [units] first position of the unit
     long long* head;  // [0] W, [1] positions per CTA
     int* start;       // [ctas] unit that holds the CTA's first position
-    unsigned* done;   // [ctas] parts finished of the item that starts in the CTA's range and leaves it
     int* seq_units;   // [N + 1] first unit of each sequence
+    // [ctas] parts finished of the item whose first tile is the CTA's: (tag << 16) | count.  A
+    // word with another tag counts as zero and the last part leaves zero, so the workspace needs
+    // no clearing and a replayed call (which has its tag again) starts clean.
+    unsigned long long* done;
+    unsigned long long tag;  // of this call, 48 bits, never 0
     // parts of cut items, two per CTA (2c: continues an item, 2c + 1: starts one): fp32
     // accumulators, not divided by the row sum, and (running max in log2 units, row sum)
     float* part_o;    // [2 ctas][rows][D]
@@ -81,12 +87,16 @@ struct FwdGeom {
     int D;          // columns of a part
     int min_chunk;  // positions per CTA at least
     int overhead;   // positions an item takes beside its key tiles
+    bool self;      // every CTA plans for itself (few units): no plan kernel, tiles per CTA
 };
+constexpr int kSelfUnits = 896;  // units (and sequences) a CTA plans for itself at most
 
 inline size_t packed_align(size_t x) { return (x + 255) / 256 * 256; }
 inline long long plan_units(const PackedFwd& a, const FwdGeom& g) {
     return a.T_q / g.tpt + (a.N < a.T_q ? a.N : a.T_q) + 1;
 }
+// A tag no earlier call of the process had.
+unsigned long long next_tag();
 // Lays the plan out in `ws`; returns the bytes it needs.
 inline size_t fwd_plan_layout(const PackedFwd& a, const FwdGeom& g, void* ws, FwdPlan* p) {
     char* b = static_cast<char*>(ws);
@@ -99,10 +109,11 @@ inline size_t fwd_plan_layout(const PackedFwd& a, const FwdGeom& g, void* ws, Fw
     };
     FwdPlan q;
     q.head = reinterpret_cast<long long*>(take(16));
-    q.tile = reinterpret_cast<FwdTile*>(take(U * sizeof(FwdTile)));
+    q.tile = reinterpret_cast<FwdTile*>(take((g.self ? C : 1) * U * sizeof(FwdTile)));
     q.base = reinterpret_cast<long long*>(take(U * 8));
     q.start = reinterpret_cast<int*>(take(C * 4));
-    q.done = reinterpret_cast<unsigned*>(take(C * 4));
+    q.done = reinterpret_cast<unsigned long long*>(take(C * 8));
+    q.tag = 0;
     q.seq_units = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
     q.part_ml = reinterpret_cast<float2*>(take(2 * C * g.rows * 8));
     q.part_o = reinterpret_cast<float*>(take(2 * C * g.rows * g.D * 4));
@@ -110,13 +121,40 @@ inline size_t fwd_plan_layout(const PackedFwd& a, const FwdGeom& g, void* ws, Fw
     return at;
 }
 
+// Counts a part of an item in; true for the last of `count`.
+__device__ __forceinline__ bool arrive_part(unsigned long long* word, unsigned long long tag, int count) {
+    unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word);
+    while (true) {
+        const int n = (seen >> 16) == tag ? (int)(seen & 0xffff) : 0;
+        const unsigned long long next = n + 1 == count ? 0ull : (tag << 16) | (unsigned)(n + 1);
+        const unsigned long long old = atomicCAS(word, seen, next);
+        if (old == seen) return n + 1 == count;
+        seen = old;
+    }
+}
+
+// Where a CTA starts.
+struct FwdShare {
+    const FwdTile* tile;       // by unit
+    long long W, chunk, base;  // positions in all and per CTA; first position of unit u
+    int u;
+    __device__ __forceinline__ void read(const FwdPlan& p, int cta) {
+        tile = p.tile;
+        W = p.head[0];
+        chunk = p.head[1];
+        u = chunk * cta < W ? p.start[cta] : 0;
+        base = chunk * cta < W ? p.base[u] : 0;
+    }
+};
+
 // A CTA's walk over its positions: segments (unit, head, key tiles [j0, j1)).
 struct FwdWalk {
     long long item, start, end, chunk;  // first position of the item's tiles; the CTA's positions
     int u, hd, j0, j1, cc, heads, overhead;
     FwdTile t;
-    __device__ __forceinline__ void load(const FwdPlan& p) {
-        const int4* r = reinterpret_cast<const int4*>(p.tile + u);
+    const FwdTile* tile;
+    __device__ __forceinline__ void load() {
+        const int4* r = reinterpret_cast<const int4*>(tile + u);
         const int4 a = r[0], b = r[1];
         t.n = a.x, t.q_tok = a.y, t.n_tok = a.z, t.pos0 = a.w;
         t.k_base = b.x, t.S_k = b.y, t.n_first = b.z, t.n_cnt = b.w;
@@ -129,28 +167,27 @@ struct FwdWalk {
         j1 = end - item < cc ? (int)(end - item) : cc;
         return true;
     }
-    __device__ __forceinline__ bool init(const FwdPlan& p, int cta, int heads_, int overhead_) {
+    __device__ __forceinline__ bool init(const FwdShare& s, int cta, int heads_, int overhead_) {
         heads = heads_;
         overhead = overhead_;
-        const long long W = p.head[0];
-        chunk = p.head[1];
+        chunk = s.chunk;
         start = chunk * cta;
-        end = start + chunk < W ? start + chunk : W;
+        end = start + chunk < s.W ? start + chunk : s.W;
         if (start >= end) return false;
-        u = p.start[cta];
-        load(p);
-        const long long base = p.base[u];
-        hd = (int)((start - base) / (cc + overhead));
-        item = base + (long long)hd * (cc + overhead) + overhead;
+        tile = s.tile;
+        u = s.u;
+        load();
+        hd = (int)((start - s.base) / (cc + overhead));
+        item = s.base + (long long)hd * (cc + overhead) + overhead;
         return cut();
     }
-    __device__ __forceinline__ bool next(const FwdPlan& p) {
+    __device__ __forceinline__ bool next() {
         item += cc;
         if (item >= end) return false;  // the next item's first position
         if (++hd == heads) {
             hd = 0;
             ++u;
-            load(p);
+            load();
         }
         item += overhead;
         return cut();
@@ -163,6 +200,197 @@ struct FwdWalk {
         count = (int)((item + cc - 1) / chunk) - first + 1;
     }
 };
+
+// ---------------------------------------------------------------- planning, device side
+// (here for the plan kernels and for the CTAs that plan for themselves)
+template <typename V>
+__device__ __forceinline__ V warp_incl_scan(V v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const V u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Exclusive scan over the block; *total gets the block's sum.  sums: 33 values.  Ends with a barrier.
+template <typename V>
+__device__ __forceinline__ V block_excl_scan(V v, V* sums, V* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
+    const V incl = warp_incl_scan(v);
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const V s = lane < warps ? sums[lane] : V(0);
+        const V si = warp_incl_scan(s);
+        sums[lane] = si - s;
+        if (lane == 31) sums[32] = si;
+    }
+    __syncthreads();
+    const V r = sums[warp] + incl - v;
+    *total = sums[32];
+    __syncthreads();
+    return r;
+}
+
+struct Seq {
+    int q0, nq, k0, nk;
+};
+
+// Lengths of sequence n; false (and empty) if they do not fit the tensors.
+__device__ __forceinline__ bool seq_at(const PackedFwd& a, int n, Seq& s) {
+    const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1];
+    bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T_q;
+    s.q0 = q0;
+    s.nq = ok ? q1 - q0 : 0;
+    if (a.cu_k != nullptr) {
+        const int k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
+        const bool okk = k0 >= 0 && k1 >= k0 && k1 <= a.T_k;
+        s.k0 = k0;
+        s.nk = okk ? k1 - k0 : 0;
+        ok = ok && okk;
+    } else {
+        const int nk = a.seq_lens[n];
+        // longer than its table, or than positions are kept for, is refused
+        const bool okk = nk >= 0 && nk <= (1 << 28) && nk <= (long long)a.max_pages * a.page_size;
+        s.k0 = 0;
+        s.nk = okk ? nk : 0;
+        ok = ok && okk;
+    }
+    return ok;
+}
+
+// Largest n with first[n] <= u (first is non-decreasing, first[N] > u).
+__device__ __forceinline__ int find_seq(const int* first, int N, int u) {
+    int lo = 0, hi = N;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Unit `i` of sequence n; its positions per head.
+__device__ __forceinline__ int make_tile(const PackedFwd& a, const FwdGeom& g, int n, int i, FwdTile& t) {
+    Seq s;
+    seq_at(a, n, s);
+    const int i0 = i * g.tpt;
+    t.n = n;
+    t.q_tok = s.q0 + i0;
+    t.n_tok = min(g.tpt, s.nq - i0);
+    t.pos0 = i0 + s.nk - s.nq;
+    t.k_base = s.k0;
+    t.S_k = s.nk;
+    Shape sh;
+    sh.S_q = s.nq;
+    sh.S_k = s.nk;
+    sh.causal = a.causal;
+    sh.window = a.window;
+    int lo, hi;
+    key_range(sh, i0, i0 + t.n_tok, lo, hi);
+    t.n_first = hi > lo ? lo / g.bn : 0;
+    t.n_cnt = hi > lo ? (hi + g.bn - 1) / g.bn - t.n_first : 0;
+    return max(t.n_cnt, 1) + g.overhead;
+}
+
+__device__ __forceinline__ long long share_of(long long W, const FwdGeom& g) {
+    const long long c = (W + g.ctas - 1) / g.ctas;
+    return c < g.min_chunk ? g.min_chunk : c;
+}
+
+// Rows before the first and behind the last sequence: O = 0, LSE = -inf.
+template <typename T>
+__device__ __forceinline__ void fill_rows(const PackedFwd& a, long long first, long long step) {
+    const int lo = a.cu_q[0], hi = a.cu_q[a.N];
+    if (lo < 0 || hi < lo || hi > a.T_q) return;  // reported with the plan
+    const int per = a.d * (int)sizeof(T) / 16;
+    const long long n = (long long)(lo + a.T_q - hi) * a.H * per;
+    for (long long e = first; e < n; e += step) {
+        const long long r = e / per;
+        const int t = (int)(r / a.H), h = (int)(r % a.H), c = (int)(e % per);
+        const int tok = t < lo ? t : t - lo + hi;
+        T* dst = static_cast<T*>(a.O) + tok * a.o.tok + h * a.o.head + c * (16 / (int)sizeof(T));
+        *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        if (c == 0) a.LSE[(size_t)h * a.T_q + tok] = -INFINITY;
+    }
+}
+
+// Scratch of plan_self in shared memory.
+struct SelfPlan {
+    long long lsum[33];
+    FwdShare share;
+    int isum[33];
+    int first[kSelfUnits + 1];
+};
+
+// The plan kernel's work, done by every CTA (kThreads threads) for itself: the same plan, of
+// which it keeps the units that hold its positions.  Reads a few KB of lengths; saves a launch.
+template <int kThreads>
+__device__ __forceinline__ void plan_self(const PackedFwd& a, const FwdGeom& g, const FwdPlan& p, int max_units,
+                                          SelfPlan* s) {
+    constexpr int kPer = kSelfUnits / kThreads;
+    static_assert(kPer * kThreads == kSelfUnits, "units per thread");
+    const int tid = threadIdx.x, cta = blockIdx.x;
+    bool bad = false;
+    int units[kPer], sum = 0, U;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int n = tid * kPer + i;
+        Seq q = {0, 0, 0, 0};
+        if (n < a.N && !seq_at(a, n, q)) bad = true;
+        units[i] = (q.nq + g.tpt - 1) / g.tpt;
+        sum += units[i];
+    }
+    int at = block_excl_scan(sum, s->isum, &U);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int n = tid * kPer + i;
+        if (n < a.N) s->first[n] = at;
+        at += units[i];
+    }
+    if (tid == 0) s->first[a.N] = U;
+    if (__syncthreads_or(bad)) {  // lengths that do not fit the tensors: nothing is computed
+        if (tid == 0 && cta == 0) atomicOr(a.err, kErrLengths);
+        U = 0;
+    }
+    FwdTile t[kPer];
+    long long cost[kPer], all = 0, W;
+    int n = tid * kPer < U ? find_seq(s->first, a.N, tid * kPer) : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int u = tid * kPer + i;
+        cost[i] = 0;
+        if (u < U) {
+            while (s->first[n + 1] <= u) ++n;
+            cost[i] = (long long)make_tile(a, g, n, u - s->first[n], t[i]) * g.heads;
+        }
+        all += cost[i];
+    }
+    long long base = block_excl_scan(all, s->lsum, &W);
+    const long long chunk = share_of(W, g);
+    const long long lo = chunk * cta, hi = lo + chunk;
+    FwdTile* mine = p.tile + (size_t)cta * max_units;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int u = tid * kPer + i;
+        if (u < U && base < hi && base + cost[i] > lo) mine[u] = t[i];
+        if (u < U && base <= lo && base + cost[i] > lo) {
+            s->share.u = u;
+            s->share.base = base;
+        }
+        base += cost[i];
+    }
+    if (tid == 0) {
+        s->share.tile = mine;
+        s->share.W = W;
+        s->share.chunk = chunk;
+    }
+    __syncthreads();
+}
 
 // packed_plan.cu
 cudaError_t launch_fwd_plan(const PackedFwd& a, const FwdGeom& g, const FwdPlan& p, cudaStream_t st);
@@ -234,6 +462,19 @@ __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p,
     }
 }
 
+// Raises a kernel's shared-memory limit once per device; `ready` has a bit per device.
+template <typename K>
+inline cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 // Forward launchers: with ws == nullptr only *bytes (the workspace they need) is set.
 // packed_fwd.cu: tensor cores (f16 / bf16)
 cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
@@ -270,20 +511,36 @@ struct alignas(16) KeyTile {
     int its;    // query tiles that see a key of this tile
     int pad;
 };
+// What one CTA does of a key tile (for one key/value head): share `part` of `parts` of its
+// (query tile, query head) iterations.  A tile with more iterations than an even share of the
+// whole call over the SMs is cut: its parts leave fp32 sums of dK and dV in slots `slot` on,
+// which the pass after the main kernel adds up in order.
+struct alignas(16) KeyWork {
+    int tile, part, parts, slot;
+};
 
 struct BwdPlan {
-    long long* head;      // [0] query tiles, [1] key tiles
+    long long* head;      // [0] query tiles, [1] works, [2] cut key tiles
     QueryTile* query;     // [max_units]
     KeyTile* key;         // [max_keys], in sequence order
-    int* order;           // [max_keys] key tiles, most query tiles first
+    KeyWork* work;        // [max_work], longest first (deterministic: in order of the tiles)
+    KeyWork* cut;         // [max_cut] tiles with more than one part (slot: the first part's)
+    float* part;          // [max_slots][H_kv][2: dV, dK][128][d] fp32 sums of the parts
     int *seq_q, *seq_k;   // [N + 1] first query / key tile of each sequence
     CUtensorMap* maps;    // [N][4] of each sequence: Q, dO, K, V (tensor-core kernel)
     unsigned *sem, *ticket;  // deterministic: turn counters [H][max_units], start-order ticket
     float *lse2, *D;      // [H][rows]
     float* dqacc;         // [rows][H][d] fp32, not scaled
     long long rows;       // max_units * 128
-    int max_units, max_keys;
+    int max_units, max_keys, max_work, max_cut, max_slots;
+    int shares;           // CTAs the iterations are spread over
+    int min_its;          // iterations a part has at least
 };
+
+int sm_count();  // of the current device (looked up once per device)
+
+// CTAs that share the work of one plan tile and head on CUDA cores (by their key rows).
+inline int simt_pieces(int d) { return d <= 128 ? 2 : 4; }
 
 inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, BwdPlan* p) {
     char* b = static_cast<char*>(ws);
@@ -297,12 +554,22 @@ inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, B
     q.max_units = a.T_q / kBwdTile + (a.N < a.T_q ? a.N : a.T_q);
     q.max_keys = a.T_k / kBwdTile + (a.N < a.T_k ? a.N : a.T_k);
     q.rows = (long long)q.max_units * kBwdTile;
+    // with x = iterations / share of a tile, the tiles' x add up to shares / H_kv per head at
+    // most, a cut tile has x > 1 and ceil(x) <= 2x parts.  On CUDA cores a plan tile is several
+    // CTAs and a CTA's fixed cost is small: two rounds of CTAs even out better.
+    q.shares = tensor_cores ? sm_count() : (2 * sm_count() + simt_pieces(a.d) - 1) / simt_pieces(a.d);
+    q.min_its = 4;
+    q.max_cut = q.shares / a.H_kv + 1;
+    q.max_work = q.max_keys + q.max_cut;
+    q.max_slots = 2 * q.max_cut;
     q.head = reinterpret_cast<long long*>(take(16));
     q.ticket = reinterpret_cast<unsigned*>(take(4));
     q.sem = reinterpret_cast<unsigned*>(take(a.deterministic ? (size_t)a.H * q.max_units * 4 : 0));
     q.query = reinterpret_cast<QueryTile*>(take((size_t)q.max_units * sizeof(QueryTile)));
     q.key = reinterpret_cast<KeyTile*>(take((size_t)q.max_keys * sizeof(KeyTile)));
-    q.order = reinterpret_cast<int*>(take((size_t)q.max_keys * 4));
+    q.work = reinterpret_cast<KeyWork*>(take((size_t)q.max_work * sizeof(KeyWork)));
+    q.cut = reinterpret_cast<KeyWork*>(take((size_t)q.max_cut * sizeof(KeyWork)));
+    q.part = reinterpret_cast<float*>(take((size_t)q.max_slots * a.H_kv * 2 * kBwdTile * a.d * 4));
     q.seq_q = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
     q.seq_k = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
     q.maps = reinterpret_cast<CUtensorMap*>(take(tensor_cores ? (size_t)a.N * 4 * sizeof(CUtensorMap) : 0));
@@ -335,15 +602,21 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 int packed_take_error_word(unsigned int* word);
 
 // ---------------------------------------------------------------- page lookup
-// Page that holds key j of a request, or `pages` (one past the cache, which TMA reads as zeros
-// and the CUDA-core kernel skips) with *bad set when the table's entry is not a page.
-__host__ __device__ __forceinline__ int page_of(const int* row, int j, int page_size, int max_pages, int pages,
-                                                bool* bad) {
+// The table's entry for key j of a request (-1 behind the table's last column) ...
+__host__ __device__ __forceinline__ int page_entry(const int* row, int j, int page_size, int max_pages) {
     const int e = j / page_size;
-    const int id = e < max_pages ? row[e] : -1;
+    return e < max_pages ? row[e] : -1;
+}
+// ... and the page it names, or `pages` (one past the cache, which TMA reads as zeros and the
+// CUDA-core kernel skips) with *bad set when the entry is not a page.
+__host__ __device__ __forceinline__ int page_checked(int id, int pages, bool* bad) {
     if (id >= 0 && id < pages) return id;
     *bad = true;
     return pages;
+}
+__host__ __device__ __forceinline__ int page_of(const int* row, int j, int page_size, int max_pages, int pages,
+                                                bool* bad) {
+    return page_checked(page_entry(row, j, page_size, max_pages), pages, bad);
 }
 
 }  // namespace fa

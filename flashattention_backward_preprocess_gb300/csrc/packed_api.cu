@@ -2,6 +2,7 @@
 // argument checks, the choice of kernel, and the device word in which their kernels record
 // what only the device can see (lengths, pages, timeouts).
 #include <math.h>
+#include <time.h>
 
 #include <mutex>
 #include <string>
@@ -132,6 +133,26 @@ int run_fwd(PackedFwd& a, void* ws, size_t ws_bytes, cudaStream_t st) {
 
 }  // namespace
 
+int sm_count() {
+    static std::atomic<int> sms[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+        sms[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+unsigned long long next_tag() {
+    static std::atomic<unsigned long long> last{(unsigned long long)time(nullptr) << 20};
+    unsigned long long t;
+    do t = (last.fetch_add(1, std::memory_order_relaxed) + 1) & ((1ull << 48) - 1);
+    while (t == 0);
+    return t;
+}
+
 int packed_take_error_word(unsigned int* word) {
     *word = 0;
     int dev = 0;
@@ -235,7 +256,7 @@ int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, c
                                     std::to_string(workspace ? workspace_bytes : 0));
     if ((rc = check_ptr(workspace, "workspace", 256))) return rc;
     // the largest grid is one CTA per 16 rows of a query tile or per piece of a key tile and head
-    if ((double)p.max_units * 8 > 2.0e9 || (double)p.max_keys * H_kv * 4 > 2.0e9 || H > 65535)
+    if ((double)p.max_units * 8 > 1.0e9 || (double)p.max_work * H_kv * 4 > 1.0e9 || H > 65535)
         return bad("shape", "tensor too large");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_bwd_plan(a, p, tc, st);

@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
     }
     if (blk / a.H_kv >= p.plan.head[1]) return;
     const int hk = blk % a.H_kv;
-    const KeyTile kt = p.plan.key[kDet ? blk / a.H_kv : p.plan.order[blk / a.H_kv]];
+    const KeyWork work = p.plan.work[blk / a.H_kv];
+    const KeyTile kt = p.plan.key[work.tile];
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
     auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
@@ -213,8 +214,10 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
     query_range(sh, n0, min(n0 + BN, S_k), q_lo, q_hi);
     const int m_start = q_lo / BM;
     const int m_end = q_hi > q_lo ? (q_hi + BM - 1) / BM : m_start;
-    const int nm = m_end - m_start;
-    const int n_it = g * nm;
+    // this CTA's iterations it0 .. it0 + n_it - 1 of the tile's (all of them unless it is cut)
+    const int all_it = g * (m_end - m_start);
+    const int it0 = (int)((long long)all_it * work.part / work.parts);
+    const int n_it = (int)((long long)all_it * (work.part + 1) / work.parts) - it0;
     // tensor maps of this sequence alone: rows past its ends read as zeros
     const CUtensorMap* tmQ = p.plan.maps + (size_t)kt.n * 4;
     const CUtensorMap *tmdO = tmQ + 1, *tmK = tmQ + 2, *tmV = tmQ + 3;
@@ -236,8 +239,8 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
     auto dt = [](int i) { return NDS == 2 ? (i & 1) : 0; };
 
     auto iter_coords = [&](int it, int& h, int& m0) {
-        h = hk * g + it % g;
-        m0 = (m_end - 1 - it / g) * BM;
+        h = hk * g + (it0 + it) % g;
+        m0 = (m_end - 1 - (it0 + it) / g) * BM;
     };
     auto acc_row = [&](int m0) { return kt.unit0 * BM + m0; };  // of the accumulator, D and LSE
     // Bulk reduce-adds of the dQ tile staged for iteration it (one thread), then the
@@ -615,10 +618,12 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
             ptx::tc_fence_after();
             T* dVrow = static_cast<T*>(a.dV) + (long long)(kt.k_tok + t) * a.sdv.tok + (long long)hk * a.sdv.head;
             T* dKrow = static_cast<T*>(a.dK) + (long long)(kt.k_tok + t) * a.sdk.tok + (long long)hk * a.sdk.head;
+            float* part_row = p.plan.part + (((size_t)work.slot * a.H_kv + hk) * 2 * BN + t) * a.d;
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {
                 const int c = hf * (D / 64) + cc;  // 32-column chunk
                 uint32_t rv[32], rk[32];
+                __syncwarp();
                 if (n_it > 0) {
                     ptx::tmem_ld32p(tmem + C::TM_DV + lane_off + c * 32, rv);
                     ptx::tmem_ld32p(tmem + C::TM_DK + lane_off + c * 32, rk);
@@ -626,6 +631,18 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) rv[k] = rk[k] = 0u;
+                }
+                if (work.parts > 1) {  // one part's sums, added up by the last pass
+                    if (row_valid && c * 32 < a.d) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            *reinterpret_cast<uint4*>(part_row + c * 32 + u * 4) =
+                                make_uint4(rv[4 * u], rv[4 * u + 1], rv[4 * u + 2], rv[4 * u + 3]);
+                            *reinterpret_cast<uint4*>(part_row + (size_t)BN * a.d + c * 32 + u * 4) =
+                                make_uint4(rk[4 * u], rk[4 * u + 1], rk[4 * u + 2], rk[4 * u + 3]);
+                        }
+                    }
+                    continue;
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -776,10 +793,11 @@ cudaError_t launch_t(const PackedBwd& a, const BwdPlan& plan, cudaStream_t st) {
     p.plan = plan;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     auto kern = a.deterministic ? packed_bwd_kernel<T, D, true> : packed_bwd_kernel<T, D, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    static std::atomic<uint64_t> ready[2];
+    cudaError_t e = allow_smem(kern, (int)C::SMEM, ready[a.deterministic ? 1 : 0]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(plan.max_keys * a.H_kv));
+    cfg.gridDim = dim3((unsigned)(plan.max_work * a.H_kv));
     cfg.blockDim = dim3(threads_for(a.deterministic != 0, D));
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;

@@ -76,9 +76,65 @@ __global__ void __launch_bounds__(kThreads) packed_preprocess_kernel(const Packe
     }
 }
 
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float4*>(p);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const T* t = reinterpret_cast<const T*>(&u);
+        return make_float4(TypeTraits<T>::to_f32(t[0]), TypeTraits<T>::to_f32(t[1]), TypeTraits<T>::to_f32(t[2]),
+                           TypeTraits<T>::to_f32(t[3]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float x, float y, float z, float w) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+    } else {
+        alignas(8) T t[4] = {TypeTraits<T>::from_f32(x), TypeTraits<T>::from_f32(y), TypeTraits<T>::from_f32(z),
+                             TypeTraits<T>::from_f32(w)};
+        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
+    }
+}
+
+constexpr int kCutBlocks = 8;  // blocks per cut key tile and head
+
+// dK and dV of a cut key tile: its parts' sums, added in order.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedBwd a, const BwdPlan p) {
+__device__ void join_cut(const PackedBwd& a, const BwdPlan& p, int b) {
+    constexpr int C4 = D / 4, kRows = kBwdTile / kCutBlocks;
+    const int i = b / kCutBlocks / a.H_kv, hk = b / kCutBlocks % a.H_kv;
+    if (i >= p.head[2]) return;
+    const KeyWork w = p.cut[i];
+    const KeyTile kt = p.key[w.tile];
+    const int r0 = b % kCutBlocks * kRows, rows = min(kRows, min(kBwdTile, kt.S_k - kt.n0) - r0);
+    const size_t step = (size_t)a.H_kv * 2 * kBwdTile * D;  // from a part to the next
+    for (int e = threadIdx.x; e < rows * 2 * C4; e += kThreads) {
+        const int c = e % C4, which = e / C4 % 2, r = r0 + e / (2 * C4);
+        const float4* s = reinterpret_cast<const float4*>(
+                              p.part + (((size_t)w.slot * a.H_kv + hk) * 2 + which) * kBwdTile * D + (size_t)r * D) + c;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < w.parts; ++k) {
+            const float4 y = __ldcs(s + k * (step / 4));
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const float f = which ? a.scale : 1.f;
+        const RowStride str = which ? a.sdk : a.sdv;
+        T* dst = static_cast<T*>(which ? a.dK : a.dV) + (long long)(kt.k_tok + r) * str.tok + (long long)hk * str.head;
+        store4<T>(dst + 4 * c, x.x * f, x.y * f, x.z * f, x.w * f);
+    }
+}
+
+// Blocks [0, dq_blocks): dQ rows; the rest: cut key tiles.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedBwd a, const BwdPlan p, int dq_blocks) {
     ptx::griddep_wait();
+    if ((int)blockIdx.x >= dq_blocks) {
+        join_cut<T, D>(a, p, blockIdx.x - dq_blocks);
+        return;
+    }
     constexpr int C8 = D / 8;  // 8-column groups per row
     const int u = blockIdx.x / (kBwdTile / kRowsPerBlock);
     if (u >= p.head[0]) return;
@@ -117,28 +173,6 @@ struct SCfg {
     static constexpr size_t SMEM = sizeof(float) * ((size_t)(2 * BN + 2 * BM) * LD + 2 * BM * LP + 2 * BM);
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p) {
-    if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float4*>(p);
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        const T* t = reinterpret_cast<const T*>(&u);
-        return make_float4(TypeTraits<T>::to_f32(t[0]), TypeTraits<T>::to_f32(t[1]), TypeTraits<T>::to_f32(t[2]),
-                           TypeTraits<T>::to_f32(t[3]));
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float x, float y, float z, float w) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
-    } else {
-        alignas(8) T t[4] = {TypeTraits<T>::from_f32(x), TypeTraits<T>::from_f32(y), TypeTraits<T>::from_f32(z),
-                             TypeTraits<T>::from_f32(w)};
-        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
-    }
-}
-
 // rows [0, n) of a tile (row stride `ld` elements) into a padded fp32 shared tile; zeros behind
 template <typename T, int D>
 __device__ __forceinline__ void stage_rows(float* dst, const T* src, long long ld, int n, int rows) {
@@ -154,7 +188,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedBwd a, const BwdPlan p) {
     using C = SCfg<D>;
     constexpr int BN = C::BN, BM = C::BM, LD = C::LD, LP = C::LP, TR = C::TR, TC = C::TC, NG = C::NG;
-    constexpr int kPieces = kBwdTile / BN;  // CTAs per plan tile and head
+    constexpr int kPieces = kBwdTile / BN;  // CTAs per work and head (simt_pieces)
     extern __shared__ float4 smem4[];
     float* smem = reinterpret_cast<float*>(smem4);
     float* sK = smem;
@@ -170,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int item = blockIdx.x / kPieces;
     if (item / a.H_kv >= p.head[1]) return;
-    const KeyTile kt = p.key[p.order[item / a.H_kv]];
+    const KeyWork work = p.work[item / a.H_kv];
+    const KeyTile kt = p.key[work.tile];
     const int hk = item % a.H_kv, g = a.H / a.H_kv;
     const int sub = (blockIdx.x % kPieces) * BN;  // this CTA's rows within the plan tile
     const int n0 = kt.n0 + sub, S_q = kt.S_q, S_k = kt.S_k;
@@ -202,7 +237,10 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
     const int nq = i_end > i_begin ? (i_end - m_first + BM - 1) / BM : 0;
     const long long q_tok0 = nq > 0 ? p.query[kt.unit0].q_tok : 0;  // first query row of the sequence
     const long long row0 = (long long)kt.unit0 * kBwdTile;          // and in the padded rows
-    for (int it = 0; it < g * nq; ++it) {
+    // this CTA's share of the iterations (all of them unless the tile is cut)
+    const int it_lo = (int)((long long)g * nq * work.part / work.parts);
+    const int it_hi = (int)((long long)g * nq * (work.part + 1) / work.parts);
+    for (int it = it_lo; it < it_hi; ++it) {
         const int h = hk * g + it / nq;
         const int m0 = m_first + (it % nq) * BM;
         const int rows = min(BM, S_q - m0);
@@ -344,10 +382,16 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
         if (rr >= krows) continue;
         T* dV = static_cast<T*>(a.dV) + (long long)(kt.k_tok + sub + rr) * a.sdv.tok + (long long)hk * a.sdv.head;
         T* dK = static_cast<T*>(a.dK) + (long long)(kt.k_tok + sub + rr) * a.sdk.tok + (long long)hk * a.sdk.head;
+        float* part = p.part + (((size_t)work.slot * a.H_kv + hk) * 2 * kBwdTile + sub + rr) * D;
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
             const int f = tx + 16 * q;
             if (!(NG * 16 * 4 == D || f < D / 4)) continue;
+            if (work.parts > 1) {  // one part's sums, added up by the last pass
+                store4<float>(part + 4 * f, accV[r][q][0], accV[r][q][1], accV[r][q][2], accV[r][q][3]);
+                store4<float>(part + kBwdTile * D + 4 * f, accK[r][q][0], accK[r][q][1], accK[r][q][2], accK[r][q][3]);
+                continue;
+            }
             store4<T>(dV + 4 * f, accV[r][q][0], accV[r][q][1], accV[r][q][2], accV[r][q][3]);
             store4<T>(dK + 4 * f, accK[r][q][0] * a.scale, accK[r][q][1] * a.scale, accK[r][q][2] * a.scale,
                       accK[r][q][3] * a.scale);
@@ -470,25 +514,25 @@ cudaError_t preprocess_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) 
 
 template <typename T, int D>
 cudaError_t dq_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
-    return launch_pdl(packed_dq_kernel<T, D>, (long long)p.max_units * (kBwdTile / kRowsPerBlock), kThreads, st, a, p);
+    const int dq = p.max_units * (kBwdTile / kRowsPerBlock);
+    return launch_pdl(packed_dq_kernel<T, D>, dq + (long long)p.max_cut * a.H_kv * kCutBlocks, kThreads, st, a, p, dq);
 }
 
 template <typename T, int D>
 cudaError_t bwd_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
     using C = SCfg<D>;
+    static std::atomic<uint64_t> ready[2];
     cudaError_t e;
     if (p.max_keys > 0) {
         auto kern = packed_bwd_simt_kernel<T, D>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-        if (e != cudaSuccess) return e;
-        kern<<<(unsigned)((long long)p.max_keys * a.H_kv * (kBwdTile / C::BN)), kThreads, C::SMEM, st>>>(a, p);
+        if ((e = allow_smem(kern, (int)C::SMEM, ready[0])) != cudaSuccess) return e;
+        kern<<<(unsigned)((long long)p.max_work * a.H_kv * (kBwdTile / C::BN)), kThreads, C::SMEM, st>>>(a, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (a.deterministic && p.max_units > 0) {
         const size_t smem = sizeof(float) * (2 * kDqRows * D + 2 * kDqKeys * D + kDqRows * kDqKeys);
         auto kern = packed_dq_simt_kernel<T, D>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
+        if ((e = allow_smem(kern, (int)smem, ready[1])) != cudaSuccess) return e;
         kern<<<dim3((unsigned)(p.max_units * (kBwdTile / kDqRows)), (unsigned)a.H), kDqThreads, smem, st>>>(a, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -506,7 +550,6 @@ cudaError_t launch_packed_preprocess(const PackedBwd& a, const BwdPlan& p, cudaS
 }
 
 cudaError_t launch_packed_dq(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
-    if (p.max_units == 0) return cudaSuccess;
 #define FA_L(T, DD) return dq_t<T, DD>(a, p, st)
     FA_DISPATCH_HEAD_DIM(a.dtype, a.d, FA_L);
 #undef FA_L

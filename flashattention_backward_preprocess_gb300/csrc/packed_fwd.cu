@@ -58,8 +58,6 @@ struct PCfg {
     static constexpr uint32_t OFF_V = OFF_K + STAGES * kTileKV_B;
     static constexpr uint32_t OFF_BAR = OFF_V + STAGES * kTileKV_B;
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
-    // boxes of one K / V tile per producer lane (pages of 8 rows are the smallest)
-    static constexpr int PIECES = (BN / 8 * 2 * BOXES + 31) / 32;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
 
@@ -106,12 +104,32 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
                  : "memory");
 }
 
-template <typename T, int D, bool kPaged>
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            int c4, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+
+// kPaged: K / V from a cache.  kGroup (paged, d a whole multiple of 64 and above 64): one box
+// per page and tensor brings all its columns, so a tile lies in shared memory as groups of 8
+// rows, each with its 64-column blocks one after another, instead of one block of all rows
+// after another.  Small boxes are what bounds a cache of small pages (about 60 ns a box,
+// whatever it holds): with pages of 16 rows the 64 x 4096-token step took 253 us with a box
+// per 64 columns.
+template <typename T, int D, bool kPaged, bool kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const PackedFwd a, const FwdPlan plan, int tpt, int overhead) {
+                      const __grid_constant__ CUtensorMap tmV, const PackedFwd a, const FwdPlan plan, const FwdGeom geo, int max_units) {
     using C = PCfg<D>;
     constexpr int BN = C::BN, NB = C::NBUF;
+    // K / V tile layout: bytes from a 64-column block to the next, and from 8 rows to the next 8
+    constexpr uint32_t kBlk = kGroup ? 1024 : C::kBoxKV_B;
+    constexpr uint32_t kRow8 = kGroup ? 1024 * C::BOXES : 1024;
+    constexpr int kPerPage = kGroup ? 2 : 2 * C::BOXES;      // boxes per page
+    constexpr int kPieces = (BN / 8 * kPerPage + 31) / 32;  // and tile per producer lane (pages of 8 rows)
     constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
     constexpr int kNumBars = P_STAGE0 + 2 * C::STAGES;
     constexpr uint32_t OFF_MISC = C::OFF_BAR + kNumBars * 8;
@@ -143,7 +161,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    ptx::griddep_wait();  // the plan
+    ptx::griddep_wait();  // the plan, or with it the lengths
+    FwdShare share;
+    if (geo.self) {
+        SelfPlan* sp = reinterpret_cast<SelfPlan*>(smem + C::OFF_K);  // before any tile lands there
+        plan_self<kThreads>(a, geo, plan, max_units, sp);
+        share = sp->share;
+        ptx::fence_proxy_async_smem();
+        if (a.fill) fill_rows<T>(a, blockIdx.x * kThreads + threadIdx.x, (long long)gridDim.x * kThreads);
+        __syncthreads();
+    } else {
+        share.read(plan, blockIdx.x);
+    }
 
     // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
     // CTA (jg), per-item ones its segments with work (ka).
@@ -154,32 +183,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // own boxes of a K / V tile.
         if (!*abort_flag) {
             FwdWalk wq, wk;
-            bool q_more = wq.init(plan, blockIdx.x, a.H_kv, overhead),
-                 kv_more = wk.init(plan, blockIdx.x, a.H_kv, overhead);
-            while (q_more && wq.tiles() == 0) q_more = wq.next(plan);
-            while (kv_more && wk.tiles() == 0) kv_more = wk.next(plan);
+            bool q_more = wq.init(share, blockIdx.x, a.H_kv, geo.overhead),
+                 kv_more = wk.init(share, blockIdx.x, a.H_kv, geo.overhead);
+            while (q_more && wq.tiles() == 0) q_more = wq.next();
+            while (kv_more && wk.tiles() == 0) kv_more = wk.next();
             int q_act = 0, jg = 0, kj = kv_more ? wk.j0 : 0;
             const int pr = kPaged ? min(a.page_size, BN) : BN;  // rows per box
-            int page[C::PIECES];                                // paged: page of this lane's boxes of the next tile
+            // paged: table entries of this lane's boxes of the next tile.  They are only loaded here
+            // and looked at when the tile is issued, so the load's latency passes meanwhile.
+            int page[kPieces];
+            int live = 0;  // boxes of that tile that hold a key
             uint32_t bytes = 2 * C::kTileKV_B;
             auto look_up = [&]() {
                 if constexpr (kPaged) {
                     const int n0 = (wk.t.n_first + kj) * BN;
-                    const int live = min((wk.t.S_k - n0 + pr - 1) / pr, BN / pr);  // boxes that hold a key
+                    live = min((wk.t.S_k - n0 + pr - 1) / pr, BN / pr);
                     bytes = (uint32_t)(live * pr) * 128u * 2u * C::BOXES;
                     const int* row = a.table + (size_t)wk.t.n * a.max_pages;
-                    // keys before the window of the unit's first row may have lost their pages:
-                    // they are masked, and read as zeros (page `pages`) without a look-up
-                    const int k_lo = a.window > 0 ? wk.t.pos0 - a.window + 1 : 0;
-                    bool bad = false;
 #pragma unroll
-                    for (int i = 0; i < C::PIECES; ++i) {
-                        const int b = (lane + 32 * i) / (2 * C::BOXES), j = n0 + b * pr;
-                        page[i] = b >= live         ? -1
-                                  : j + pr <= k_lo ? a.pages
-                                                    : page_of(row, j, a.page_size, a.max_pages, a.pages, &bad);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int b = (lane + 32 * i) / kPerPage;
+                        page[i] = b < live ? page_entry(row, n0 + b * pr, a.page_size, a.max_pages) : -1;
                     }
-                    if (bad) atomicOr(err, kErrPage);
                 }
             };
             if (kv_more) look_up();
@@ -196,13 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 act = __shfl_sync(0xffffffffu, act, 0);
                 if (act & 1) {
                     if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(tpt * g) * 128u * C::BOXES);
+                        ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(geo.tpt * g) * 128u * C::BOXES);
                         for (int x = 0; x < C::BOXES; ++x)
                             ptx::tma_load_3d(sbase + C::OFF_Q + x * C::kBoxQ_B, &tmQ, x * 64, wq.hd * g, wq.t.q_tok,
                                              bar(P_Q));
                     }
                     ++q_act;
-                    do q_more = wq.next(plan);
+                    do q_more = wq.next();
                     while (q_more && wq.tiles() == 0);
                 }
                 if (act & 2) {
@@ -211,15 +236,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full(s), bytes);
                     __syncwarp();
                     if constexpr (kPaged) {
+                        // keys before the window of the unit's first row may have lost their pages:
+                        // they are masked, and read as zeros (page `pages`) whatever the table says
+                        const int k_lo = a.window > 0 ? wk.t.pos0 - a.window + 1 : 0;
+                        bool bad = false;
 #pragma unroll
-                        for (int i = 0; i < C::PIECES; ++i) {
-                            const int e = lane + 32 * i, b = e / (2 * C::BOXES), x = (e >> 1) % C::BOXES;
-                            if (b < BN / pr && page[i] >= 0)
-                                tma_load_4d(sbase + ((e & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B +
-                                                x * C::kBoxKV_B + b * pr * 128,
-                                            (e & 1) ? &tmV : &tmK, x * 64, wk.hd, (n0 + b * pr) % a.page_size,
-                                            page[i], bar_full(s));
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int e = lane + 32 * i, b = e / kPerPage;
+                            if (b >= live) continue;
+                            const int pg = n0 + (b + 1) * pr <= k_lo ? a.pages : page_checked(page[i], a.pages, &bad);
+                            const uint32_t dst = sbase + ((e & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B;
+                            const CUtensorMap* map = (e & 1) ? &tmV : &tmK;
+                            const int row = (n0 + b * pr) % a.page_size;
+                            if constexpr (kGroup) {
+                                const long long hs = (e & 1) ? a.v.head : a.k.head;
+                                tma_load_5d(dst + b * pr * (D * 2), map, (int)(wk.hd * hs), 0, 0, row / 8, pg,
+                                            bar_full(s));
+                            } else {
+                                const int x = (e >> 1) % C::BOXES;
+                                tma_load_4d(dst + x * C::kBoxKV_B + b * pr * 128, map, x * 64, wk.hd, row, pg,
+                                            bar_full(s));
+                            }
                         }
+                        if (bad) atomicOr(err, kErrPage);
                     } else if (lane < 2 * C::BOXES) {
                         const int x = lane >> 1;
                         ptx::tma_load_3d(sbase + ((lane & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B +
@@ -228,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ++jg;
                     if (++kj == wk.j1) {
-                        do kv_more = wk.next(plan);
+                        do kv_more = wk.next();
                         while (kv_more && wk.tiles() == 0);
                         kj = wk.j0;
                     }
@@ -269,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             int jg = 0, ka = 0;
             FwdWalk w;
-            bool more = w.init(plan, blockIdx.x, a.H_kv, overhead);
+            bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead);
             if (warp == kWarpMma) {
                 const uint64_t dQ_k = ptx::sw128_desc(sbase + C::OFF_Q, 16, 1024);
-                const uint64_t dK_k = ptx::sw128_desc(sbase + C::OFF_K, 16, 1024);
-                for (; ok && more; more = w.next(plan)) {
+                const uint64_t dK_k = ptx::sw128_desc(sbase + C::OFF_K, 16, kRow8);
+                for (; ok && more; more = w.next()) {
                     const int nt = w.tiles();
                     if (nt == 0) continue;
                     if (!(ok = wait_bar(bar(P_Q), ka & 1, abort_flag, err))) break;
@@ -287,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t kq = (kk / 4) * C::kBoxQ_B + (kk % 4) * 32;
-                            const uint32_t kv = (kk / 4) * C::kBoxKV_B + (kk % 4) * 32;
+                            const uint32_t kv = (kk / 4) * kBlk + (kk % 4) * 32;
                             ptx::mma_ss(tmem + C::TM_S + (jg % NB) * 128, desc_add(dQ_k, kq), desc_add(dK_k, so + kv),
                                         ID_S, kk > 0);
                         }
@@ -300,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every S product is read by a P V product, so all are complete once the other
                 // issuer has drained
             } else {
-                const uint64_t dV_mn = ptx::sw128_desc(sbase + C::OFF_V, C::kBoxKV_B, 1024);
-                for (; ok && more; more = w.next(plan)) {
+                const uint64_t dV_mn = ptx::sw128_desc(sbase + C::OFF_V, kBlk, kRow8);
+                for (; ok && more; more = w.next()) {
                     const int nt = w.tiles();
                     if (nt == 0) continue;
                     for (int j = 0; j < nt; ++j, ++jg) {
@@ -314,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
                             ptx::mma_ts(tmem + C::TM_O, tmem + C::TM_S + (jg % NB) * 128 + kk * 8,
-                                        desc_add(dV_mn, (uint32_t)s * C::kTileKV_B + kk * 2048), ID_PV,
+                                        desc_add(dV_mn, (uint32_t)s * C::kTileKV_B + kk * 2 * kRow8), ID_PV,
                                         (j > 0 || kk > 0) ? 1u : 0u);
                         ptx::mma_commit(bar(P_PV0 + jg % NB));
                         ptx::mma_commit(bar_empty(s));
@@ -338,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = !*abort_flag;
         int jg = 0, ka = 0;
         FwdWalk w;
-        bool more = w.init(plan, blockIdx.x, a.H_kv, overhead);
-        for (; ok && more; more = w.next(plan)) {
+        bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead);
+        for (; ok && more; more = w.next()) {
             const int rows = w.t.n_tok * g;
             const bool row_valid = t < rows;
             const bool warp_live = warp * 32 < rows;
@@ -367,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < C::BOXES; ++x)
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
-                                *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::kTileKV_B + x * C::kBoxKV_B +
-                                                          t * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::kTileKV_B + x * kBlk +
+                                                          (t >> 3) * kRow8 + (t & 7) * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     ptx::fence_proxy_async_smem();
                 }
@@ -506,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w.parts(first, count);
                 __threadfence();
                 ptx::named_bar_sync(kSoftBarrier, 128);
-                if (t == 0) *last_flag = atomicAdd(&plan.done[first], 1u) == (unsigned)(count - 1);
+                if (t == 0) *last_flag = arrive_part(&plan.done[first], plan.tag, count);
                 ptx::named_bar_sync(kSoftBarrier, 128);
                 if (*last_flag) {
                     __threadfence();
@@ -535,14 +574,7 @@ bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, 
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms > 0 ? sms : 148;
-}
-
-template <typename T, int D, bool kPaged>
+template <typename T, int D, bool kPaged, bool kGroup>
 cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     using C = PCfg<D>;
     constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16 + BM * 8;
@@ -557,9 +589,12 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     geo.D = D;
     geo.min_chunk = 2;
     geo.overhead = 3;
+    const long long units = plan_units(a, geo);
+    geo.self = units <= kSelfUnits && a.N <= kSelfUnits;
     FwdPlan plan;
     *bytes = fwd_plan_layout(a, geo, ws, &plan);
     if (ws == nullptr) return cudaSuccess;
+    plan.tag = next_tag();
     const CUtensorMapDataType dt =
         TypeTraits<T>::kId == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tq, tk, tv;
@@ -577,7 +612,16 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
         long long page;
     } kv[2] = {{&tk, a.K, a.k, a.k_page}, {&tv, a.V, a.v, a.v_page}};
     for (int i = 0; i < 2; ++i) {
-        if constexpr (kPaged) {
+        if constexpr (kGroup) {
+            // columns of a head (its offset is part of the column coordinate), 8 rows, 64-column
+            // blocks, groups of 8 rows, pages
+            const cuuint64_t row = (cuuint64_t)kv[i].s.tok * 2;
+            const cuuint64_t dims[5] = {(cuuint64_t)((a.H_kv - 1) * kv[i].s.head + 64), 8, D / 64,
+                                        (cuuint64_t)(a.page_size / 8), (cuuint64_t)a.pages};
+            const cuuint64_t str[4] = {row, 128, row * 8, (cuuint64_t)kv[i].page * 2};
+            const cuuint32_t box[5] = {64, 8, D / 64, (cuuint32_t)((a.page_size < C::BN ? a.page_size : C::BN) / 8), 1};
+            ok = ok && encode(kv[i].m, kv[i].p, dt, 5, dims, str, box);
+        } else if constexpr (kPaged) {
             const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.H_kv, (cuuint64_t)a.page_size,
                                         (cuuint64_t)a.pages};
             const cuuint64_t str[3] = {(cuuint64_t)kv[i].s.head * 2, (cuuint64_t)kv[i].s.tok * 2,
@@ -592,12 +636,12 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
         }
     }
     if (!ok) return cudaErrorInvalidValue;
-    cudaError_t e = launch_fwd_plan(a, geo, plan, st);
-    if (e != cudaSuccess) return e;
-    auto kern = packed_fwd_kernel<T, D, kPaged>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e != cudaSuccess) return e;
-    // programmatic dependent launch: barriers and TMEM are set up while the plan is made
+    cudaError_t e;
+    if (!geo.self && (e = launch_fwd_plan(a, geo, plan, st)) != cudaSuccess) return e;
+    auto kern = packed_fwd_kernel<T, D, kPaged, kGroup>;
+    static std::atomic<uint64_t> ready{0};
+    if ((e = allow_smem(kern, (int)kSmem, ready)) != cudaSuccess) return e;
+    // programmatic dependent launch: barriers and TMEM are set up while the kernel before runs
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)geo.ctas);
     cfg.blockDim = dim3(kThreads);
@@ -608,20 +652,24 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, plan, geo.tpt, geo.overhead);
+    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, plan, geo, (int)units);
 }
 
 template <typename T>
 cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     const int D = a.d == 256 ? 256 : tc_head_dim(a.d);
     if (a.paged()) {
-        if (D == 64) return launch_t<T, 64, true>(a, ws, bytes, st);
-        if (D == 128) return launch_t<T, 128, true>(a, ws, bytes, st);
-        if (D == 256) return launch_t<T, 256, true>(a, ws, bytes, st);
+        // head dims 32 and 96 keep a box per 64 columns, whose missing columns read as zeros
+        const bool group = a.d == D && (long long)a.H_kv * (a.k.head > a.v.head ? a.k.head : a.v.head) < (1ll << 31);
+        if (D == 64) return launch_t<T, 64, true, false>(a, ws, bytes, st);
+        if (D == 128 && group) return launch_t<T, 128, true, true>(a, ws, bytes, st);
+        if (D == 128) return launch_t<T, 128, true, false>(a, ws, bytes, st);
+        if (D == 256 && group) return launch_t<T, 256, true, true>(a, ws, bytes, st);
+        if (D == 256) return launch_t<T, 256, true, false>(a, ws, bytes, st);
     } else {
-        if (D == 64) return launch_t<T, 64, false>(a, ws, bytes, st);
-        if (D == 128) return launch_t<T, 128, false>(a, ws, bytes, st);
-        if (D == 256) return launch_t<T, 256, false>(a, ws, bytes, st);
+        if (D == 64) return launch_t<T, 64, false, false>(a, ws, bytes, st);
+        if (D == 128) return launch_t<T, 128, false, false>(a, ws, bytes, st);
+        if (D == 256) return launch_t<T, 256, false, false>(a, ws, bytes, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -10,104 +10,17 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-template <typename V>
-__device__ __forceinline__ V warp_incl_scan(V v) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const V u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    return v;
-}
-
-// Exclusive scan over the block; *total gets the block's sum.  Ends with a barrier.
-template <typename V>
-__device__ __forceinline__ V block_excl_scan(V v, V* sums, V* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
-    const V incl = warp_incl_scan(v);
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-        const V s = lane < warps ? sums[lane] : V(0);
-        const V si = warp_incl_scan(s);
-        sums[lane] = si - s;
-        if (lane == 31) sums[32] = si;
-    }
-    __syncthreads();
-    const V r = sums[warp] + incl - v;
-    *total = sums[32];
-    __syncthreads();
-    return r;
-}
-
-struct Seq {
-    int q0, nq, k0, nk;
-};
-
-// Lengths of sequence n; false if they do not fit the tensors.
-__device__ __forceinline__ bool seq_at(const PackedFwd& a, int n, Seq& s) {
-    const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1];
-    bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T_q;
-    s.q0 = q0;
-    s.nq = ok ? q1 - q0 : 0;
-    if (a.cu_k != nullptr) {
-        const int k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
-        const bool okk = k0 >= 0 && k1 >= k0 && k1 <= a.T_k;
-        s.k0 = k0;
-        s.nk = okk ? k1 - k0 : 0;
-        ok = ok && okk;
-    } else {
-        const int nk = a.seq_lens[n];
-        // longer than its table, or than positions are kept for, is refused
-        const bool okk = nk >= 0 && nk <= (1 << 28) && nk <= (long long)a.max_pages * a.page_size;
-        s.k0 = 0;
-        s.nk = okk ? nk : 0;
-        ok = ok && okk;
-    }
-    return ok;
-}
-
-// Largest n with first[n] <= u (first is non-decreasing, first[N] > u).
-__device__ __forceinline__ int find_seq(const int* first, int N, int u) {
-    int lo = 0, hi = N;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= u)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
 constexpr int kSmemSeqs = 4096;  // sequences whose unit offsets are also kept in shared memory
 
-template <typename T>
-__device__ void fill_rows(const PackedFwd& a) {
-    // rows before the first and behind the last sequence: O = 0, LSE = -inf
-    const int lo = a.cu_q[0], hi = a.cu_q[a.N];
-    if (lo < 0 || hi < lo || hi > a.T_q) return;  // reported by the planning block
-    const long long rows = (long long)(lo + a.T_q - hi) * a.H;
-    const int per = a.d * (int)sizeof(T) / 16;
-    const long long step = (long long)(gridDim.x - 1) * blockDim.x;
-    for (long long e = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x; e < rows * per; e += step) {
-        const long long r = e / per;
-        const int t = (int)(r / a.H), h = (int)(r % a.H), c = (int)(e % per);
-        const int tok = t < lo ? t : t - lo + hi;
-        T* dst = static_cast<T*>(a.O) + tok * a.o.tok + h * a.o.head + c * (16 / (int)sizeof(T));
-        *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-        if (c == 0) a.LSE[(size_t)h * a.T_q + tok] = -INFINITY;
-    }
-}
-
-__global__ void __launch_bounds__(kPlanThreads) fwd_plan_kernel(const PackedFwd a, const FwdGeom g, const FwdPlan p) {
+__global__ void __launch_bounds__(kPlanThreads, 1) fwd_plan_kernel(const PackedFwd a, const FwdGeom g, const FwdPlan p) {
     ptx::griddep_launch_dependents();
     if (blockIdx.x > 0) {
+        const long long first = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+        const long long step = (long long)(gridDim.x - 1) * blockDim.x;
         if (a.dtype == FA_F32)
-            fill_rows<float>(a);
+            fill_rows<float>(a, first, step);
         else
-            fill_rows<__half>(a);
+            fill_rows<__half>(a, first, step);
         return;
     }
     __shared__ int s_first[kSmemSeqs + 1];
@@ -145,27 +58,9 @@ __global__ void __launch_bounds__(kPlanThreads) fwd_plan_kernel(const PackedFwd 
         long long cost = 0;
         if (u < U) {
             const int n = find_seq(first, a.N, u);
-            Seq s;
-            seq_at(a, n, s);
-            const int i0 = (u - first[n]) * g.tpt;
             FwdTile t;
-            t.n = n;
-            t.q_tok = s.q0 + i0;
-            t.n_tok = min(g.tpt, s.nq - i0);
-            t.pos0 = i0 + s.nk - s.nq;
-            t.k_base = s.k0;
-            t.S_k = s.nk;
-            Shape sh;
-            sh.S_q = s.nq;
-            sh.S_k = s.nk;
-            sh.causal = a.causal;
-            sh.window = a.window;
-            int lo, hi;
-            key_range(sh, i0, i0 + t.n_tok, lo, hi);
-            t.n_first = hi > lo ? lo / g.bn : 0;
-            t.n_cnt = hi > lo ? (hi + g.bn - 1) / g.bn - t.n_first : 0;
+            cost = (long long)make_tile(a, g, n, u - first[n], t) * g.heads;
             p.tile[u] = t;
-            cost = (long long)(max(t.n_cnt, 1) + g.overhead) * g.heads;
         }
         long long total;
         const long long at = block_excl_scan(cost, s_lsum, &total);
@@ -174,13 +69,11 @@ __global__ void __launch_bounds__(kPlanThreads) fwd_plan_kernel(const PackedFwd 
     }
 
     // equal shares, and the unit each CTA starts in
-    long long chunk = (W + g.ctas - 1) / g.ctas;
-    if (chunk < g.min_chunk) chunk = g.min_chunk;
+    const long long chunk = share_of(W, g);
     if (tid == 0) {
         p.head[0] = W;
         p.head[1] = chunk;
     }
-    for (int c = tid; c < g.ctas; c += kPlanThreads) p.done[c] = 0u;
     for (int u = tid; u < U; u += kPlanThreads) {
         const long long b = p.base[u];
         const long long e = b + (long long)(max(p.tile[u].n_cnt, 1) + g.overhead) * g.heads;
@@ -248,7 +141,7 @@ __device__ __forceinline__ bool seq_at(const PackedBwd& a, int n, Seq& s) {
 constexpr int kBuckets = 2048;
 
 // Block 0 plans; blocks 1 .. map_blocks write tensor maps, one warp a map; the rest fill.
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     bwd_plan_kernel(const PackedBwd a, const BwdPlan p, const __grid_constant__ BwdMaps maps, int map_blocks) {
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x;
@@ -305,10 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (tid == 0) atomicOr(a.err, kErrLengths);
         UQ = UK = 0;
     }
-    if (tid == 0) {
-        p.head[0] = UQ;
-        p.head[1] = UK;
-    }
+    if (tid == 0) p.head[0] = UQ;
     if (a.deterministic)
         for (long long i = tid; i < (long long)a.H * p.max_units; i += kPlanThreads) p.sem[i] = 0u;
     for (int i = tid; i < kBuckets; i += kPlanThreads) s_count[i] = 0;
@@ -318,6 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int i0 = (u - p.seq_q[n]) * kBwdTile, q0 = a.cu_q[n], nq = a.cu_q[n + 1] - q0;
         p.query[u] = {q0 + i0, min(kBwdTile, nq - i0)};
     }
+    long long its = 0;
     for (int v = tid; v < UK; v += kPlanThreads) {
         const int n = find_seq(p.seq_k, a.N, v);
         Seq s;
@@ -339,11 +230,46 @@ __global__ void __launch_bounds__(kPlanThreads)
         t.its = hi > lo ? (hi + kBwdTile - 1) / kBwdTile - lo / kBwdTile : 0;
         t.pad = 0;
         p.key[v] = t;
-        atomicAdd(&s_count[min(t.its, kBuckets - 1)], 1);
+        its += t.its;
     }
+    // iterations of an even share
+    const int g = a.H / a.H_kv;
+    __shared__ long long s_lsum[33];
+    long long all;
+    block_excl_scan(its, s_lsum, &all);
+    const long long share = max((all * a.H + p.shares - 1) / p.shares, (long long)p.min_its);
+    // parts of each tile, in tile order; bucket sizes of the sort by length (most first)
+    auto parts_of = [&](int v) {
+        const long long n = v < UK ? (long long)p.key[v].its * g : 0;
+        return v >= UK ? 0 : n > share ? (int)((n + share - 1) / share) : 1;
+    };
+    auto bucket = [&](int v, int parts) {
+        return (int)min(((long long)p.key[v].its * g + parts - 1) / parts, (long long)kBuckets - 1);
+    };
+    int works = 0, cuts = 0, slots = 0;
+    for (int v0 = 0; v0 < UK; v0 += kPlanThreads) {
+        const int v = v0 + tid, n = parts_of(v);
+        int total_w, total_c, total_s;
+        const int w = works + block_excl_scan(n, s_sum, &total_w);
+        const int c = cuts + block_excl_scan(n > 1 ? 1 : 0, s_sum, &total_c);
+        const int sl = slots + block_excl_scan(n > 1 ? n : 0, s_sum, &total_s);
+        if (n > 1) p.cut[c] = {v, 0, n, sl};
+        if (a.deterministic)
+            for (int i = 0; i < n; ++i) p.work[w + i] = {v, i, n, sl + i};
+        else if (n > 0)
+            atomicAdd(&s_count[bucket(v, n)], n);
+        works += total_w;
+        cuts += total_c;
+        slots += total_s;
+    }
+    if (tid == 0) {
+        p.head[1] = works;
+        p.head[2] = cuts;
+    }
+    if (a.deterministic) return;
     __syncthreads();
-    // counting sort, most query tiles first (within a bucket in any order: it decides only which
-    // CTA starts first)
+    // counting sort, longest first (within a bucket in any order: it decides only which CTA
+    // starts first)
     const int b0 = kBuckets - 1 - 2 * tid, b1 = b0 - 1;
     const int c0 = s_count[b0], c1 = s_count[b1];
     int total;
@@ -351,7 +277,15 @@ __global__ void __launch_bounds__(kPlanThreads)
     s_count[b0] = at;
     s_count[b1] = at + c0;
     __syncthreads();
-    for (int v = tid; v < UK; v += kPlanThreads) p.order[atomicAdd(&s_count[min(p.key[v].its, kBuckets - 1)], 1)] = v;
+    slots = 0;
+    for (int v0 = 0; v0 < UK; v0 += kPlanThreads) {
+        const int v = v0 + tid, n = parts_of(v);
+        int total_s;
+        const int sl = slots + block_excl_scan(n > 1 ? n : 0, s_sum, &total_s);
+        const int w = n > 0 ? atomicAdd(&s_count[bucket(v, n)], n) : 0;
+        for (int i = 0; i < n; ++i) p.work[w + i] = {v, i, n, sl + i};
+        slots += total_s;
+    }
 }
 
 bool row_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es, int d, int heads, long long rows,

@@ -32,8 +32,10 @@ __global__ void __launch_bounds__(kThreads)
     const T* Q = static_cast<const T*>(a.Q);
     const T* K = static_cast<const T*>(a.K);
     const T* V = static_cast<const T*>(a.V);
+    FwdShare share;
+    share.read(plan, blockIdx.x);
     FwdWalk w;
-    for (bool more = w.init(plan, blockIdx.x, a.H_kv * hsub, kOverhead); more; more = w.next(plan)) {
+    for (bool more = w.init(share, blockIdx.x, a.H_kv * hsub, kOverhead); more; more = w.next()) {
         // groups of more heads than a tile has rows are cut into hsub pieces of up to 64
         const int hk = w.hd / hsub, h0 = (w.hd % hsub) * BM;
         const int gh = min(g - h0, BM);      // heads of this item
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kThreads)
             w.parts(first, count);
             __threadfence();
             __syncthreads();
-            if (tid == 0) s_last = atomicAdd(&plan.done[first], 1u) == (unsigned)(count - 1);
+            if (tid == 0) s_last = arrive_part(&plan.done[first], plan.tag, count);
             __syncthreads();
             if (s_last) {
                 __threadfence();
@@ -191,21 +193,20 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     auto kern = packed_fwd_simt_kernel<T, D>;
     const int g = a.H / a.H_kv;
     const int hsub = (g + BM - 1) / BM;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     FwdGeom geo;
     geo.rows = BM;
     geo.tpt = g < BM ? BM / g : 1;
     geo.bn = BN;
     geo.heads = a.H_kv * hsub;
-    geo.ctas = (sms > 0 ? sms : 148) * (D <= 96 ? 2 : 1);  // resident CTAs by shared memory
+    geo.ctas = sm_count() * (D <= 96 ? 2 : 1);  // resident CTAs by shared memory
     geo.D = D;
     geo.min_chunk = 2;
     geo.overhead = kOverhead;
+    geo.self = false;
     FwdPlan plan;
     *bytes = fwd_plan_layout(a, geo, ws, &plan);
     if (ws == nullptr) return cudaSuccess;
+    plan.tag = next_tag();
     cudaError_t e = launch_fwd_plan(a, geo, plan, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -325,3 +325,14 @@ def test_bad_lengths_and_pages_are_reported():
     with pytest.raises(fa.FaError, match="page or slot"):
         fa.fa_check_device()
     assert torch.equal(Kc.view(16, 64)[3], K[0, 0]) and Kc.count_nonzero() == K[0].count_nonzero()
+
+
+def test_strided_head_dimension_is_refused():
+    Q, K, V = _packed(1, [8], [8], 2, 2, 128, torch.bfloat16)
+    with pytest.raises(fa.FaError, match="Q: the head dimension must be contiguous"):
+        fa.fa_varlen_fwd(Q[..., ::2], K[..., :64], V[..., :64], _cu([8]), _cu([8]))
+    with pytest.raises(fa.FaError, match="strides: entry"):  # rows of 65 elements
+        wide = torch.zeros(8, 2, 65, dtype=torch.bfloat16, device="cuda")
+        fa.fa_varlen_fwd(wide[..., :64], K[..., :64], V[..., :64], _cu([8]), _cu([8]))
+    with pytest.raises(fa.FaError, match="strides: entry"):  # broadcast heads
+        fa.fa_varlen_fwd(Q, K[:, :1].expand(-1, 2, -1), V, _cu([8]), _cu([8]))

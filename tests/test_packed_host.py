@@ -132,7 +132,11 @@ def test_binding_refuses_before_the_library():
         (lambda: fa.fa_varlen_fwd(q, k[..., :32], k, cu, cu), "K"),
         (lambda: fa.fa_varlen_fwd(q, k, k, cu.long(), cu), "cu_q"),
         (lambda: fa.fa_varlen_fwd(q, k, k, cu, cu[:1]), "cu_k"),
-        (lambda: fa.fa_varlen_fwd(q.transpose(1, 2), k, k, cu, cu), "Q"),
+        (lambda: fa.fa_varlen_fwd(q.transpose(1, 2), k, k, cu, cu), "K"),
+        (lambda: fa.fa_varlen_bwd(q, q, k, k, q, torch.zeros(4, 6), cu, cu), "LSE"),
+        (lambda: fa.fa_varlen_bwd(q[:4], q, k, k, q, torch.zeros(4, 5), cu, cu), "dO"),
+        (lambda: fa.fa_varlen_bwd(q, q, k, k, q, torch.zeros(4, 5), cu, cu, dV=q), "dV"),
+        (lambda: fa.fa_varlen_bwd(q, q, k, k, q, torch.zeros(4, 5), cu, cu), "tensors"),
         (lambda: fa.fa_paged_fwd(q, cache[0], cache, table, cu, lens), "K_cache"),
         (lambda: fa.fa_paged_fwd(q, cache, cache, table[0], cu, lens), "block_table"),
         (lambda: fa.fa_paged_fwd(q, cache, cache, table, cu, lens.long()), "seq_lens"),
@@ -140,7 +144,7 @@ def test_binding_refuses_before_the_library():
         (lambda: fa.fa_page_slots(lens.long(), cu, table, lens, lens, 16, 5), "ctx_lens"),
         (lambda: fa.fa_page_slots(lens, cu, table, lens, lens, 16, -5), "tokens"),
         (lambda: fa.fa_paged_write(k, k, lens, cache, cache), "slots"),
-        (lambda: fa.fa_paged_write(k, k, torch.zeros(5, dtype=torch.int64), cache[..., :32], cache), "K_cache"),
+        (lambda: fa.fa_paged_write(k, k, torch.zeros(5, dtype=torch.int64), cache[..., :32], cache[..., :32]), "K_cache"),
     ]
     for call, arg in cases:
         with pytest.raises(fa.FaError) as e:
