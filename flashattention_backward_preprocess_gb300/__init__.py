@@ -44,3 +44,4 @@ from .packed import (  # noqa: F401
     fa_varlen_bwd,
     fa_varlen_fwd,
 )
+from .cache import PagedKVCache  # noqa: F401

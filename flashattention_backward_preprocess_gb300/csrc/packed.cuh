@@ -332,57 +332,53 @@ struct SelfPlan {
 template <int kThreads>
 __device__ __forceinline__ void plan_self(const PackedFwd& a, const FwdGeom& g, const FwdPlan& p, int max_units,
                                           SelfPlan* s) {
-    constexpr int kPer = kSelfUnits / kThreads;
-    static_assert(kPer * kThreads == kSelfUnits, "units per thread");
     const int tid = threadIdx.x, cta = blockIdx.x;
     bool bad = false;
-    int units[kPer], sum = 0, U;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int n = tid * kPer + i;
+    int U = 0;
+    for (int n0 = 0; n0 < a.N; n0 += kThreads) {
+        const int n = n0 + tid;
         Seq q = {0, 0, 0, 0};
         if (n < a.N && !seq_at(a, n, q)) bad = true;
-        units[i] = (q.nq + g.tpt - 1) / g.tpt;
-        sum += units[i];
-    }
-    int at = block_excl_scan(sum, s->isum, &U);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int n = tid * kPer + i;
-        if (n < a.N) s->first[n] = at;
-        at += units[i];
+        int total;
+        const int at = block_excl_scan((q.nq + g.tpt - 1) / g.tpt, s->isum, &total);
+        if (n < a.N) s->first[n] = U + at;
+        U += total;
     }
     if (tid == 0) s->first[a.N] = U;
     if (__syncthreads_or(bad)) {  // lengths that do not fit the tensors: nothing is computed
         if (tid == 0 && cta == 0) atomicOr(a.err, kErrLengths);
         U = 0;
     }
-    FwdTile t[kPer];
-    long long cost[kPer], all = 0, W;
-    int n = tid * kPer < U ? find_seq(s->first, a.N, tid * kPer) : 0;
+    constexpr int kRounds = (kSelfUnits + kThreads - 1) / kThreads;
+    FwdTile t[kRounds];
+    int cost[kRounds];  // per head
+    long long base[kRounds], W = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int u = tid * kPer + i;
+    for (int i = 0; i < kRounds; ++i) {
+        const int u = i * kThreads + tid;
         cost[i] = 0;
+        if (i * kThreads >= U) continue;
         if (u < U) {
-            while (s->first[n + 1] <= u) ++n;
-            cost[i] = (long long)make_tile(a, g, n, u - s->first[n], t[i]) * g.heads;
+            const int n = find_seq(s->first, a.N, u);
+            cost[i] = make_tile(a, g, n, u - s->first[n], t[i]);
         }
-        all += cost[i];
+        long long total;
+        base[i] = W + block_excl_scan((long long)cost[i] * g.heads, s->lsum, &total);
+        W += total;
     }
-    long long base = block_excl_scan(all, s->lsum, &W);
     const long long chunk = share_of(W, g);
     const long long lo = chunk * cta, hi = lo + chunk;
     FwdTile* mine = p.tile + (size_t)cta * max_units;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int u = tid * kPer + i;
-        if (u < U && base < hi && base + cost[i] > lo) mine[u] = t[i];
-        if (u < U && base <= lo && base + cost[i] > lo) {
+    for (int i = 0; i < kRounds; ++i) {
+        const int u = i * kThreads + tid;
+        if (u >= U) continue;
+        const long long end = base[i] + (long long)cost[i] * g.heads;
+        if (base[i] < hi && end > lo) mine[u] = t[i];
+        if (base[i] <= lo && end > lo) {
             s->share.u = u;
-            s->share.base = base;
+            s->share.base = base[i];
         }
-        base += cost[i];
     }
     if (tid == 0) {
         s->share.tile = mine;

@@ -37,11 +37,16 @@ namespace fa {
 namespace {
 
 constexpr int BM = 128;  // rows per tile
-constexpr int kThreads = 224;
-constexpr int kWarpTma = 4, kWarpMma = 5, kWarpPv = 6;
+// warps 0-3 softmax, 4-7 epilogue, 8 TMA, 9 S products and TMEM, 10 P V products (11 only makes
+// the warpgroup whole)
+constexpr int kThreads = 384;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpPv = 10;
+// registers per thread of the softmax and the last warpgroup; the epilogue keeps the 168 that
+// each of the three is launched with (232 + 168 + 104 = 3 x 168)
+constexpr int kRegsSoft = 232, kRegsOther = 104;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only past this margin
-constexpr uint32_t kSoftBarrier = 1;
+constexpr uint32_t kEpiBarrier = 1;  // the epilogue's four warps
 
 template <int D>
 struct PCfg {
@@ -56,7 +61,9 @@ struct PCfg {
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = OFF_Q + kTileQ_B;
     static constexpr uint32_t OFF_V = OFF_K + STAGES * kTileKV_B;
-    static constexpr uint32_t OFF_BAR = OFF_V + STAGES * kTileKV_B;
+    // float2 per row: two slots of the rows' max and sum
+    static constexpr uint32_t OFF_ROW = OFF_V + STAGES * kTileKV_B;
+    static constexpr uint32_t OFF_BAR = OFF_ROW + 2 * BM * 8;
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
@@ -69,8 +76,9 @@ enum {
     P_FINAL = P_PV0 + 3,   // every product done
     P_QE,                  // the item's S products are done: the Q tile may be reloaded
     P_OFULL,               // O of an item complete
-    P_OFREE,               // O of an item read (4 softmax warps)
-    P_STAGE0               // STAGES "full", then STAGES "empty"
+    P_OFREE,               // O of an item read (4 epilogue warps)
+    P_ML0,                 // max and sum of an item's rows written (4 softmax warps), 2 slots
+    P_STAGE0 = P_ML0 + 2   // STAGES "full", then STAGES "empty"
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((sbase & 1023u) != 0) atomicOr(err, kErrSmemAlign);
         *abort_flag = (sbase & 1023u) != 0;
         for (int i = 0; i < kNumBars; ++i)
-            ptx::mbar_init(bar(i), ((i >= P_P0 && i < P_P0 + 3) || i == P_OFREE) ? 4u : 1u);
+            ptx::mbar_init(bar(i), ((i >= P_P0 && i < P_P0 + 3) || (i >= P_OFREE && i < P_STAGE0)) ? 4u : 1u);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -176,6 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
     // CTA (jg), per-item ones its segments with work (ka).
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpTma) {
         // ------------------------------------------------------------ producer
         // Two streams over the same segments, polled in turn: the Q tile (once the previous
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kWarpMma || warp == kWarpPv) {
         // ------------------------------------------------------------ MMA issuers
-        // Warp 5 issues S = Q K^T, warp 6 O += P V, so that each hides the other's waits.  S
+        // One warp issues S = Q K^T, another O += P V, so that each hides the other's waits.  S
         // of tile jg goes into buffer jg % NB once the P V product of tile jg - NB has read P
         // out of it; the P V product runs once the softmax has packed P.
         if (lane == 0 && !*abort_flag) {
@@ -367,22 +377,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ softmax + epilogue
-        const int t = warp * 32 + lane;  // TMEM lane == row of the tile
+    }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int t = threadIdx.x;  // TMEM lane == row of the tile
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        const int ti = t / g, th = t - ti * g;  // token and head of the row
+        const int ti = t / g;  // token of the row
         const float scale_log2 = a.scale * 1.4426950408889634f;
-        const bool wide = ((reinterpret_cast<uintptr_t>(a.O) | (a.o.tok * 2) | (a.o.head * 2)) & 31) == 0;
+        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ROW);
         bool ok = !*abort_flag;
         int jg = 0, ka = 0;
         FwdWalk w;
         bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead);
         for (; ok && more; more = w.next()) {
-            const int rows = w.t.n_tok * g;
-            const bool row_valid = t < rows;
-            const bool warp_live = warp * 32 < rows;
+            const bool warp_live = warp * 32 < w.t.n_tok * g;
             const int nt = w.tiles();
+            if (nt == 0) continue;
             float m_run = -INFINITY;  // running max of s * log2(e), moved lazily
             float l_run = 0.f;        // sum of exp2(x - m_run)
             for (int j = 0; ok && j < nt; ++j, ++jg) {
@@ -479,11 +490,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(bar(P_P0 + jg % NB));
             }
             if (!ok) break;
-            // ---- epilogue: O = acc / l and LSE = (m + log2 l) ln 2 of a whole item, the raw
-            // accumulator with (m, l) of a cut one
-            const bool has = nt > 0;
+            // The slot's last reader was the epilogue of two items ago, which read it before it
+            // released O; this item's products could not have run without that.
+            ml[(ka & 1) * BM + t] = make_float2(m_run, l_run);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(P_ML0 + (ka & 1)));
+            ++ka;
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // O = acc / l and LSE = (m + log2 l) ln 2 of a whole item; of a cut one the raw
+        // accumulator with (m, l), and the last part to arrive joins them.  Meanwhile the
+        // softmax warps are at the next item; its first P V product waits for O to be read.
+        const int t = threadIdx.x - 128;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const int ti = t / g, th = t - ti * g;  // token and head of the row
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.O) | (a.o.tok * 2) | (a.o.head * 2)) & 31) == 0;
+        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ROW);
+        int ka = 0;
+        FwdWalk w;
+        bool more = !*abort_flag && w.init(share, blockIdx.x, a.H_kv, geo.overhead);
+        for (; more; more = w.next()) {
+            const int rows = w.t.n_tok * g;
+            const bool row_valid = t < rows;
+            const bool warp_live = (warp & 3) * 32 < rows;
+            const bool has = w.tiles() > 0;
             const bool whole = w.whole();
-            if (has && !(ok = wait_bar_warp(bar(P_OFULL), ka & 1, abort_flag, err))) break;
+            float m_run = -INFINITY, l_run = 0.f;
+            if (has) {
+                // all four warps take the same decision (they meet at a barrier below)
+                const bool ok = ptx::named_bar_and(kEpiBarrier, 128,
+                                                   wait_bar(bar(P_ML0 + (ka & 1)), (ka >> 1) & 1, abort_flag, err) &&
+                                                       wait_bar(bar(P_OFULL), ka & 1, abort_flag, err));
+                if (!ok) break;
+                const float2 x = ml[(ka & 1) * BM + t];
+                m_run = x.x, l_run = x.y;
+                ++ka;
+            }
             ptx::tc_fence_after();
             const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
             const int tok = w.t.q_tok + ti, head = w.hd * g + th;
@@ -540,21 +583,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_arrive(bar(P_OFREE));
             }
             if (!whole) {
-                // the last part to arrive joins the item
                 int first, count;
                 w.parts(first, count);
                 __threadfence();
-                ptx::named_bar_sync(kSoftBarrier, 128);
+                ptx::named_bar_sync(kEpiBarrier, 128);
                 if (t == 0) *last_flag = arrive_part(&plan.done[first], plan.tag, count);
-                ptx::named_bar_sync(kSoftBarrier, 128);
+                ptx::named_bar_sync(kEpiBarrier, 128);
                 if (*last_flag) {
                     __threadfence();
+                    // scratch: the item's own slot, read above and next written for the item
+                    // after the next, whose products wait for this epilogue
                     join_parts<T, 128, BM, D>(a, plan, w.t, w.hd * g, g, rows, first, count, t,
-                                              reinterpret_cast<float2*>(smem + OFF_MISC + 16),
-                                              [] { ptx::named_bar_sync(kSoftBarrier, 128); });
+                                              ml + ((ka - 1) & 1) * BM,
+                                              [] { ptx::named_bar_sync(kEpiBarrier, 128); });
+                    ptx::named_bar_sync(kEpiBarrier, 128);
                 }
             }
-            if (has) ++ka;
         }
     }
 
@@ -577,7 +621,7 @@ bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, 
 template <typename T, int D, bool kPaged, bool kGroup>
 cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     using C = PCfg<D>;
-    constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16 + BM * 8;
+    constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
     const int g = a.H / a.H_kv;
     FwdGeom geo;
