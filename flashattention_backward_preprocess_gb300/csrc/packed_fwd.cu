@@ -78,7 +78,8 @@ enum {
     P_OFULL,               // O of an item complete
     P_OFREE,               // O of an item read (4 epilogue warps)
     P_ML0,                 // max and sum of an item's rows written (4 softmax warps), 2 slots
-    P_STAGE0 = P_ML0 + 2   // STAGES "full", then STAGES "empty"
+    P_MR0 = P_ML0 + 2,     // and read by the epilogue (4 warps), 2 slots
+    P_STAGE0 = P_MR0 + 2   // STAGES "full", then STAGES "empty"
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -94,6 +95,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                             uint32_t bar) {
@@ -239,6 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++q_act;
                     do q_more = wq.next();
                     while (q_more && wq.tiles() == 0);
+                    // the next item's Q tile to L2, so that its load, which the S products wait
+                    // for, is short
+                    if (q_more && lane < C::BOXES) tma_prefetch_3d(&tmQ, lane * 64, wq.hd * g, wq.t.q_tok);
                 }
                 if (act & 2) {
                     const int s = jg % C::STAGES;
@@ -490,8 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(bar(P_P0 + jg % NB));
             }
             if (!ok) break;
-            // The slot's last reader was the epilogue of two items ago, which read it before it
-            // released O; this item's products could not have run without that.
+            // the slot's values of two items ago must have been read (items of a tile or two can be
+            // through here before the epilogue of the first of them has begun)
+            if (ka > 1 && !(ok = wait_bar_warp(bar(P_MR0 + (ka & 1)), ((ka >> 1) - 1) & 1, abort_flag, err))) break;
             ml[(ka & 1) * BM + t] = make_float2(m_run, l_run);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(P_ML0 + (ka & 1)));
@@ -519,12 +530,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY, l_run = 0.f;
             if (has) {
                 // all four warps take the same decision (they meet at a barrier below)
-                const bool ok = ptx::named_bar_and(kEpiBarrier, 128,
-                                                   wait_bar(bar(P_ML0 + (ka & 1)), (ka >> 1) & 1, abort_flag, err) &&
-                                                       wait_bar(bar(P_OFULL), ka & 1, abort_flag, err));
-                if (!ok) break;
+                bool ok = wait_bar_warp(bar(P_ML0 + (ka & 1)), (ka >> 1) & 1, abort_flag, err);
+                ok = ok && wait_bar_warp(bar(P_OFULL), ka & 1, abort_flag, err);
+                __syncwarp();
+                if (!ptx::named_bar_and(kEpiBarrier, 128, ok)) break;
                 const float2 x = ml[(ka & 1) * BM + t];
                 m_run = x.x, l_run = x.y;
+                __syncwarp();
+                // (of a whole item; a cut one's slot serves as scratch below)
+                if (whole && lane == 0) ptx::mbar_arrive(bar(P_MR0 + (ka & 1)));
                 ++ka;
             }
             ptx::tc_fence_after();
@@ -586,18 +600,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int first, count;
                 w.parts(first, count);
                 __threadfence();
+                __syncwarp();
                 ptx::named_bar_sync(kEpiBarrier, 128);
                 if (t == 0) *last_flag = arrive_part(&plan.done[first], plan.tag, count);
+                __syncwarp();
                 ptx::named_bar_sync(kEpiBarrier, 128);
                 if (*last_flag) {
                     __threadfence();
-                    // scratch: the item's own slot, read above and next written for the item
-                    // after the next, whose products wait for this epilogue
                     join_parts<T, 128, BM, D>(a, plan, w.t, w.hd * g, g, rows, first, count, t,
-                                              ml + ((ka - 1) & 1) * BM,
-                                              [] { ptx::named_bar_sync(kEpiBarrier, 128); });
+                                              ml + ((ka - 1) & 1) * BM, [] {
+                                                  __syncwarp();
+                                                  ptx::named_bar_sync(kEpiBarrier, 128);
+                                              });
+                    __syncwarp();
                     ptx::named_bar_sync(kEpiBarrier, 128);
                 }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(P_MR0 + ((ka - 1) & 1)));
             }
         }
     }

@@ -336,3 +336,33 @@ def test_strided_head_dimension_is_refused():
         fa.fa_varlen_fwd(wide[..., :64], K[..., :64], V[..., :64], _cu([8]), _cu([8]))
     with pytest.raises(fa.FaError, match="strides: entry"):  # broadcast heads
         fa.fa_varlen_fwd(Q, K[:, :1].expand(-1, 2, -1), V, _cu([8]), _cu([8]))
+
+
+@pytest.mark.parametrize("N,H,H_kv,d", [(700, 8, 8, 64), (1500, 8, 2, 128), (600, 4, 4, 256)])
+def test_varlen_fwd_many_short_sequences(N, H, H_kv, d):
+    """Items of one key tile each, many per CTA, with the plan of one block and of every CTA."""
+    lens = [1 + (i * 31) % 40 for i in range(N)]
+    Q, K, V = _packed(13, lens, lens, H, H_kv, d, torch.bfloat16)
+    cu = _cu(lens)
+    O, LSE = fa.fa_varlen_fwd(Q, K, V, cu, cu, causal=True)
+    for _ in range(5):
+        O2, LSE2 = fa.fa_varlen_fwd(Q, K, V, cu, cu, causal=True)
+        torch.cuda.synchronize()
+        fa.fa_check_device()
+        assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+    # one padded batch in 64 bits
+    m, off = max(lens), torch.tensor([0] + lens).cumsum(0)[:-1]
+    at = (off[:, None] + torch.arange(m)).clamp(max=sum(lens) - 1)
+    q, k, v = (x.double().cpu()[at].transpose(1, 2) for x in (Q, K, V))
+    k, v = (x.repeat_interleave(H // H_kv, 1) for x in (k, v))
+    s = (q @ k.transpose(-1, -2)) * d ** -0.5
+    see = torch.ones(m, m).tril().bool()
+    s = s.masked_fill(~see, -math.inf)
+    lse = torch.logsumexp(s, -1)
+    P = torch.exp(s - lse[..., None])
+    s_err = d * ref.STEP * d ** -0.5 * float((q.abs() @ k.abs().transpose(-1, -2)).max())
+    e = 2 * math.expm1(s_err) + m * ref.STEP + 2.0 ** -21
+    inside = torch.arange(m) < torch.tensor(lens)[:, None]
+    pick = lambda x: x.transpose(1, 2)[inside]
+    ref.check("O", O, pick(P @ v), pick(P @ v.abs()), e, torch.bfloat16)
+    ref.check_lse(LSE, lse.transpose(1, 2)[inside].t(), e)
