@@ -394,7 +394,7 @@ cudaError_t launch_fwd_plan(const PackedFwd& a, const FwdGeom& g, const FwdPlan&
 // Joins the parts of one cut item (kThreads threads, all of them past the barrier that follows
 // the last part's arrival): O = sum_k O_k 2^(m_k - M) / sum_k l_k 2^(m_k - M), parts in the order
 // of their keys.  s_row: `rows` float2 of shared memory; sync: a barrier of those threads.
-template <typename T, int kThreads, int kRowsLd, int kD, typename Sync>
+template <typename T, int kThreads, int kRowsLd, int kD, int kBatch, typename Sync>
 __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p, const FwdTile& t, int head0, int g,
                                            int rows, int first, int count, int tid, float2* s_row, Sync sync) {
     auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * first + 1 : 2 * (first + k)) * kRowsLd; };
@@ -416,7 +416,7 @@ __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p,
     }
     sync();
     // four columns of a row per thread and step; kBatch steps' loads in flight together
-    constexpr int kBatch = 8, C4 = kD / 4;
+    constexpr int C4 = kD / 4;
     for (int e0 = tid; e0 < rows * C4; e0 += kBatch * kThreads) {
         float4 s[kBatch];
 #pragma unroll

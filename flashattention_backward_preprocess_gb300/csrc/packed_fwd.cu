@@ -20,9 +20,9 @@
 //     V behind the sequence's last key (another sequence's, or whatever a page holds) are
 //     zeroed in shared memory before the P V product: P is 0 there, but 0 * inf is not;
 //   * S = Q K^T and O += P V with tcgen05.mma, P as the TMEM A operand; three S buffers
-//     (two at d = 256); warps 0-3 softmax and epilogue (one row per thread), warp 4 TMA,
-//     warp 5 S products, warp 6 P V products.  The next item's loads and S products overlap
-//     this item's epilogue.  Softmax warps whose rows are all padding (single-token steps fill
+//     (two at d = 256); eight softmax warps (two threads per row), four epilogue warps, a warp
+//     each for TMA, the S products and the P V products.  The next item's loads, S products and
+//     softmax overlap this item's epilogue.  Softmax warps whose rows are all padding (single-token steps fill
 //     g of 128 rows) only pass the barriers on;
 //   * P is rounded to the inputs' 16-bit type for the product (the tensor core's operand type);
 //     the row sum adds the unrounded fp32 values;
@@ -37,16 +37,17 @@ namespace fa {
 namespace {
 
 constexpr int BM = 128;  // rows per tile
-// warps 0-3 softmax, 4-7 epilogue, 8 TMA, 9 S products and TMEM, 10 P V products (11 only makes
-// the warpgroup whole)
-constexpr int kThreads = 384;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpPv = 10;
-// registers per thread of the softmax and the last warpgroup; the epilogue keeps the 168 that
-// each of the three is launched with (232 + 168 + 104 = 3 x 168)
-constexpr int kRegsSoft = 232, kRegsOther = 104;
+// warps 0-7 softmax, 8-11 epilogue, 12 TMA, 13 S products and TMEM, 14 P V products (15 only
+// makes the warpgroup whole)
+constexpr int kThreads = 512;
+constexpr int kWarpEpi = 8, kWarpTma = 12, kWarpMma = 13, kWarpPv = 14;
+// registers per thread of the two softmax warpgroups, the epilogue and the last one: together
+// 4 x 128, what the block is launched with
+constexpr int kRegsSoft = 152, kRegsEpi = 120, kRegsOther = 88;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.f;  // move the running max only past this margin
-constexpr uint32_t kEpiBarrier = 1;  // the epilogue's four warps
+constexpr float kMaxSum = 16384.f;    // of a tile's half row before the running max is looked at again
+constexpr uint32_t kEpiBarrier = 1;   // the epilogue's four warps
+constexpr uint32_t kPairBarrier = 2;  // + lane quadrant: the two softmax warps of a row
 
 template <int D>
 struct PCfg {
@@ -61,9 +62,11 @@ struct PCfg {
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = OFF_Q + kTileQ_B;
     static constexpr uint32_t OFF_V = OFF_K + STAGES * kTileKV_B;
-    // float2 per row: two slots of the rows' max and sum
+    // float2 per row: two slots of the rows' max and sum; then a float per row that a row's two
+    // softmax threads exchange
     static constexpr uint32_t OFF_ROW = OFF_V + STAGES * kTileKV_B;
-    static constexpr uint32_t OFF_BAR = OFF_ROW + 2 * BM * 8;
+    static constexpr uint32_t OFF_XCH = OFF_ROW + 2 * BM * 8;
+    static constexpr uint32_t OFF_BAR = OFF_XCH + BM * 4;
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
@@ -71,7 +74,7 @@ struct PCfg {
 enum {
     P_Q = 0,               // Q tile landed (TMA)
     P_S0,                  // S in buffer b (MMA commit), three slots
-    P_P0 = P_S0 + 3,       // P packed in buffer b (4 softmax warps), three slots
+    P_P0 = P_S0 + 3,       // P packed in buffer b (8 softmax warps), three slots
     P_PV0 = P_P0 + 3,      // P V product of buffer b done (MMA commit), three slots
     P_FINAL = P_PV0 + 3,   // every product done
     P_QE,                  // the item's S products are done: the Q tile may be reloaded
@@ -86,6 +89,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+// TMEM column (relative to a buffer) of the packed 16-bit P for 16 keys, MMA k-step k: each half
+// of the BN key columns is packed into the first half of the columns it was read from.
+template <int BN>
+__device__ __forceinline__ constexpr uint32_t packed_col(int k) {
+    return (uint32_t)((k / (BN / 32)) * (BN / 2) + (k % (BN / 32)) * 8);
 }
 template <bool kBF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((sbase & 1023u) != 0) atomicOr(err, kErrSmemAlign);
         *abort_flag = (sbase & 1023u) != 0;
         for (int i = 0; i < kNumBars; ++i)
-            ptx::mbar_init(bar(i), ((i >= P_P0 && i < P_P0 + 3) || (i >= P_OFREE && i < P_STAGE0)) ? 4u : 1u);
+            ptx::mbar_init(bar(i), i >= P_P0 && i < P_P0 + 3 ? 8u : i >= P_OFREE && i < P_STAGE0 ? 4u : 1u);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -191,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
     // CTA (jg), per-item ones its segments with work (ka).
-    if (warp >= 8) {
+    if (warp >= kWarpTma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpTma) {
         // ------------------------------------------------------------ producer
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
-                            ptx::mma_ts(tmem + C::TM_O, tmem + C::TM_S + (jg % NB) * 128 + kk * 8,
+                            ptx::mma_ts(tmem + C::TM_O, tmem + C::TM_S + (jg % NB) * 128 + packed_col<BN>(kk),
                                         desc_add(dV_mn, (uint32_t)s * C::kTileKV_B + kk * 2 * kRow8), ID_PV,
                                         (j > 0 || kk > 0) ? 1u : 0u);
                         ptx::mma_commit(bar(P_PV0 + jg % NB));
@@ -388,109 +397,151 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     }
-    } else if (warp < 4) {
+    } else if (warp < kWarpEpi) {
         // ------------------------------------------------------------ softmax
+        // Two threads per row, in warps w and w + 4 (of one TMEM lane quadrant), each half of a
+        // tile's key columns.  (One thread per row took 1620 cycles a tile, mostly latency that
+        // one warp per scheduler cannot hide; the two products of a tile take 1310.)
+        //
+        // The two need one reference m for their exponentials.  It need not be the max: exp2(x -
+        // m) keeps its relative precision and only must not overflow.  So m is the max over the
+        // first tile in which the row sees a key, and is found anew only when a row's half sum
+        // over a tile exceeds kMaxSum (which bounds every P, also for fp16); in between the two
+        // threads agree that it did not with one barrier.  S stays in TMEM until P replaces it.
+        // A timeout never leaves the loop, so that the partner is not left at a barrier: all
+        // waits return at once then.
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        const int t = threadIdx.x;  // TMEM lane == row of the tile
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        constexpr int HN = BN / 2;  // columns of a thread
+        const int hf = warp >> 2, qd = warp & 3;
+        const int t = qd * 32 + lane;  // TMEM lane == row of the tile
+        const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+        const uint32_t pair = kPairBarrier + qd;
         const int ti = t / g;  // token of the row
         const float scale_log2 = a.scale * 1.4426950408889634f;
         float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ROW);
-        bool ok = !*abort_flag;
+        volatile float* xch = reinterpret_cast<volatile float*>(smem + C::OFF_XCH) + t;
         int jg = 0, ka = 0;
         FwdWalk w;
-        bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead);
-        for (; ok && more; more = w.next()) {
-            const bool warp_live = warp * 32 < w.t.n_tok * g;
+        bool more = !(sbase & 1023u) && w.init(share, blockIdx.x, a.H_kv, geo.overhead);
+        for (; more; more = w.next()) {
+            const bool row_valid = t < w.t.n_tok * g;
+            const bool warp_live = qd * 32 < w.t.n_tok * g;
             const int nt = w.tiles();
             if (nt == 0) continue;
-            float m_run = -INFINITY;  // running max of s * log2(e), moved lazily
-            float l_run = 0.f;        // sum of exp2(x - m_run)
-            for (int j = 0; ok && j < nt; ++j, ++jg) {
-                const uint32_t buf = tmem + C::TM_S + (jg % NB) * 128 + lane_off;
+            float m_run = -INFINITY;  // reference of the row's exponentials, in units of s * log2(e)
+            float l_run = 0.f;        // sum of exp2(x - m_run) over this thread's columns
+            for (int j = 0; j < nt; ++j, ++jg) {
+                const uint32_t buf = tmem + C::TM_S + (jg % NB) * 128 + lane_off + hf * HN;
                 const int n0 = (w.t.n_first + w.j0 + j) * BN;
                 const int k_live = w.t.S_k - n0;  // keys of the sequence from this tile on
                 int c_lo, c_hi;
                 visible_keys(w.t.pos0 + ti - n0, a.causal, a.window, c_lo, c_hi);
-                c_lo = max(c_lo, 0);
-                c_hi = min(c_hi, k_live);
+                c_lo = max(c_lo, 0) - hf * HN;
+                c_hi = min(c_hi, k_live) - hf * HN;
                 const unsigned c_span = c_hi > c_lo ? (unsigned)(c_hi - c_lo) : 0u;
-                const bool masked = __any_sync(0xffffffffu, !(c_lo <= 0 && c_hi >= BN));
-                if (!(ok = wait_bar_warp(bar(P_S0 + jg % NB), (jg / NB) & 1, abort_flag, err))) break;
+                const bool masked = __any_sync(0xffffffffu, !(c_lo <= 0 && c_hi >= HN));
+                wait_bar_warp(bar(P_S0 + jg % NB), (jg / NB) & 1, abort_flag, err);
                 if (k_live < BN) {
                     // V rows behind the last key: zeros (this wait only orders the zeros after
                     // the loads; S could not be complete before them)
                     const int s = jg % C::STAGES;
-                    if (!(ok = wait_bar_warp(bar_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
-                    if (t < BN && t >= k_live) {
+                    wait_bar_warp(bar_full(s), (jg / C::STAGES) & 1, abort_flag, err);
+                    if (hf == 0 && t < BN && t >= k_live) {
 #pragma unroll
                         for (int x = 0; x < C::BOXES; ++x)
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
                                 *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::kTileKV_B + x * kBlk +
-                                                          (t >> 3) * kRow8 + (t & 7) * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                                          (t >> 3) * kRow8 + (t & 7) * 128 + q * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
                     }
                     ptx::fence_proxy_async_smem();
                 }
                 ptx::tc_fence_after();
                 if (warp_live) {
-                    uint32_t r[BN];
+                    float alpha = 1.f, sum = 0.f;
+                    bool rescale = false;
+                    uint32_t Pp[HN / 2];
+                    auto load = [&](uint32_t* r) {
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c) ptx::tmem_ld32p(buf + c * 32, r + c * 32);
-                    ptx::tmem_wait_ld();
-                    if (masked) {
+                        for (int c = 0; c < HN / 32; ++c) ptx::tmem_ld32p(buf + c * 32, r + c * 32);
+                        ptx::tmem_wait_ld();
+                        if (masked) {
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            r[c] = (unsigned)(c - c_lo) < c_span ? r[c] : __float_as_uint(-INFINITY);
-                    }
-                    float mx8[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < BN; c += 2)
-                        mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-                    float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                     fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-                    mx = mx == -INFINITY ? -INFINITY : mx * scale_log2;
-                    float alpha = 1.f;
-                    const bool rescale = mx > m_run + kRescaleLog2;
-                    if (rescale) {
-                        alpha = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - mx);
-                        m_run = mx;
-                    }
-                    const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                    const float2 sc2 = make_float2(scale_log2, scale_log2);
-                    const float2 nm2 = make_float2(-m_use, -m_use);
-                    float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                      make_float2(0.f, 0.f)};
-                    uint32_t Pp[BN / 2];
-#pragma unroll
-                    for (int c = 0; c < BN; c += 2) {
-                        const float2 x =
-                            __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nm2);
-                        const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-                        sum2[(c >> 1) & 3] = __fadd2_rn(sum2[(c >> 1) & 3], pp);
-                        Pp[c / 2] = pack2<kBF16>(pp.x, pp.y);
-                    }
-                    const float2 s2 = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
-                    l_run = l_run * alpha + (s2.x + s2.y);
-#pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) ptx::tmem_st32(buf + c * 32, Pp + c * 32);
-                    // rescale the O row before the next P V product accumulates into it
-                    if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-                        if (!(ok = wait_bar_warp(bar(P_PV0 + (jg - 1) % NB), ((jg - 1) / NB) & 1, abort_flag, err))) {
-                            ptx::tmem_wait_st();  // no TMEM store in flight at the release
-                            break;
+                            for (int c = 0; c < HN; ++c)
+                                r[c] = (unsigned)(c - c_lo) < c_span ? r[c] : __float_as_uint(-INFINITY);
                         }
+                    };
+                    auto exps = [&](const uint32_t* r) {
+                        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                        const float2 sc2 = make_float2(scale_log2, scale_log2);
+                        const float2 nm2 = make_float2(-m_use, -m_use);
+                        float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                          make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int c = 0; c < HN; c += 2) {
+                            const float2 x =
+                                __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nm2);
+                            const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                            sum2[(c >> 1) & 3] = __fadd2_rn(sum2[(c >> 1) & 3], pp);
+                            Pp[c / 2] = pack2<kBF16>(pp.x, pp.y);
+                        }
+                        const float2 s2 = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
+                        sum = s2.x + s2.y;
+                    };
+                    bool done = false;
+                    // both threads of a row have the same m, so both warps decide alike
+                    if (j > 0 && !__any_sync(0xffffffffu, row_valid && m_run == -INFINITY)) {
+                        uint32_t r[HN];
+                        load(r);
+                        exps(r);
+                        __syncwarp();
+                        done = ptx::named_bar_and(pair, 64, !(row_valid && sum > kMaxSum));
+                    }
+                    if (!done) {
+                        uint32_t r[HN];
+                        load(r);
+                        float mx8[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < HN; c += 2)
+                            mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                        float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                        // the max of both halves, by way of the second half's thread
+                        if (hf == 1) *xch = mx;
+                        __syncwarp();
+                        ptx::named_bar_sync(pair, 64);
+                        if (hf == 0) *xch = mx = fmaxf(mx, *xch);
+                        __syncwarp();
+                        ptx::named_bar_sync(pair, 64);
+                        if (hf == 1) mx = *xch;
+                        mx = mx == -INFINITY ? -INFINITY : mx * scale_log2;
+                        rescale = mx > m_run;
+                        if (rescale) {
+                            alpha = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - mx);
+                            m_run = mx;
+                        }
+                        exps(r);
+                    }
+                    l_run = l_run * alpha + sum;
+#pragma unroll
+                    for (int c = 0; c < HN / 2; c += 16) ptx::tmem_st16(buf + c, *reinterpret_cast<uint32_t(*)[16]>(Pp + c));
+                    // rescale the O row before the next P V product accumulates into it (each
+                    // thread half of the columns)
+                    if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+                        wait_bar_warp(bar(P_PV0 + (jg - 1) % NB), ((jg - 1) / NB) & 1, abort_flag, err);
                         ptx::tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
+                        for (int c = 0; c < D / 64; ++c) {
                             uint32_t o[32];
-                            ptx::tmem_ld32p(tmem + C::TM_O + lane_off + c * 32, o);
+                            const uint32_t at = tmem + C::TM_O + lane_off + hf * (D / 2) + c * 32;
+                            ptx::tmem_ld32p(at, o);
                             ptx::tmem_wait_ld();
 #pragma unroll
                             for (int kk = 0; kk < 32; ++kk) o[kk] = __float_as_uint(__uint_as_float(o[kk]) * alpha);
-                            ptx::tmem_st32(tmem + C::TM_O + lane_off + c * 32, o);
+                            ptx::tmem_st32(at, o);
                         }
                     }
                     ptx::tmem_wait_st();
@@ -499,13 +550,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(P_P0 + jg % NB));
             }
-            if (!ok) break;
-            // the slot's values of two items ago must have been read (items of a tile or two can be
-            // through here before the epilogue of the first of them has begun)
-            if (ka > 1 && !(ok = wait_bar_warp(bar(P_MR0 + (ka & 1)), ((ka >> 1) - 1) & 1, abort_flag, err))) break;
-            ml[(ka & 1) * BM + t] = make_float2(m_run, l_run);
+            // (m, l) of the row to the epilogue, once the slot's values of two items ago have been
+            // read (items of a tile or two can be through here before the epilogue of the first
+            // of them has begun)
+            if (hf == 1) *xch = l_run;
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(P_ML0 + (ka & 1)));
+            ptx::named_bar_sync(pair, 64);
+            if (hf == 0) {
+                if (ka > 1) wait_bar_warp(bar(P_MR0 + (ka & 1)), ((ka >> 1) - 1) & 1, abort_flag, err);
+                ml[(ka & 1) * BM + t] = make_float2(m_run, l_run + *xch);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(P_ML0 + (ka & 1)));
+            }
+            __syncwarp();
+            ptx::named_bar_sync(pair, 64);  // the exchange word is free again
             ++ka;
         }
     } else {
@@ -513,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O = acc / l and LSE = (m + log2 l) ln 2 of a whole item; of a cut one the raw
         // accumulator with (m, l), and the last part to arrive joins them.  Meanwhile the
         // softmax warps are at the next item; its first P V product waits for O to be read.
-        const int t = threadIdx.x - 128;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        const int t = threadIdx.x - kWarpEpi * 32;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const int ti = t / g, th = t - ti * g;  // token and head of the row
         const bool wide = ((reinterpret_cast<uintptr_t>(a.O) | (a.o.tok * 2) | (a.o.head * 2)) & 31) == 0;
@@ -607,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::named_bar_sync(kEpiBarrier, 128);
                 if (*last_flag) {
                     __threadfence();
-                    join_parts<T, 128, BM, D>(a, plan, w.t, w.hd * g, g, rows, first, count, t,
+                    join_parts<T, 128, BM, D, 4>(a, plan, w.t, w.hd * g, g, rows, first, count, t,
                                               ml + ((ka - 1) & 1) * BM, [] {
                                                   __syncwarp();
                                                   ptx::named_bar_sync(kEpiBarrier, 128);

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads)
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join_parts<T, kThreads, BM, D>(a, plan, w.t, head0, gh, rows, first, count, tid, s_row,
+                join_parts<T, kThreads, BM, D, 8>(a, plan, w.t, head0, gh, rows, first, count, tid, s_row,
                                                [] { __syncthreads(); });
             }
         }
