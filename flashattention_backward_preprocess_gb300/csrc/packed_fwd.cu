@@ -37,10 +37,10 @@ namespace fa {
 namespace {
 
 constexpr int BM = 128;  // rows per tile
-// warps 0-7 softmax, 8-11 epilogue, 12 TMA, 13 S products and TMEM, 14 P V products (15 only
-// makes the warpgroup whole)
+// warps 0-7 softmax, 8-11 epilogue, 12 loads of Q and K, 13 S products and TMEM, 14 P V products,
+// 15 loads of V
 constexpr int kThreads = 512;
-constexpr int kWarpEpi = 8, kWarpTma = 12, kWarpMma = 13, kWarpPv = 14;
+constexpr int kWarpEpi = 8, kWarpLoadK = 12, kWarpMma = 13, kWarpPv = 14, kWarpLoadV = 15;
 // registers per thread of the two softmax warpgroups, the epilogue and the last one: together
 // 4 x 128, what the block is launched with
 constexpr int kRegsSoft = 152, kRegsEpi = 120, kRegsOther = 88;
@@ -67,6 +67,8 @@ struct PCfg {
     static constexpr uint32_t OFF_ROW = OFF_V + STAGES * kTileKV_B;
     static constexpr uint32_t OFF_XCH = OFF_ROW + 2 * BM * 8;
     static constexpr uint32_t OFF_BAR = OFF_XCH + BM * 4;
+    // V(j)'s slot is past V(j - STAGES) once S(j) is complete (the softmax warps' rare waits for V)
+    static_assert(STAGES >= NBUF, "see above");
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
@@ -82,7 +84,7 @@ enum {
     P_OFREE,               // O of an item read (4 epilogue warps)
     P_ML0,                 // max and sum of an item's rows written (4 softmax warps), 2 slots
     P_MR0 = P_ML0 + 2,     // and read by the epilogue (4 warps), 2 slots
-    P_STAGE0 = P_MR0 + 2   // STAGES "full", then STAGES "empty"
+    P_SLOT0 = P_MR0 + 2    // STAGES "full" and STAGES "empty" of the K ring, then of the V ring
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -152,10 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // K / V tile layout: bytes from a 64-column block to the next, and from 8 rows to the next 8
     constexpr uint32_t kBlk = kGroup ? 1024 : C::kBoxKV_B;
     constexpr uint32_t kRow8 = kGroup ? 1024 * C::BOXES : 1024;
-    constexpr int kPerPage = kGroup ? 2 : 2 * C::BOXES;      // boxes per page
+    constexpr int kPerPage = kGroup ? 1 : C::BOXES;          // boxes per page of K or V
     constexpr int kPieces = (BN / 8 * kPerPage + 31) / 32;  // and tile per producer lane (pages of 8 rows)
     constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
-    constexpr int kNumBars = P_STAGE0 + 2 * C::STAGES;
+    constexpr int kNumBars = P_SLOT0 + 4 * C::STAGES;
     constexpr uint32_t OFF_MISC = C::OFF_BAR + kNumBars * 8;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
@@ -164,8 +166,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC + 4);
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
     auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
-    auto bar_full = [&](int s) { return bar(P_STAGE0 + s); };
-    auto bar_empty = [&](int s) { return bar(P_STAGE0 + C::STAGES + s); };
+    // a ring each for K and V: a K slot is free once S is computed, well before V's
+    auto k_full = [&](int s) { return bar(P_SLOT0 + s); };
+    auto k_empty = [&](int s) { return bar(P_SLOT0 + C::STAGES + s); };
+    auto v_full = [&](int s) { return bar(P_SLOT0 + 2 * C::STAGES + s); };
+    auto v_empty = [&](int s) { return bar(P_SLOT0 + 3 * C::STAGES + s); };
     const int g = a.H / a.H_kv;
     unsigned int* err = a.err;
 
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((sbase & 1023u) != 0) atomicOr(err, kErrSmemAlign);
         *abort_flag = (sbase & 1023u) != 0;
         for (int i = 0; i < kNumBars; ++i)
-            ptx::mbar_init(bar(i), i >= P_P0 && i < P_P0 + 3 ? 8u : i >= P_OFREE && i < P_STAGE0 ? 4u : 1u);
+            ptx::mbar_init(bar(i), i >= P_P0 && i < P_P0 + 3 ? 8u : i >= P_OFREE && i < P_SLOT0 ? 4u : 1u);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -200,129 +205,102 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
     // CTA (jg), per-item ones its segments with work (ka).
-    if (warp >= kWarpTma) {
+    if (warp >= kWarpLoadK) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kWarpTma) {
-        // ------------------------------------------------------------ producer
-        // Two streams over the same segments, polled in turn: the Q tile (once the previous
-        // item's S products are done) and the K / V ring.  Lane 0 polls; every lane issues its
-        // own boxes of a K / V tile.
-        if (!*abort_flag) {
-            FwdWalk wq, wk;
-            bool q_more = wq.init(share, blockIdx.x, a.H_kv, geo.overhead),
-                 kv_more = wk.init(share, blockIdx.x, a.H_kv, geo.overhead);
-            while (q_more && wq.tiles() == 0) q_more = wq.next();
-            while (kv_more && wk.tiles() == 0) kv_more = wk.next();
-            int q_act = 0, jg = 0, kj = kv_more ? wk.j0 : 0;
-            const int pr = kPaged ? min(a.page_size, BN) : BN;  // rows per box
-            // paged: table entries of this lane's boxes of the next tile.  They are only loaded here
-            // and looked at when the tile is issued, so the load's latency passes meanwhile.
-            int page[kPieces];
-            int live = 0;  // boxes of that tile that hold a key
-            uint32_t bytes = 2 * C::kTileKV_B;
-            auto look_up = [&]() {
-                if constexpr (kPaged) {
-                    const int n0 = (wk.t.n_first + kj) * BN;
-                    live = min((wk.t.S_k - n0 + pr - 1) / pr, BN / pr);
-                    bytes = (uint32_t)(live * pr) * 128u * 2u * C::BOXES;
-                    const int* row = a.table + (size_t)wk.t.n * a.max_pages;
+    if (warp == kWarpLoadK || warp == kWarpLoadV) {
+        // ------------------------------------------------------------ producers
+        // One warp loads the Q tile of each item (once the previous item's S products are done)
+        // and its K tiles, the other the V tiles; every lane issues its own boxes of a tile.
+        const bool is_v = warp == kWarpLoadV;
+        const CUtensorMap* map = is_v ? &tmV : &tmK;
+        const uint32_t ring = sbase + (is_v ? C::OFF_V : C::OFF_K);
+        const int hs = (int)(is_v ? a.v.head : a.k.head);
+        const int pr = kPaged ? min(a.page_size, BN) : BN;           // rows per box
+        const int per_tile = BN / pr;                                // pages per tile
+        const int tiles_page = kPaged ? max(a.page_size / BN, 1) : 1;  // or tiles per page
+        int q_act = 0, jg = 0;  // Q tiles and ring tiles loaded
+        // paged: table entries of this lane's boxes of the next tile.  They are only loaded here
+        // and looked at when the tile is issued, so the load's latency passes meanwhile.
+        int page[kPieces];
+        int live = 0;  // boxes of that tile that hold a key
+        FwdWalk w;
+        bool ok = !*abort_flag;
+        bool more = ok && w.init(share, blockIdx.x, a.H_kv, geo.overhead);
+        while (more && w.tiles() == 0) more = w.next();
+        int j = more ? w.j0 : 0;
+        auto look_up = [&]() {
+            if constexpr (kPaged) {
+                const int tile = w.t.n_first + j;
+                live = min((w.t.S_k - tile * BN + pr - 1) / pr, per_tile);
+                const int* row = a.table + (size_t)w.t.n * a.max_pages;
+                const int e0 = tiles_page > 1 ? tile / tiles_page : tile * per_tile;
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int b = (lane + 32 * i) / kPerPage;
-                        page[i] = b < live ? page_entry(row, n0 + b * pr, a.page_size, a.max_pages) : -1;
-                    }
+                for (int i = 0; i < kPieces; ++i) {
+                    const int b = (lane + 32 * i) / kPerPage;
+                    page[i] = b < live && e0 + b < a.max_pages ? row[e0 + b] : -1;
                 }
-            };
-            if (kv_more) look_up();
-            uint64_t t0 = ptx::globaltimer();
-            uint32_t spins = 0;
-            while (q_more || kv_more) {
-                int act = 0;
-                if (lane == 0) {
-                    if (q_more && (q_act == 0 || ptx::mbar_test_wait(bar(P_QE), (q_act - 1) & 1))) act |= 1;
-                    if (kv_more && (jg < C::STAGES ||
-                                    ptx::mbar_test_wait(bar_empty(jg % C::STAGES), ((jg / C::STAGES) - 1) & 1)))
-                        act |= 2;
-                }
-                act = __shfl_sync(0xffffffffu, act, 0);
-                if (act & 1) {
-                    if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(geo.tpt * g) * 128u * C::BOXES);
-                        for (int x = 0; x < C::BOXES; ++x)
-                            ptx::tma_load_3d(sbase + C::OFF_Q + x * C::kBoxQ_B, &tmQ, x * 64, wq.hd * g, wq.t.q_tok,
-                                             bar(P_Q));
-                    }
-                    ++q_act;
-                    do q_more = wq.next();
-                    while (q_more && wq.tiles() == 0);
-                    // the next item's Q tile to L2, so that its load, which the S products wait
-                    // for, is short
-                    if (q_more && lane < C::BOXES) tma_prefetch_3d(&tmQ, lane * 64, wq.hd * g, wq.t.q_tok);
-                }
-                if (act & 2) {
-                    const int s = jg % C::STAGES;
-                    const int n0 = (wk.t.n_first + kj) * BN;
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full(s), bytes);
-                    __syncwarp();
-                    if constexpr (kPaged) {
-                        // keys before the window of the unit's first row may have lost their pages:
-                        // they are masked, and read as zeros (page `pages`) whatever the table says
-                        const int k_lo = a.window > 0 ? wk.t.pos0 - a.window + 1 : 0;
-                        bool bad = false;
+            }
+        };
+        if (more) look_up();
+        while (more) {
+            if (!is_v && j == w.j0) {
+                if (q_act > 0 && !(ok = wait_bar_warp(bar(P_QE), (q_act - 1) & 1, abort_flag, err))) break;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(geo.tpt * g) * 128u * C::BOXES);
+                __syncwarp();
+                if (lane < C::BOXES)
+                    ptx::tma_load_3d(sbase + C::OFF_Q + lane * C::kBoxQ_B, &tmQ, lane * 64, w.hd * g, w.t.q_tok, bar(P_Q));
+                ++q_act;
+            }
+            const int s = jg % C::STAGES;
+            const uint32_t full = is_v ? v_full(s) : k_full(s);
+            if (jg >= C::STAGES &&
+                !(ok = wait_bar_warp(is_v ? v_empty(s) : k_empty(s), (jg / C::STAGES - 1) & 1, abort_flag, err)))
+                break;
+            const int tile = w.t.n_first + j;
+            const uint32_t dst = ring + s * C::kTileKV_B;
+            if (lane == 0)
+                ptx::mbar_arrive_expect_tx(full, kPaged ? (uint32_t)(live * pr) * 128u * C::BOXES : C::kTileKV_B);
+            __syncwarp();
+            if constexpr (kPaged) {
+                // keys before the window of the unit's first row may have lost their pages: they
+                // are masked, and read as zeros (page `pages`) whatever the table says
+                const int k_lo = a.window > 0 ? w.t.pos0 - a.window + 1 : 0;
+                const int row8 = tiles_page > 1 ? tile % tiles_page * (BN / 8) : 0;
+                bool bad = false;
 #pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            const int e = lane + 32 * i, b = e / kPerPage;
-                            if (b >= live) continue;
-                            const int pg = n0 + (b + 1) * pr <= k_lo ? a.pages : page_checked(page[i], a.pages, &bad);
-                            const uint32_t dst = sbase + ((e & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B;
-                            const CUtensorMap* map = (e & 1) ? &tmV : &tmK;
-                            const int row = (n0 + b * pr) % a.page_size;
-                            if constexpr (kGroup) {
-                                const long long hs = (e & 1) ? a.v.head : a.k.head;
-                                tma_load_5d(dst + b * pr * (D * 2), map, (int)(wk.hd * hs), 0, 0, row / 8, pg,
-                                            bar_full(s));
-                            } else {
-                                const int x = (e >> 1) % C::BOXES;
-                                tma_load_4d(dst + x * C::kBoxKV_B + b * pr * 128, map, x * 64, wk.hd, row, pg,
-                                            bar_full(s));
-                            }
-                        }
-                        if (bad) atomicOr(err, kErrPage);
-                    } else if (lane < 2 * C::BOXES) {
-                        const int x = lane >> 1;
-                        ptx::tma_load_3d(sbase + ((lane & 1) ? C::OFF_V : C::OFF_K) + s * C::kTileKV_B +
-                                             x * C::kBoxKV_B,
-                                         (lane & 1) ? &tmV : &tmK, x * 64, wk.hd, wk.t.k_base + n0, bar_full(s));
-                    }
-                    ++jg;
-                    if (++kj == wk.j1) {
-                        do kv_more = wk.next();
-                        while (kv_more && wk.tiles() == 0);
-                        kj = wk.j0;
-                    }
-                    if (kv_more) look_up();
-                }
-                int stop = 0;
-                if (lane == 0) {
-                    if (act) {
-                        t0 = ptx::globaltimer();
-                    } else if (++spins % 64 == 0) {
-                        if (*abort_flag) stop = 1;
-                        if (ptx::globaltimer() - t0 > kWaitLimitNs) {
-                            *abort_flag = 1;
-                            atomicOr(err, kErrTimeout);
-                            stop = 1;
-                        }
+                for (int i = 0; i < kPieces; ++i) {
+                    const int c = lane + 32 * i, b = c / kPerPage;
+                    if (b >= live) continue;
+                    const int pg = tile * BN + (b + 1) * pr <= k_lo ? a.pages : page_checked(page[i], a.pages, &bad);
+                    if constexpr (kGroup) {
+                        tma_load_5d(dst + b * pr * (D * 2), map, w.hd * hs, 0, 0, row8, pg, full);
+                    } else {
+                        const int x = c % kPerPage;
+                        tma_load_4d(dst + x * C::kBoxKV_B + b * pr * 128, map, x * 64, w.hd, row8 * 8, pg, full);
                     }
                 }
-                if (__shfl_sync(0xffffffffu, stop, 0)) break;
+                if (bad) atomicOr(err, kErrPage);
+            } else if (lane < C::BOXES) {
+                ptx::tma_load_3d(dst + lane * C::kBoxKV_B, map, lane * 64, w.hd, w.t.k_base + tile * BN, full);
             }
-            // never leave copies in flight into shared memory that is about to be released
-            if (lane == 0) {
-                if (q_act > 0) drain_wait(bar(P_Q), (q_act - 1) & 1);
-                for (int j = jg - C::STAGES < 0 ? 0 : jg - C::STAGES; j < jg; ++j)
-                    drain_wait(bar_full(j % C::STAGES), (j / C::STAGES) & 1);
+            ++jg;
+            if (++j == w.j1) {
+                do more = w.next();
+                while (more && w.tiles() == 0);
+                if (more) {
+                    j = w.j0;
+                    // the next item's Q tile to L2: the S products wait for its load
+                    if (!is_v && lane < C::BOXES) tma_prefetch_3d(&tmQ, lane * 64, w.hd * g, w.t.q_tok);
+                }
             }
+            if (more) look_up();
+        }
+        __syncwarp();
+        // never leave copies in flight into shared memory that is about to be released
+        if (lane == 0) {
+            if (q_act > 0) drain_wait(bar(P_Q), (q_act - 1) & 1);
+            for (int k = jg - C::STAGES < 0 ? 0 : jg - C::STAGES; k < jg; ++k)
+                drain_wait(is_v ? v_full(k % C::STAGES) : k_full(k % C::STAGES), (k / C::STAGES) & 1);
         }
         __syncwarp();
     } else if (warp == kWarpMma || warp == kWarpPv) {
@@ -347,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait_bar(bar(P_Q), ka & 1, abort_flag, err))) break;
                     for (int j = 0; j < nt; ++j, ++jg) {
                         const int s = jg % C::STAGES;
-                        if (!(ok = wait_bar(bar_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
+                        if (!(ok = wait_bar(k_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
                         if (jg >= NB && !(ok = wait_bar(bar(P_PV0 + jg % NB), (jg / NB - 1) & 1, abort_flag, err)))
                             break;
                         ptx::tc_fence_after();
@@ -360,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         ID_S, kk > 0);
                         }
                         ptx::mma_commit(bar(P_S0 + jg % NB));
+                        ptx::mma_commit(k_empty(s));
                     }
                     if (!ok) break;
                     ptx::mma_commit(bar(P_QE));
@@ -374,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (nt == 0) continue;
                     for (int j = 0; j < nt; ++j, ++jg) {
                         const int s = jg % C::STAGES;
+                        if (!(ok = wait_bar(v_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
                         if (!(ok = wait_bar(bar(P_P0 + jg % NB), (jg / NB) & 1, abort_flag, err))) break;
                         // the first product of an item overwrites O: the epilogue of the
                         // previous item must have read it
@@ -385,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         desc_add(dV_mn, (uint32_t)s * C::kTileKV_B + kk * 2 * kRow8), ID_PV,
                                         (j > 0 || kk > 0) ? 1u : 0u);
                         ptx::mma_commit(bar(P_PV0 + jg % NB));
-                        ptx::mma_commit(bar_empty(s));
+                        ptx::mma_commit(v_empty(s));
                     }
                     if (!ok) break;
                     ptx::mma_commit(bar(P_OFULL));
@@ -442,10 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool masked = __any_sync(0xffffffffu, !(c_lo <= 0 && c_hi >= HN));
                 wait_bar_warp(bar(P_S0 + jg % NB), (jg / NB) & 1, abort_flag, err);
                 if (k_live < BN) {
-                    // V rows behind the last key: zeros (this wait only orders the zeros after
-                    // the loads; S could not be complete before them)
+                    // V rows behind the last key: zeros, once the loads have landed
                     const int s = jg % C::STAGES;
-                    wait_bar_warp(bar_full(s), (jg / C::STAGES) & 1, abort_flag, err);
+                    wait_bar_warp(v_full(s), (jg / C::STAGES) & 1, abort_flag, err);
                     if (hf == 0 && t < BN && t >= k_live) {
 #pragma unroll
                         for (int x = 0; x < C::BOXES; ++x)
@@ -699,7 +678,7 @@ bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, 
 template <typename T, int D, bool kPaged, bool kGroup>
 cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     using C = PCfg<D>;
-    constexpr uint32_t kSmem = C::OFF_BAR + (P_STAGE0 + 2 * C::STAGES) * 8 + 16;
+    constexpr uint32_t kSmem = C::OFF_BAR + (P_SLOT0 + 4 * C::STAGES) * 8 + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
     const int g = a.H / a.H_kv;
     FwdGeom geo;
