@@ -530,6 +530,7 @@ struct BwdPlan {
     long long rows;       // max_units * 128
     int max_units, max_keys, max_work, max_cut, max_slots;
     int shares;           // CTAs the iterations are spread over
+    int one_round;        // CTAs of the main kernel (works x heads) that run at the same time
     int min_its;          // iterations a part has at least
 };
 
@@ -554,6 +555,7 @@ inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, B
     // most, a cut tile has x > 1 and ceil(x) <= 2x parts.  On CUDA cores a plan tile is several
     // CTAs and a CTA's fixed cost is small: two rounds of CTAs even out better.
     q.shares = tensor_cores ? sm_count() : (2 * sm_count() + simt_pieces(a.d) - 1) / simt_pieces(a.d);
+    q.one_round = tensor_cores ? sm_count() : sm_count() / simt_pieces(a.d);
     q.min_its = 4;
     q.max_cut = q.shares / a.H_kv + 1;
     q.max_work = q.max_keys + q.max_cut;

@@ -25,7 +25,8 @@ constexpr int lanes_per_row(int chunks) {
     return l;
 }
 
-constexpr int kRowsPerBlock = 16;  // tile rows of one block; its rows are kRowsPerBlock x H
+constexpr int kRowsPerBlock = 8;  // tile rows of one block; its rows are kRowsPerBlock x H
+constexpr int kBatch = 4;         // rows whose loads a thread has in flight together
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_preprocess_kernel(const PackedBwd a, const BwdPlan p) {
@@ -40,38 +41,53 @@ __global__ void __launch_bounds__(kThreads) packed_preprocess_kernel(const Packe
     const QueryTile t = p.query[u];
     const int lane = threadIdx.x % LPR;
     const int total = kRowsPerBlock * a.H;
-    // whole groups of LPR lanes stay together: total rows are walked in steps of the block's groups
-    for (int e0 = 0; e0 < total; e0 += kThreads / LPR) {
-        const int e = e0 + threadIdx.x / LPR;
-        const int r = r0 + e / a.H, h = e % a.H;
-        const bool in = e < total;
-        const bool valid = in && r < t.rows;
-        float acc = 0.f;
-        if (valid) {
+    // groups of LPR lanes take a row each; kBatch rows' loads go out before the first is used
+    constexpr int G = kThreads / LPR, CH = (CPR + LPR - 1) / LPR;  // rows per step, pieces per lane
+    for (int e0 = 0; e0 < total; e0 += kBatch * G) {
+        int4 x[kBatch][CH], y[kBatch][CH];
+        float acc[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + b * G + threadIdx.x / LPR, r = r0 + e / a.H, h = e % a.H;
+            const bool valid = e < total && r < t.rows;
             const T* dO = static_cast<const T*>(a.dO) + (long long)(t.q_tok + r) * a.sdo.tok + (long long)h * a.sdo.head;
             const T* O = static_cast<const T*>(a.O) + (long long)(t.q_tok + r) * a.so.tok + (long long)h * a.so.head;
-            float* z = p.dqacc + (((long long)u * kBwdTile + r) * a.H + h) * D;
 #pragma unroll
-            for (int ch = lane; ch < CPR; ch += LPR) {
-                const int4 x = __ldcs(reinterpret_cast<const int4*>(dO) + ch);
-                const int4 y = __ldcs(reinterpret_cast<const int4*>(O) + ch);
-                const T* tx = reinterpret_cast<const T*>(&x);
-                const T* ty = reinterpret_cast<const T*>(&y);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k)
-                    acc = fmaf(TypeTraits<T>::to_f32(tx[k]), TypeTraits<T>::to_f32(ty[k]), acc);
-#pragma unroll
-                for (int k = 0; k < VEC / 4; ++k)
-                    reinterpret_cast<float4*>(z)[ch * (VEC / 4) + k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < CH; ++c) {
+                const int ch = lane + c * LPR;
+                const bool in = valid && (CPR % LPR == 0 || ch < CPR);
+                x[b][c] = in ? __ldcs(reinterpret_cast<const int4*>(dO) + ch) : make_int4(0, 0, 0, 0);
+                y[b][c] = in ? __ldcs(reinterpret_cast<const int4*>(O) + ch) : make_int4(0, 0, 0, 0);
             }
         }
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o, LPR);
-        if (in && lane == 0) {
-            const long long row = h * p.rows + (long long)u * kBwdTile + r;
-            const float l = valid ? a.LSE[(size_t)h * a.T_q + t.q_tok + r] : -INFINITY;
-            p.D[row] = acc;
-            p.lse2[row] = (l == -INFINITY || isnan(l)) ? INFINITY : l * 1.4426950408889634f;
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + b * G + threadIdx.x / LPR, r = r0 + e / a.H, h = e % a.H;
+            const bool valid = e < total && r < t.rows;
+            float* z = p.dqacc + (((long long)u * kBwdTile + r) * a.H + h) * D;
+            acc[b] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int ch = lane + c * LPR;
+                const T* tx = reinterpret_cast<const T*>(&x[b][c]);
+                const T* ty = reinterpret_cast<const T*>(&y[b][c]);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    acc[b] = fmaf(TypeTraits<T>::to_f32(tx[k]), TypeTraits<T>::to_f32(ty[k]), acc[b]);
+                if (valid && (CPR % LPR == 0 || ch < CPR)) {
+#pragma unroll
+                    for (int k = 0; k < VEC / 4; ++k)
+                        reinterpret_cast<float4*>(z)[ch * (VEC / 4) + k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) acc[b] += __shfl_xor_sync(0xffffffffu, acc[b], o, LPR);
+            if (e < total && lane == 0) {
+                const long long row = h * p.rows + (long long)u * kBwdTile + r;
+                const float l = valid ? a.LSE[(size_t)h * a.T_q + t.q_tok + r] : -INFINITY;
+                p.D[row] = acc[b];
+                p.lse2[row] = (l == -INFINITY || isnan(l)) ? INFINITY : l * 1.4426950408889634f;
+            }
         }
     }
 }
@@ -141,22 +157,37 @@ __global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedBwd a, 
     const int r0 = (blockIdx.x % (kBwdTile / kRowsPerBlock)) * kRowsPerBlock;
     const QueryTile t = p.query[u];
     const int rows = min(kRowsPerBlock, t.rows - r0);
-    for (int e = threadIdx.x; e < rows * a.H * C8; e += kThreads) {
-        const int c = e % C8, rh = e / C8;
-        const int r = r0 + rh / a.H, h = rh % a.H;
-        const float4* s = reinterpret_cast<const float4*>(p.dqacc + (((long long)u * kBwdTile + r) * a.H + h) * D) + 2 * c;
-        const float4 x = __ldcs(s), y = __ldcs(s + 1);
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        T* dst = static_cast<T*>(a.dQ) + (long long)(t.q_tok + r) * a.sdq.tok + (long long)h * a.sdq.head + 8 * c;
-        if constexpr (sizeof(T) == 4) {
-            float4* o = reinterpret_cast<float4*>(dst);
-            o[0] = make_float4(v[0] * a.scale, v[1] * a.scale, v[2] * a.scale, v[3] * a.scale);
-            o[1] = make_float4(v[4] * a.scale, v[5] * a.scale, v[6] * a.scale, v[7] * a.scale);
-        } else {
-            alignas(16) T o[8];
+    const int total = rows * a.H * C8;
+    for (int e0 = threadIdx.x; e0 < total; e0 += kBatch * kThreads) {
+        float4 x[kBatch], y[kBatch];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = TypeTraits<T>::from_f32(v[k] * a.scale);
-            __stcs(reinterpret_cast<int4*>(dst), *reinterpret_cast<const int4*>(o));
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + b * kThreads;
+            if (e < total) {
+                // rows of the block are consecutive in the accumulator
+                const float4* s = reinterpret_cast<const float4*>(p.dqacc + ((long long)u * kBwdTile + r0) * a.H * D) + 2ll * e;
+                x[b] = __ldcs(s);
+                y[b] = __ldcs(s + 1);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + b * kThreads;
+            if (e >= total) break;
+            const int c = e % C8, rh = e / C8;
+            const int r = r0 + rh / a.H, h = rh % a.H;
+            const float v[8] = {x[b].x, x[b].y, x[b].z, x[b].w, y[b].x, y[b].y, y[b].z, y[b].w};
+            T* dst = static_cast<T*>(a.dQ) + (long long)(t.q_tok + r) * a.sdq.tok + (long long)h * a.sdq.head + 8 * c;
+            if constexpr (sizeof(T) == 4) {
+                float4* o = reinterpret_cast<float4*>(dst);
+                o[0] = make_float4(v[0] * a.scale, v[1] * a.scale, v[2] * a.scale, v[3] * a.scale);
+                o[1] = make_float4(v[4] * a.scale, v[5] * a.scale, v[6] * a.scale, v[7] * a.scale);
+            } else {
+                alignas(16) T o[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = TypeTraits<T>::from_f32(v[k] * a.scale);
+                __stcs(reinterpret_cast<int4*>(dst), *reinterpret_cast<const int4*>(o));
+            }
         }
     }
 }

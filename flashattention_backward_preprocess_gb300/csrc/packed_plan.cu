@@ -139,6 +139,8 @@ __device__ __forceinline__ bool seq_at(const PackedBwd& a, int n, Seq& s) {
 }
 
 constexpr int kBuckets = 2048;
+constexpr int kBwdSmemSeqs = 2047;  // sequences whose tile offsets are kept in shared memory
+constexpr int kSmallPlan = 256;     // threads of a plan block that has no more of anything to place
 
 // Block 0 plans; blocks 1 .. map_blocks write tensor maps, one warp a map; the rest fill.
 __global__ void __launch_bounds__(kPlanThreads, 1)
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (blockIdx.x > 0) {
         __shared__ __align__(128) uint32_t s_map[kPlanThreads / 32][32];
         const int lane = tid & 31, w = tid >> 5;
-        const long long i = (long long)(blockIdx.x - 1) * (kPlanThreads / 32) + w;
+        const long long i = (long long)(blockIdx.x - 1) * (blockDim.x / 32) + w;
         const int n = (int)(i >> 2), which = (int)(i & 3);
         if (n >= a.N) return;
         Seq s;
@@ -170,29 +172,36 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
                   static_cast<const char*>(base) + (long long)(q ? s.q0 : s.k0) * str.tok * 2, len, lane);
         return;
     }
-    __shared__ int s_sum[33];
+    __shared__ long long s_sum[33];
     __shared__ int s_count[kBuckets];
-    // first query and key tile of each sequence
-    int UQ = 0, UK = 0;
+    __shared__ int s_first[2][kBwdSmemSeqs + 1];
+    const int threads = blockDim.x;
+    // first query and key tile of each sequence (in shared memory where they fit)
+    int* first_q = a.N <= kBwdSmemSeqs ? s_first[0] : p.seq_q;
+    int* first_k = a.N <= kBwdSmemSeqs ? s_first[1] : p.seq_k;
+    long long tiles = 0;  // query tiles | key tiles << 32
     bool bad = false;
-    for (int n0 = 0; n0 < a.N; n0 += kPlanThreads) {
+    for (int n0 = 0; n0 < a.N; n0 += threads) {
         const int n = n0 + tid;
         Seq s = {0, 0, 0, 0};
         if (n < a.N && !seq_at(a, n, s)) bad = true;
-        int tq, tk;
-        const int uq = block_excl_scan((s.nq + kBwdTile - 1) / kBwdTile, s_sum, &tq);
-        const int uk = block_excl_scan((s.nk + kBwdTile - 1) / kBwdTile, s_sum, &tk);
+        long long total;
+        const long long at = tiles + block_excl_scan((long long)((s.nq + kBwdTile - 1) / kBwdTile) |
+                                                         (long long)((s.nk + kBwdTile - 1) / kBwdTile) << 32,
+                                                     s_sum, &total);
         if (n < a.N) {
-            p.seq_q[n] = UQ + uq;
-            p.seq_k[n] = UK + uk;
+            first_q[n] = (int)at;
+            first_k[n] = (int)(at >> 32);
+            p.seq_q[n] = (int)at;
         }
-        UQ += tq;
-        UK += tk;
+        tiles += total;
     }
+    int UQ = (int)tiles, UK = (int)(tiles >> 32);
     if (tid == 0) {
+        first_q[a.N] = UQ;
+        first_k[a.N] = UK;
         p.seq_q[a.N] = UQ;
-        p.seq_k[a.N] = UK;
-        if (p.ticket) *p.ticket = 0u;
+        *p.ticket = 0u;
     }
     if (__syncthreads_or(bad)) {
         if (tid == 0) atomicOr(a.err, kErrLengths);
@@ -200,26 +209,25 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     }
     if (tid == 0) p.head[0] = UQ;
     if (a.deterministic)
-        for (long long i = tid; i < (long long)a.H * p.max_units; i += kPlanThreads) p.sem[i] = 0u;
-    for (int i = tid; i < kBuckets; i += kPlanThreads) s_count[i] = 0;
-    __syncthreads();
-    for (int u = tid; u < UQ; u += kPlanThreads) {
-        const int n = find_seq(p.seq_q, a.N, u);
-        const int i0 = (u - p.seq_q[n]) * kBwdTile, q0 = a.cu_q[n], nq = a.cu_q[n + 1] - q0;
+        for (long long i = tid; i < (long long)a.H * p.max_units; i += threads) p.sem[i] = 0u;
+    for (int u = tid; u < UQ; u += threads) {
+        const int n = find_seq(first_q, a.N, u);
+        const int i0 = (u - first_q[n]) * kBwdTile, q0 = a.cu_q[n], nq = a.cu_q[n + 1] - q0;
         p.query[u] = {q0 + i0, min(kBwdTile, nq - i0)};
     }
     long long its = 0;
-    for (int v = tid; v < UK; v += kPlanThreads) {
-        const int n = find_seq(p.seq_k, a.N, v);
+    int mine = 0;  // query tiles of the thread's key tile in the first round
+    for (int v = tid; v < UK; v += threads) {
+        const int n = find_seq(first_k, a.N, v);
         Seq s;
         seq_at(a, n, s);
         KeyTile t;
         t.n = n;
-        t.n0 = (v - p.seq_k[n]) * kBwdTile;
+        t.n0 = (v - first_k[n]) * kBwdTile;
         t.k_tok = s.k0 + t.n0;
         t.S_q = s.nq;
         t.S_k = s.nk;
-        t.unit0 = p.seq_q[n];
+        t.unit0 = first_q[n];
         Shape sh;
         sh.S_q = s.nq;
         sh.S_k = s.nk;
@@ -230,61 +238,80 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         t.its = hi > lo ? (hi + kBwdTile - 1) / kBwdTile - lo / kBwdTile : 0;
         t.pad = 0;
         p.key[v] = t;
+        if (v == tid) mine = t.its;
         its += t.its;
     }
     // iterations of an even share
     const int g = a.H / a.H_kv;
-    __shared__ long long s_lsum[33];
     long long all;
-    block_excl_scan(its, s_lsum, &all);
+    block_excl_scan(its, s_sum, &all);
     const long long share = max((all * a.H + p.shares - 1) / p.shares, (long long)p.min_its);
-    // parts of each tile, in tile order; bucket sizes of the sort by length (most first)
-    auto parts_of = [&](int v) {
-        const long long n = v < UK ? (long long)p.key[v].its * g : 0;
-        return v >= UK ? 0 : n > share ? (int)((n + share - 1) / share) : 1;
-    };
-    auto bucket = [&](int v, int parts) {
-        return (int)min(((long long)p.key[v].its * g + parts - 1) / parts, (long long)kBuckets - 1);
-    };
-    int works = 0, cuts = 0, slots = 0;
-    for (int v0 = 0; v0 < UK; v0 += kPlanThreads) {
-        const int v = v0 + tid, n = parts_of(v);
-        int total_w, total_c, total_s;
-        const int w = works + block_excl_scan(n, s_sum, &total_w);
-        const int c = cuts + block_excl_scan(n > 1 ? 1 : 0, s_sum, &total_c);
-        const int sl = slots + block_excl_scan(n > 1 ? n : 0, s_sum, &total_s);
-        if (n > 1) p.cut[c] = {v, 0, n, sl};
-        if (a.deterministic)
-            for (int i = 0; i < n; ++i) p.work[w + i] = {v, i, n, sl + i};
-        else if (n > 0)
-            atomicAdd(&s_count[bucket(v, n)], n);
-        works += total_w;
-        cuts += total_c;
-        slots += total_s;
+    // iterations, and parts, of tile v
+    auto length = [&](int v) { return v < UK ? (long long)(v == tid ? mine : p.key[v].its) * g : 0; };
+    auto parts_of = [&](int v, long long n) { return v >= UK ? 0 : n > share ? (int)((n + share - 1) / share) : 1; };
+    // Works in tile order, or sorted by length, most first, when they take more than one round of
+    // CTAs.  Running totals: works | cut tiles << 32 | slots << 48 (both below 2 x 16 bits: the
+    // cut tiles are fewer than the SMs).
+    const bool in_order = a.deterministic || UK <= threads;
+    bool sorted = !a.deterministic;
+    if (!in_order) {
+        for (int i = tid; i < kBuckets; i += threads) s_count[i] = 0;
+        __syncthreads();
+    }
+    long long run = 0;
+    for (int v0 = 0; v0 < UK; v0 += threads) {
+        const int v = v0 + tid;
+        const long long len = length(v);
+        const int n = parts_of(v, len);
+        long long total;
+        const long long at =
+            run + block_excl_scan((long long)n | (n > 1 ? 1ll << 32 | (long long)n << 48 : 0ll), s_sum, &total);
+        const int w = (int)at, slot = (int)(at >> 48);
+        if (n > 1) p.cut[(int)(at >> 32) & 0xffff] = {v, 0, n, slot};
+        run += total;
+        if (in_order) {
+            // one round of CTAs: their order does not matter
+            if (UK <= threads && (long long)(int)run * a.H_kv <= p.one_round) sorted = false;
+            if (!sorted)
+                for (int i = 0; i < n; ++i) p.work[w + i] = {v, i, n, slot + i};
+        } else if (n > 0) {
+            atomicAdd(&s_count[(int)min((len + n - 1) / n, (long long)kBuckets - 1)], n);
+        }
     }
     if (tid == 0) {
-        p.head[1] = works;
-        p.head[2] = cuts;
+        p.head[1] = (int)run;
+        p.head[2] = (int)(run >> 32) & 0xffff;
     }
-    if (a.deterministic) return;
+    if (!sorted) return;
+    if (in_order) {  // one round of tiles, more than one of CTAs: count them now
+        for (int i = tid; i < kBuckets; i += threads) s_count[i] = 0;
+        __syncthreads();
+        const long long len = length(tid);
+        const int n = parts_of(tid, len);
+        if (n > 0) atomicAdd(&s_count[(int)min((len + n - 1) / n, (long long)kBuckets - 1)], n);
+    }
     __syncthreads();
-    // counting sort, longest first (within a bucket in any order: it decides only which CTA
-    // starts first)
-    const int b0 = kBuckets - 1 - 2 * tid, b1 = b0 - 1;
-    const int c0 = s_count[b0], c1 = s_count[b1];
-    int total;
-    const int at = block_excl_scan(c0 + c1, s_sum, &total);
-    s_count[b0] = at;
-    s_count[b1] = at + c0;
+    // first place of each bucket, longest first (within a bucket in any order)
+    const int per = kBuckets / threads;
+    long long sum = 0, total;
+    for (int i = 0; i < per; ++i) sum += s_count[kBuckets - 1 - (tid * per + i)];
+    int at = (int)block_excl_scan(sum, s_sum, &total);
+    for (int i = 0; i < per; ++i) {
+        int& c = s_count[kBuckets - 1 - (tid * per + i)];
+        const int n = c;
+        c = at;
+        at += n;
+    }
     __syncthreads();
-    slots = 0;
-    for (int v0 = 0; v0 < UK; v0 += kPlanThreads) {
-        const int v = v0 + tid, n = parts_of(v);
-        int total_s;
-        const int sl = slots + block_excl_scan(n > 1 ? n : 0, s_sum, &total_s);
-        const int w = n > 0 ? atomicAdd(&s_count[bucket(v, n)], n) : 0;
-        for (int i = 0; i < n; ++i) p.work[w + i] = {v, i, n, sl + i};
-        slots += total_s;
+    run = 0;
+    for (int v0 = 0; v0 < UK; v0 += threads) {
+        const int v = v0 + tid;
+        const long long len = length(v);
+        const int n = parts_of(v, len);
+        const long long slot = run + block_excl_scan(n > 1 ? (long long)n : 0ll, s_sum, &total);
+        run += total;
+        const int w = n > 0 ? atomicAdd(&s_count[(int)min((len + n - 1) / n, (long long)kBuckets - 1)], n) : 0;
+        for (int i = 0; i < n; ++i) p.work[w + i] = {v, i, n, (int)slot + i};
     }
 }
 
@@ -308,7 +335,9 @@ bool bwd_acc_map(CUtensorMap* m, const PackedBwd& a, const BwdPlan& p) {
 }
 
 cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_cores, cudaStream_t st) {
-    static_assert(kBuckets == 2 * kPlanThreads, "two buckets a thread");
+    static_assert(kBuckets % kPlanThreads == 0 && kBuckets % kSmallPlan == 0, "whole buckets a thread");
+    const bool small = a.N <= kSmallPlan && p.max_units <= kSmallPlan && p.max_keys <= kSmallPlan;
+    const int threads = small ? kSmallPlan : kPlanThreads;
     BwdMaps maps = {};
     int map_blocks = 0;
     if (tensor_cores) {
@@ -324,9 +353,9 @@ cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_co
             !row_map(&maps.m[2], k, dt, 2, a.d, a.H_kv, 1, a.sk.head, a.sk.tok) ||
             !row_map(&maps.m[3], v, dt, 2, a.d, a.H_kv, 1, a.sv.head, a.sv.tok))
             return cudaErrorInvalidValue;
-        map_blocks = (int)(((long long)a.N * 4 + kPlanThreads / 32 - 1) / (kPlanThreads / 32));
+        map_blocks = (int)(((long long)a.N * 4 + threads / 32 - 1) / (threads / 32));
     }
-    bwd_plan_kernel<<<1 + map_blocks + (a.fill ? 32 : 0), kPlanThreads, 0, st>>>(a, p, maps, map_blocks);
+    bwd_plan_kernel<<<1 + map_blocks + (a.fill ? 32 : 0), threads, 0, st>>>(a, p, maps, map_blocks);
     return cudaGetLastError();
 }
 
