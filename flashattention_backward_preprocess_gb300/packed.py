@@ -23,7 +23,7 @@ import torch
 from .binding import _DT, FaError, _check, load_library
 
 _I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
-_empty = torch.empty
+_empty, _empty_like, _Tensor = torch.empty, torch.empty_like, torch.Tensor
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -48,7 +48,7 @@ def _same(name, t, shape, dtype):
 
 
 def _ints(name, t, shape, dtype=_I32):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _refuse(name, f"must be contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -58,12 +58,7 @@ def _lse(t, shape):
 
 
 def _strides(*named):
-    """Element strides of all but the last dimension of each (name, tensor); None when every tensor is dense."""
-    for _, t in named:
-        if not t.is_contiguous():
-            break
-    else:
-        return None
+    """Element strides of all but the last dimension of each (name, tensor)."""
     flat = []
     for name, t in named:
         if t.is_contiguous():
@@ -83,10 +78,11 @@ def _strides(*named):
 def _device(first, *rest):
     """The one CUDA device all given tensors are on."""
     dev = first.device
+    i = first.get_device()
     for t in rest:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != i:
             _refuse("tensors", f"expected one device, got {dev} and {t.device}")
-    if dev.type != "cuda":
+    if not first.is_cuda:
         _refuse("tensors", f"device pointers required, got {dev}")
     return dev
 
@@ -123,7 +119,8 @@ def _shape3(name, t):
 def _outputs(Q, T, H, O, LSE):
     """O, LSE and whether the call sets their rows of no sequence (it does when both are new)."""
     if O is None and LSE is None:
-        return (_empty(Q.shape, dtype=Q.dtype, device=Q.device), _empty((H, T), dtype=_F32, device=Q.device), 1)
+        o = _empty_like(Q) if Q.is_contiguous() else _empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        return o, _empty((H, T), dtype=_F32, device=Q.device), 1
     if LSE is None:
         LSE = torch.full((H, T), -math.inf, dtype=_F32, device=Q.device)
     else:
@@ -155,7 +152,9 @@ def fa_varlen_fwd(Q, K, V, cu_q, cu_k, scale: float | None = None, causal: bool 
         ws = _empty(need, dtype=_U8, device=dev)
         _check(load_library().fa_varlen_fwd(
             Q.data_ptr(), K.data_ptr(), V.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
-            N, T_q, T_k, H, H_kv, d, _strides(("Q", Q), ("K", K), ("V", V), ("O", o)),
+            N, T_q, T_k, H, H_kv, d,
+            None if Q.is_contiguous() and K.is_contiguous() and V.is_contiguous() and o.is_contiguous() else
+            _strides(("Q", Q), ("K", K), ("V", V), ("O", o)),
             d ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
             need, st))
         return o, lse
@@ -193,6 +192,7 @@ def fa_varlen_bwd(dO, Q, K, V, O, LSE, cu_q, cu_k, scale: float | None = None, c
         _check(load_library().fa_varlen_bwd(
             dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(), gq.data_ptr(),
             gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), N, T_q, T_k, H, H_kv, d,
+            None if all(map(_Tensor.is_contiguous, (dO, Q, K, V, O, gq, gk, gv))) else
             _strides(("dO", dO), ("Q", Q), ("K", K), ("V", V), ("O", O), ("dQ", gq), ("dK", gk), ("dV", gv)),
             d ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window_size), int(bool(deterministic)),
             fill, dt, ws.data_ptr(), need, st))
@@ -236,6 +236,7 @@ def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float 
         _check(load_library().fa_paged_fwd(
             Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), o.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
             cu_q.data_ptr(), seq_lens.data_ptr(), N, T_q, pages, page, cols, H, H_kv, d,
+            None if Q.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous() and o.is_contiguous() else
             _strides(("Q", Q), ("K_cache", K_cache), ("V_cache", V_cache), ("O", o)),
             d ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
             need, st))
@@ -267,8 +268,8 @@ def fa_page_slots(ctx_lens, cu_q, block_table, free_pages, free_start, page_size
     def body(st):
         out = (_empty(tokens, dtype=_I64, device=dev) if slots is None else slots,
                _empty(tokens, dtype=_I32, device=dev) if positions is None else positions,
-               _empty(N, dtype=_I32, device=dev) if seq_lens is None else seq_lens,
-               _empty(1, dtype=_I32, device=dev) if free_next is None else free_next)
+               _empty_like(ctx_lens) if seq_lens is None else seq_lens,
+               _empty_like(free_start) if free_next is None else free_next)
         _check(load_library().fa_page_slots(
             ctx_lens.data_ptr(), cu_q.data_ptr(), free_pages.data_ptr(), free_start.data_ptr(), block_table.data_ptr(),
             out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), N, tokens, n_free,
@@ -292,6 +293,7 @@ def fa_paged_write(K, V, slots, K_cache, V_cache, stream=None):
     def body(st):
         _check(load_library().fa_paged_write(
             K.data_ptr(), V.data_ptr(), slots.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), T, pages, page, H_kv, d,
+            None if K.is_contiguous() and V.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous() else
             _strides(("K", K), ("V", V), ("K_cache", K_cache), ("V_cache", V_cache)), dt, st))
         return K_cache, V_cache
 
