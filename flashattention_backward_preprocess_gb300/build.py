@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "preprocess.cu", "bwd_simt.cu", "fwd_simt.cu", "fwd_sm103.cu", "bwd_sm103.cu", "bwd_d256.cu",
            "noalloc.cu", "selftest.cu", "packed_api.cu", "packed_plan.cu", "packed_fwd.cu", "packed_simt.cu",
-           "packed_bwd.cu", "packed_bwd_simt.cu", "paged_cache.cu"]
+           "packed_bwd.cu", "packed_bwd_d256.cu", "packed_bwd_simt.cu", "paged_cache.cu"]
 
 
 def _nvcc() -> str:

@@ -536,8 +536,8 @@ struct BwdPlan {
 
 int sm_count();  // of the current device (looked up once per device)
 
-// CTAs that share the work of one plan tile and head on CUDA cores (by their key rows).
-inline int simt_pieces(int d) { return d <= 128 ? 2 : 4; }
+// CTAs that share the work of one plan tile and head, by their key rows.
+inline int bwd_pieces(bool tensor_cores, int d) { return tensor_cores ? (d <= 128 ? 1 : 2) : (d <= 128 ? 2 : 4); }
 
 inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, BwdPlan* p) {
     char* b = static_cast<char*>(ws);
@@ -554,8 +554,9 @@ inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, B
     // with x = iterations / share of a tile, the tiles' x add up to shares / H_kv per head at
     // most, a cut tile has x > 1 and ceil(x) <= 2x parts.  On CUDA cores a plan tile is several
     // CTAs and a CTA's fixed cost is small: two rounds of CTAs even out better.
-    q.shares = tensor_cores ? sm_count() : (2 * sm_count() + simt_pieces(a.d) - 1) / simt_pieces(a.d);
-    q.one_round = tensor_cores ? sm_count() : sm_count() / simt_pieces(a.d);
+    const int pieces = bwd_pieces(tensor_cores, a.d);
+    q.shares = ((tensor_cores ? 1 : 2) * sm_count() + pieces - 1) / pieces;
+    q.one_round = sm_count() / pieces;
     q.min_its = 4;
     q.max_cut = q.shares / a.H_kv + 1;
     q.max_work = q.max_keys + q.max_cut;
@@ -580,12 +581,16 @@ inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, B
 
 // packed_plan.cu: tiles, order, maps, counters; with a.fill the gradient rows of no sequence
 cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_cores, cudaStream_t st);
-// packed_simt.cu: D, the LSE copy and a zeroed accumulator; dQ from the accumulator
+// packed_bwd_simt.cu: D, the LSE copy and a zeroed accumulator; dQ from the accumulator
 cudaError_t launch_packed_preprocess(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
 cudaError_t launch_packed_dq(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
-// packed_bwd.cu (f16 / bf16, head dim <= 128) and packed_bwd_simt.cu (f32, head dim 256)
+// f16 / bf16: packed_bwd.cu (head dim <= 128), packed_bwd_d256.cu; f32: packed_bwd_simt.cu
 cudaError_t launch_packed_bwd(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
+cudaError_t launch_packed_bwd_d256(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
 cudaError_t launch_packed_bwd_simt(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
+// packed_bwd_simt.cu: the accumulator in deterministic mode where the main kernel leaves it out
+// (f32, head dim 256)
+cudaError_t launch_packed_dq_ordered(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
 
 // Map of the fp32 accumulator [rows][H][d]: boxes of 32 columns, one head, 128 rows.
 bool bwd_acc_map(CUtensorMap* m, const PackedBwd& a, const BwdPlan& p);

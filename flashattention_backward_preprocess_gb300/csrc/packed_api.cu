@@ -106,7 +106,7 @@ bool use_tensor_cores(const PackedFwd& a) {
     return a.page_size % 8 == 0 && (bn % a.page_size == 0 || a.page_size % bn == 0);
 }
 
-bool bwd_tensor_cores(const PackedBwd& a) { return a.dtype != FA_F32 && tc_head_dim(a.d) != 0; }
+bool bwd_tensor_cores(const PackedBwd& a) { return a.dtype != FA_F32; }
 
 size_t fwd_bytes(const PackedFwd& a) {
     size_t n = 0;
@@ -262,7 +262,8 @@ int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, c
     cudaError_t e = launch_bwd_plan(a, p, tc, st);
     if (e != cudaSuccess) return cuda_bad("plan launch", e);
     if ((e = launch_packed_preprocess(a, p, st)) != cudaSuccess) return cuda_bad("preprocess launch", e);
-    e = tc ? launch_packed_bwd(a, p, st) : launch_packed_bwd_simt(a, p, st);
+    e = !tc ? launch_packed_bwd_simt(a, p, st) : d == 256 ? launch_packed_bwd_d256(a, p, st) : launch_packed_bwd(a, p, st);
+    if (e == cudaSuccess && deterministic && (!tc || d == 256)) e = launch_packed_dq_ordered(a, p, st);
     if (e != cudaSuccess) return cuda_bad("main kernel launch", e);
     if ((e = launch_packed_dq(a, p, st)) != cudaSuccess) return cuda_bad("dq launch", e);
     return FA_OK;

@@ -1,5 +1,5 @@
 // packed_bwd_simt.cu -- the passes around the packed backward's main kernel, and that kernel
-// on CUDA cores (fp32 inputs; head dim 256).
+// on CUDA cores (fp32 inputs).
 //
 // Preprocess, per query row and head: D = sum_c dO_c O_c (fp32), LSE * log2 e into rows padded
 // to whole query tiles (+inf on padding rows and rows without keys, so their P is 0), and the
@@ -219,7 +219,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedBwd a, const BwdPlan p) {
     using C = SCfg<D>;
     constexpr int BN = C::BN, BM = C::BM, LD = C::LD, LP = C::LP, TR = C::TR, TC = C::TC, NG = C::NG;
-    constexpr int kPieces = kBwdTile / BN;  // CTAs per work and head (simt_pieces)
+    constexpr int kPieces = kBwdTile / BN;  // CTAs per work and head (bwd_pieces)
     extern __shared__ float4 smem4[];
     float* smem = reinterpret_cast<float*>(smem4);
     float* sK = smem;
@@ -552,22 +552,26 @@ cudaError_t dq_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t bwd_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
     using C = SCfg<D>;
-    static std::atomic<uint64_t> ready[2];
+    static std::atomic<uint64_t> ready{0};
     cudaError_t e;
     if (p.max_keys > 0) {
         auto kern = packed_bwd_simt_kernel<T, D>;
-        if ((e = allow_smem(kern, (int)C::SMEM, ready[0])) != cudaSuccess) return e;
+        if ((e = allow_smem(kern, (int)C::SMEM, ready)) != cudaSuccess) return e;
         kern<<<(unsigned)((long long)p.max_work * a.H_kv * (kBwdTile / C::BN)), kThreads, C::SMEM, st>>>(a, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if (a.deterministic && p.max_units > 0) {
-        const size_t smem = sizeof(float) * (2 * kDqRows * D + 2 * kDqKeys * D + kDqRows * kDqKeys);
-        auto kern = packed_dq_simt_kernel<T, D>;
-        if ((e = allow_smem(kern, (int)smem, ready[1])) != cudaSuccess) return e;
-        kern<<<dim3((unsigned)(p.max_units * (kBwdTile / kDqRows)), (unsigned)a.H), kDqThreads, smem, st>>>(a, p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
     return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t dq_ordered_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (2 * kDqRows * D + 2 * kDqKeys * D + kDqRows * kDqKeys);
+    auto kern = packed_dq_simt_kernel<T, D>;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem(kern, (int)smem, ready);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)(p.max_units * (kBwdTile / kDqRows)), (unsigned)a.H), kDqThreads, smem, st>>>(a, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -588,16 +592,26 @@ cudaError_t launch_packed_dq(const PackedBwd& a, const BwdPlan& p, cudaStream_t 
 }
 
 cudaError_t launch_packed_bwd_simt(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
-    if (a.dtype == FA_F32) {
-        switch (a.d) {
-            case 32: return bwd_t<float, 32>(a, p, st);
-            case 64: return bwd_t<float, 64>(a, p, st);
-            case 96: return bwd_t<float, 96>(a, p, st);
-            case 128: return bwd_t<float, 128>(a, p, st);
-            case 256: return bwd_t<float, 256>(a, p, st);
-        }
-    } else if (a.d == 256) {
-        return a.dtype == FA_F16 ? bwd_t<__half, 256>(a, p, st) : bwd_t<__nv_bfloat16, 256>(a, p, st);
+    switch (a.d) {
+        case 32: return bwd_t<float, 32>(a, p, st);
+        case 64: return bwd_t<float, 64>(a, p, st);
+        case 96: return bwd_t<float, 96>(a, p, st);
+        case 128: return bwd_t<float, 128>(a, p, st);
+        case 256: return bwd_t<float, 256>(a, p, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_packed_dq_ordered(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
+    if (p.max_units == 0) return cudaSuccess;
+    if (a.dtype == FA_F16) return dq_ordered_t<__half, 256>(a, p, st);
+    if (a.dtype == FA_BF16) return dq_ordered_t<__nv_bfloat16, 256>(a, p, st);
+    switch (a.d) {
+        case 32: return dq_ordered_t<float, 32>(a, p, st);
+        case 64: return dq_ordered_t<float, 64>(a, p, st);
+        case 96: return dq_ordered_t<float, 96>(a, p, st);
+        case 128: return dq_ordered_t<float, 128>(a, p, st);
+        case 256: return dq_ordered_t<float, 256>(a, p, st);
     }
     return cudaErrorInvalidValue;
 }

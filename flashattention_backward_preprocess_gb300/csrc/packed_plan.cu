@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 }
 
 bool row_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es, int d, int heads, long long rows,
-             long long head_stride, long long row_stride) {
+             long long head_stride, long long row_stride, int box_rows) {
     TmaEncodeTiledFn enc = tma_encode_fn();
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t str[2] = {(cuuint64_t)head_stride * es, (cuuint64_t)row_stride * es};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), 1, kBwdTile};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), 1, (cuuint32_t)box_rows};
     const cuuint32_t one[3] = {1, 1, 1};
     return enc && enc(m, dt, 3, const_cast<void*>(base), dims, str, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -331,7 +331,7 @@ bool row_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es, i
 
 bool bwd_acc_map(CUtensorMap* m, const PackedBwd& a, const BwdPlan& p) {
     return row_map(m, p.dqacc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.d, a.H, p.rows > 0 ? p.rows : 1, a.d,
-                   (long long)a.H * a.d);
+                   (long long)a.H * a.d, kBwdTile);
 }
 
 cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_cores, cudaStream_t st) {
@@ -343,15 +343,16 @@ cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_co
     if (tensor_cores) {
         const CUtensorMapDataType dt =
             a.dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const int rows = a.d == 256 ? 64 : kBwdTile;  // of the kernel's tiles
         // an empty axis is never loaded: its maps are built over the other axis' rows
         const void* q = a.T_q > 0 ? a.Q : a.K;
         const void* g = a.T_q > 0 ? a.dO : a.K;
         const void* k = a.T_k > 0 ? a.K : a.Q;
         const void* v = a.T_k > 0 ? a.V : a.Q;
-        if (!row_map(&maps.m[0], q, dt, 2, a.d, a.H, 1, a.sq.head, a.sq.tok) ||
-            !row_map(&maps.m[1], g, dt, 2, a.d, a.H, 1, a.sdo.head, a.sdo.tok) ||
-            !row_map(&maps.m[2], k, dt, 2, a.d, a.H_kv, 1, a.sk.head, a.sk.tok) ||
-            !row_map(&maps.m[3], v, dt, 2, a.d, a.H_kv, 1, a.sv.head, a.sv.tok))
+        if (!row_map(&maps.m[0], q, dt, 2, a.d, a.H, 1, a.sq.head, a.sq.tok, rows) ||
+            !row_map(&maps.m[1], g, dt, 2, a.d, a.H, 1, a.sdo.head, a.sdo.tok, rows) ||
+            !row_map(&maps.m[2], k, dt, 2, a.d, a.H_kv, 1, a.sk.head, a.sk.tok, rows) ||
+            !row_map(&maps.m[3], v, dt, 2, a.d, a.H_kv, 1, a.sv.head, a.sv.tok, rows))
             return cudaErrorInvalidValue;
         map_blocks = (int)(((long long)a.N * 4 + threads / 32 - 1) / (threads / 32));
     }

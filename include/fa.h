@@ -241,7 +241,7 @@ size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d
  *   deterministic : as in fa_bwd_ex (0 = dQ reduced with fp32 atomics, 1 =
  *                   bitwise reproducible dQ); dK and dV are reproducible in both
  *   fill          : gradient rows of no sequence are 0 = left, 1 = set to 0
- * F16/BF16 with d <= 128 run a tcgen05 kernel, F32 and d = 256 an FFMA kernel.
+ * F16/BF16 run tcgen05 kernels, F32 an FFMA kernel.
  */
 int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, const void* O,
                   const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q, const int* cu_k,
