@@ -34,6 +34,16 @@ def _varlen(lib, **kw):
     return lib.fa_varlen_fwd(*a.values())
 
 
+def _varlen_bwd(lib, **kw):
+    a = dict(dO=P[0], Q=P[1], K=P[2], V=P[3], O=P[4], LSE=P[5], dQ=P[6], dK=P[7], dV=P[8], cu_q=P[9], cu_k=P[10], N=3, T_q=100,
+             T_k=100, H=4, H_kv=2, d=64, strides=None, scale=0.125, causal=1, window=0, det=0, fill=0, dtype=fa.FA_BF16,
+             ws=P[11], ws_bytes=0, stream=None)
+    assert not set(kw) - set(a)
+    a.update(kw)
+    a["strides"] = _arr(a["strides"])
+    return lib.fa_varlen_bwd(*a.values())
+
+
 def _paged(lib, **kw):
     a = dict(Q=P[0], K=P[1], V=P[2], O=P[3], LSE=P[4], table=P[5], cu_q=P[6], seq_lens=P[7], N=3, T_q=10, num_pages=50,
              page_size=16, max_pages=8, H=4, H_kv=2, d=64, strides=None, scale=0.125, causal=1, window=0, fill=0,
@@ -86,7 +96,17 @@ def test_paged_fwd_refuses(lib, kw, arg):
     assert fa.fa_last_error().startswith(arg + ":"), fa.fa_last_error()
 
 
+@pytest.mark.parametrize("kw,arg", [c for c in COMMON if "O" not in c[0] and "LSE" not in c[0]] + [
+    (dict(dO=None), "dO"), (dict(O=P[4] + 8), "O"), (dict(LSE=None), "LSE"), (dict(K=None), "K"), (dict(V=P[3] + 4), "V"),
+    (dict(dQ=None), "dQ"), (dict(dK=P[7] + 2), "dK"), (dict(dV=None), "dV"), (dict(cu_k=P[10] + 2), "cu_k"), (dict(det=2), "deterministic"),
+    (dict(T_k=-5), "T_k"), (dict(strides=[256, 64, 256, 64, 128, 64, 128, 64, 256, 64, 256, 64, 128, 64, 128, 4]), "strides")])
+def test_varlen_bwd_refuses(lib, kw, arg):
+    assert _varlen_bwd(lib, **kw) == 1, kw
+    assert fa.fa_last_error().startswith(arg + ":"), fa.fa_last_error()
+
+
 def test_unsupported_head_dim(lib):
+    assert _varlen_bwd(lib, d=80) == 2
     assert _varlen(lib, d=80) == 2 and _paged(lib, d=48) == 2 and _write(lib, d=80) == 2
     assert lib.fa_varlen_workspace_bytes(3, 100, 100, 4, 2, 80, fa.FA_BF16, 0) == 0
     assert lib.fa_varlen_workspace_bytes(0, 100, 100, 4, 2, 64, fa.FA_BF16, 0) == 0
@@ -98,6 +118,7 @@ def test_no_rows_is_no_work(lib):
     assert _varlen(lib, T_q=0, Q=None, O=None, LSE=None) == 0
     assert _paged(lib, T_q=0, Q=None, O=None, LSE=None) == 0
     assert _write(lib, T=0, K=None, V=None, slots=None) == 0
+    assert _varlen_bwd(lib, T_q=0, T_k=0, dO=None, Q=None, K=None, V=None, O=None, LSE=None, dQ=None, dK=None, dV=None) == 0
 
 
 @pytest.mark.parametrize("kw,arg", [
