@@ -317,6 +317,22 @@ int fa_page_slots(const int* ctx_lens, const int* cu_q, const int* free_pages, c
         return rc;
     if (num_free > 0 && (rc = check_ptr(free_pages, "free_pages", 4))) return rc;
     if (T > 0 && ((rc = check_ptr(slots, "slots", 8)) || (rc = check_ptr(positions, "positions", 4)))) return rc;
+    // every block reads the inputs of the requests before its own, at no set time
+    struct Span {
+        const char* name;
+        const void* p;
+        long long bytes;
+    };
+    const Span in[] = {{"ctx_lens", ctx_lens, 4ll * N}, {"cu_q", cu_q, 4ll * (N + 1)},
+                       {"free_pages", free_pages, 4ll * num_free}, {"free_start", free_start, 4}};
+    const Span out[] = {{"slots", slots, 8ll * T}, {"positions", positions, 4ll * T}, {"seq_lens", seq_lens, 4ll * N},
+                        {"free_next", free_next, 4}, {"block_table", block_table, 4ll * N * max_pages}};
+    for (const Span& o : out)
+        for (const Span& i : in) {
+            const uintptr_t op = reinterpret_cast<uintptr_t>(o.p), ip = reinterpret_cast<uintptr_t>(i.p);
+            if (op < ip + i.bytes && ip < op + o.bytes)
+                return bad(o.name, std::string("must not overlap ") + i.name);
+        }
     PageSlots a = {};
     a.ctx_lens = ctx_lens, a.cu_q = cu_q, a.free_pages = free_pages, a.free_start = free_start;
     a.table = block_table, a.slots = slots, a.positions = positions, a.seq_lens = seq_lens, a.free_next = free_next;

@@ -292,7 +292,8 @@ size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page
  *   free_next   : [1] int32 out, free_start[0] plus the pages taken
  * When the free list or the table has no room, the entries and slots concerned
  * are -1 and fa_check_device reports FA_ERR_INVALID_ARG.  The call changes
- * neither free_pages nor free_start, so running it again gives the same result.
+ * neither free_pages nor free_start, so running it again gives the same result;
+ * an output that overlaps an input is refused.
  */
 int fa_page_slots(const int* ctx_lens, const int* cu_q, const int* free_pages, const int* free_start,
                   int* block_table, long long* slots, int* positions, int* seq_lens, int* free_next,

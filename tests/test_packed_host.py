@@ -131,6 +131,13 @@ def test_page_slots_refuses(lib, kw, arg):
     assert fa.fa_last_error().startswith(arg + ":"), fa.fa_last_error()
 
 
+@pytest.mark.parametrize("out,of", [
+    ("lens", P[0]), ("nxt", P[3]), ("slots", P[1]), ("pos", P[2] + 64), ("lens", P[1] + 4), ("table", P[0] - 4)])
+def test_page_slots_refuses_outputs_over_inputs(lib, out, of):
+    assert _slots(lib, **{out: of}) == 1
+    assert "must not overlap" in fa.fa_last_error()
+
+
 @pytest.mark.parametrize("kw,arg", [
     (dict(K=None), "K"), (dict(V=P[1] + 2), "V"), (dict(slots=None), "slots"), (dict(Kc=None), "K_cache"), (dict(Vc=P[4] + 8), "V_cache"),
     (dict(T=-1), "T"), (dict(num_pages=0), "num_pages"), (dict(page_size=-1), "page_size"), (dict(H_kv=0), "H"), (dict(dtype=5), "dtype"),
