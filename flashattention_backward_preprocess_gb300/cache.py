@@ -6,7 +6,9 @@ One step of a model, for the new tokens of all requests (one each, or chunks of 
     cache.begin(cu_q, tokens)                      # fa_page_slots: pages, slots, positions
     for layer in range(layers):
         O, LSE = cache.attend(layer, Q, K, V)      # fa_paged_write, fa_paged_fwd
-Everything stays on the device and in stream order; nothing waits for the GPU but release().
+Everything stays on the device and in stream order; nothing waits for the GPU but release().  A
+step can be captured into a graph; every replay takes the step again, for the tokens and offsets
+that its input tensors then hold.
 """
 from __future__ import annotations
 
@@ -41,8 +43,10 @@ class PagedKVCache:
         """Takes the pages of the step's new tokens (int32 offsets cu_q [rows + 1], `tokens` rows in
         the step's tensors, padding behind cu_q[rows] included) and returns their positions."""
         self.cu_q = cu_q
-        self.slots, self.positions, self.lens, self.free_start = packed.fa_page_slots(
+        self.slots, self.positions, lens, start = packed.fa_page_slots(
             self.lens, cu_q, self.block_table, self.free_pages, self.free_start, self.page_size, tokens)
+        # in place: the replays of a captured step go on from where the last one ended
+        torch._foreach_copy_([self.lens, self.free_start], [lens, start])
         return self.positions
 
     def attend(self, layer: int, Q, K, V, scale: float | None = None, window_size: int = 0):

@@ -117,3 +117,39 @@ def test_step_is_capturable():
         fa.fa_check_device()
         assert torch.equal(O, want[0]) and torch.equal(LSE, want[1])
     assert lens.tolist() == [40, 21, 36, 27]
+
+
+def test_replays_of_a_step_go_on():
+    """Nothing but the step is captured; eager steps and a release come between replays."""
+    rows, H, H_kv, d, page = 3, 4, 2, 64, 8
+    a, b = (fa.PagedKVCache(1, 40, page, H_kv, d, rows, 8) for _ in range(2))
+    gen = torch.Generator().manual_seed(3)
+    r = lambda h: torch.randn(rows, h, d, generator=gen).bfloat16().cuda()
+    cu = _cu([1] * rows)
+    Q, K, V = r(H), r(H_kv), r(H_kv)
+    for c in (a, b):
+        c.begin(cu, rows)
+        c.attend(0, Q, K, V)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.begin(cu, rows)
+        O, LSE = a.attend(0, Q, K, V)
+    for i in range(24):
+        for t, h in ((Q, H), (K, H_kv), (V, H_kv)):
+            t.copy_(r(h))
+        if i % 7 == 3:
+            got = (a.begin(cu, rows), a.attend(0, Q, K, V))[1]
+        else:
+            g.replay()
+            got = O, LSE
+        b.begin(cu, rows)
+        want = b.attend(0, Q, K, V)
+        torch.cuda.synchronize()
+        fa.fa_check_device()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
+        if i == 12:
+            a.release(1)
+            b.release(1)
+        assert a.lens.tolist() == b.lens.tolist() and a.free_start.tolist() == b.free_start.tolist()
+    assert a.lens.tolist() == [25, 11, 25]
