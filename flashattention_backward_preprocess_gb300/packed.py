@@ -29,6 +29,12 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+def _scale(scale, d):
+    if scale is None:
+        return max(d, 1) ** -0.5  # the library refuses d = 0
+    return float(scale)
+
+
 def _refuse(name, reason):
     raise FaError(1, f"{name}: {reason}")
 
@@ -155,7 +161,7 @@ def fa_varlen_fwd(Q, K, V, cu_q, cu_k, scale: float | None = None, causal: bool 
             N, T_q, T_k, H, H_kv, d,
             None if Q.is_contiguous() and K.is_contiguous() and V.is_contiguous() and o.is_contiguous() else
             _strides(("Q", Q), ("K", K), ("V", V), ("O", o)),
-            d ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
+            _scale(scale, d), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
             need, st))
         return o, lse
 
@@ -194,7 +200,7 @@ def fa_varlen_bwd(dO, Q, K, V, O, LSE, cu_q, cu_k, scale: float | None = None, c
             gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), N, T_q, T_k, H, H_kv, d,
             None if all(map(_Tensor.is_contiguous, (dO, Q, K, V, O, gq, gk, gv))) else
             _strides(("dO", dO), ("Q", Q), ("K", K), ("V", V), ("O", O), ("dQ", gq), ("dK", gk), ("dV", gv)),
-            d ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window_size), int(bool(deterministic)),
+            _scale(scale, d), int(bool(causal)), int(window_size), int(bool(deterministic)),
             fill, dt, ws.data_ptr(), need, st))
         return gq, gk, gv
 
@@ -238,7 +244,7 @@ def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float 
             cu_q.data_ptr(), seq_lens.data_ptr(), N, T_q, pages, page, cols, H, H_kv, d,
             None if Q.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous() and o.is_contiguous() else
             _strides(("Q", Q), ("K_cache", K_cache), ("V_cache", V_cache), ("O", o)),
-            d ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
+            _scale(scale, d), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
             need, st))
         return o, lse
 

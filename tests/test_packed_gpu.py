@@ -366,3 +366,15 @@ def test_varlen_fwd_many_short_sequences(N, H, H_kv, d):
     pick = lambda x: x.transpose(1, 2)[inside]
     ref.check("O", O, pick(P @ v), pick(P @ v.abs()), e, torch.bfloat16)
     ref.check_lse(LSE, lse.transpose(1, 2)[inside].t(), e)
+
+
+def test_empty_head_dimension_is_refused():
+    q = torch.zeros(4, 2, 0, dtype=torch.bfloat16, device="cuda")
+    cu = _cu([4])
+    cache = torch.zeros(2, 8, 2, 0, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.full((1,), 4, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(2, 4, device="cuda")
+    for call in (lambda: fa.fa_varlen_fwd(q, q, q, cu, cu), lambda: fa.fa_varlen_bwd(q, q, q, q, q, lse, cu, cu),
+                 lambda: fa.fa_paged_fwd(q, cache, cache, table, cu, lens)):
+        with pytest.raises(fa.FaError, match=" d:"):
+            call()
