@@ -215,6 +215,70 @@ __device__ __forceinline__ void stage_rows(float* dst, const T* src, long long l
     }
 }
 
+// S and dP blocks: rows ty + 16r of Q and dO, keys tx + 16c, 4 head-dim columns a step.
+template <int D, int TR, int TC>
+__device__ __forceinline__ void block_products(const float* sQ, const float* sdO, const float* sK, const float* sV, int ty,
+                                               int tx, float (&accS)[TR][TC], float (&accP)[TR][TC]) {
+    constexpr int LD = SCfg<D>::LD;
+#pragma unroll
+    for (int r = 0; r < TR; ++r)
+#pragma unroll
+        for (int c = 0; c < TC; ++c) accS[r][c] = accP[r][c] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < D; k += 4) {
+        float4 q[TR], o[TR], kk[TC], v[TC];
+#pragma unroll
+        for (int r = 0; r < TR; ++r) {
+            q[r] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * r) * LD + k);
+            o[r] = *reinterpret_cast<const float4*>(sdO + (ty + 16 * r) * LD + k);
+        }
+#pragma unroll
+        for (int c = 0; c < TC; ++c) {
+            kk[c] = *reinterpret_cast<const float4*>(sK + (tx + 16 * c) * LD + k);
+            v[c] = *reinterpret_cast<const float4*>(sV + (tx + 16 * c) * LD + k);
+        }
+#pragma unroll
+        for (int r = 0; r < TR; ++r)
+#pragma unroll
+            for (int c = 0; c < TC; ++c) {
+                accS[r][c] = fmaf(q[r].x, kk[c].x, accS[r][c]);
+                accS[r][c] = fmaf(q[r].y, kk[c].y, accS[r][c]);
+                accS[r][c] = fmaf(q[r].z, kk[c].z, accS[r][c]);
+                accS[r][c] = fmaf(q[r].w, kk[c].w, accS[r][c]);
+                accP[r][c] = fmaf(o[r].x, v[c].x, accP[r][c]);
+                accP[r][c] = fmaf(o[r].y, v[c].y, accP[r][c]);
+                accP[r][c] = fmaf(o[r].z, v[c].z, accP[r][c]);
+                accP[r][c] = fmaf(o[r].w, v[c].w, accP[r][c]);
+            }
+    }
+}
+
+// accQ += dS K: query rows ty + 16r, column groups tx + 16q, keys in order.
+template <int D, int TR, int NG, int BN>
+__device__ __forceinline__ void add_ds_k(const float* sdS, const float* sK, int ty, int tx, float (&accQ)[TR][NG][4]) {
+    constexpr int LD = SCfg<D>::LD, LP = SCfg<D>::LP;
+#pragma unroll 2
+    for (int jj = 0; jj < BN; ++jj) {
+        float ds[TR];
+#pragma unroll
+        for (int r = 0; r < TR; ++r) ds[r] = sdS[(ty + 16 * r) * LP + jj];
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const int f = tx + 16 * q;
+            if (NG * 16 * 4 == D || f < D / 4) {
+                const float4 kv = *reinterpret_cast<const float4*>(sK + jj * LD + 4 * f);
+#pragma unroll
+                for (int r = 0; r < TR; ++r) {
+                    accQ[r][q][0] = fmaf(ds[r], kv.x, accQ[r][q][0]);
+                    accQ[r][q][1] = fmaf(ds[r], kv.y, accQ[r][q][1]);
+                    accQ[r][q][2] = fmaf(ds[r], kv.z, accQ[r][q][2]);
+                    accQ[r][q][3] = fmaf(ds[r], kv.w, accQ[r][q][3]);
+                }
+            }
+        }
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedBwd a, const BwdPlan p) {
     using C = SCfg<D>;
@@ -287,37 +351,7 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
         __syncthreads();
         // ---- S and dP blocks (rows ty + 16r, keys tx + 16c), 4 head-dim columns a step
         float accS[TR][TC], accP[TR][TC];
-#pragma unroll
-        for (int r = 0; r < TR; ++r)
-#pragma unroll
-            for (int c = 0; c < TC; ++c) accS[r][c] = accP[r][c] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < D; k += 4) {
-            float4 q[TR], o[TR], kk[TC], v[TC];
-#pragma unroll
-            for (int r = 0; r < TR; ++r) {
-                q[r] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * r) * LD + k);
-                o[r] = *reinterpret_cast<const float4*>(sdO + (ty + 16 * r) * LD + k);
-            }
-#pragma unroll
-            for (int c = 0; c < TC; ++c) {
-                kk[c] = *reinterpret_cast<const float4*>(sK + (tx + 16 * c) * LD + k);
-                v[c] = *reinterpret_cast<const float4*>(sV + (tx + 16 * c) * LD + k);
-            }
-#pragma unroll
-            for (int r = 0; r < TR; ++r)
-#pragma unroll
-                for (int c = 0; c < TC; ++c) {
-                    accS[r][c] = fmaf(q[r].x, kk[c].x, accS[r][c]);
-                    accS[r][c] = fmaf(q[r].y, kk[c].y, accS[r][c]);
-                    accS[r][c] = fmaf(q[r].z, kk[c].z, accS[r][c]);
-                    accS[r][c] = fmaf(q[r].w, kk[c].w, accS[r][c]);
-                    accP[r][c] = fmaf(o[r].x, v[c].x, accP[r][c]);
-                    accP[r][c] = fmaf(o[r].y, v[c].y, accP[r][c]);
-                    accP[r][c] = fmaf(o[r].z, v[c].z, accP[r][c]);
-                    accP[r][c] = fmaf(o[r].w, v[c].w, accP[r][c]);
-                }
-        }
+        block_products<D, TR, TC>(sQ, sdO, sK, sV, ty, tx, accS, accP);
         // ---- P = exp(scale S - LSE) on visible pairs, dS = P (dP - D)
 #pragma unroll
         for (int r = 0; r < TR; ++r) {
@@ -371,26 +405,7 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
                 for (int q = 0; q < NG; ++q)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) accQ[r][q][u] = 0.f;
-#pragma unroll 2
-            for (int jj = 0; jj < BN; ++jj) {
-                float ds[TR];
-#pragma unroll
-                for (int r = 0; r < TR; ++r) ds[r] = sdS[(ty + 16 * r) * LP + jj];
-#pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    const int f = tx + 16 * q;
-                    if (NG * 16 * 4 == D || f < D / 4) {
-                        const float4 kv = *reinterpret_cast<const float4*>(sK + jj * LD + 4 * f);
-#pragma unroll
-                        for (int r = 0; r < TR; ++r) {
-                            accQ[r][q][0] = fmaf(ds[r], kv.x, accQ[r][q][0]);
-                            accQ[r][q][1] = fmaf(ds[r], kv.y, accQ[r][q][1]);
-                            accQ[r][q][2] = fmaf(ds[r], kv.z, accQ[r][q][2]);
-                            accQ[r][q][3] = fmaf(ds[r], kv.w, accQ[r][q][3]);
-                        }
-                    }
-                }
-            }
+            add_ds_k<D, TR, NG, BN>(sdS, sK, ty, tx, accQ);
 #pragma unroll
             for (int r = 0; r < TR; ++r) {
                 const int ri = ty + 16 * r;
@@ -430,27 +445,31 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
     }
 }
 
-// Deterministic dQ: one CTA per (kDqRows query rows, head) forms the accumulator rows itself,
-// visiting the visible keys in index order, so every row is one fixed sequence of additions.
-constexpr int kDqRows = 16;
-constexpr int kDqKeys = 32;
-constexpr int kDqThreads = 128;
+// Deterministic dQ of fp32 inputs and of head dim 256: one CTA per (BM query rows, head) forms the
+// accumulator rows itself, visiting the key tiles in index order, so every row is one fixed
+// sequence of additions.  The block products are those of the main kernel.
+template <int D>
+constexpr size_t dq_smem() {
+    using C = SCfg<D>;
+    return sizeof(float) * ((size_t)(2 * C::BN + 2 * C::BM) * C::LD + C::BM * C::LP);
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kDqThreads) packed_dq_simt_kernel(const PackedBwd a, const BwdPlan p) {
-    extern __shared__ float smem[];
-    float* sQ = smem;
-    float* sdO = sQ + kDqRows * D;
-    float* sK = sdO + kDqRows * D;
-    float* sV = sK + kDqKeys * D;
-    float* sdS = sV + kDqKeys * D;
-    constexpr int kPerThread = kDqRows * D / kDqThreads;
-    const int tid = threadIdx.x;
-    const int u = blockIdx.x / (kBwdTile / kDqRows);
+__global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(const PackedBwd a, const BwdPlan p) {
+    using C = SCfg<D>;
+    constexpr int BN = C::BN, BM = C::BM, LD = C::LD, LP = C::LP, TR = C::TR, TC = C::TC, NG = C::NG;
+    extern __shared__ float4 smem4[];
+    float* sK = reinterpret_cast<float*>(smem4);
+    float* sV = sK + BN * LD;
+    float* sQ = sV + BN * LD;
+    float* sdO = sQ + BM * LD;
+    float* sdS = sdO + BM * LD;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int u = blockIdx.x / (kBwdTile / BM);
     if (u >= p.head[0]) return;
     const QueryTile t = p.query[u];
-    const int r0 = (blockIdx.x % (kBwdTile / kDqRows)) * kDqRows;  // within the query tile
-    const int rows = min(kDqRows, t.rows - r0);
+    const int r0 = (blockIdx.x % (kBwdTile / BM)) * BM;  // within the query tile
+    const int rows = min(BM, t.rows - r0);
     if (rows <= 0) return;
     // the sequence of this query tile
     int n = 0;
@@ -468,18 +487,20 @@ __global__ void __launch_bounds__(kDqThreads) packed_dq_simt_kernel(const Packed
     const int off = S_k - S_q;
     const float sc2 = a.scale * 1.4426950408889634f;
     const long long row = (long long)u * kBwdTile + r0;
-    const T* Q = static_cast<const T*>(a.Q) + (long long)(t.q_tok + r0) * a.sq.tok + (long long)h * a.sq.head;
-    const T* dO = static_cast<const T*>(a.dO) + (long long)(t.q_tok + r0) * a.sdo.tok + (long long)h * a.sdo.head;
-    const T* K = static_cast<const T*>(a.K) + (long long)k_tok0 * a.sk.tok + (long long)hk * a.sk.head;
-    const T* V = static_cast<const T*>(a.V) + (long long)k_tok0 * a.sv.tok + (long long)hk * a.sv.head;
-    for (int e = tid; e < kDqRows * D; e += kDqThreads) {
-        const int r = e / D, c = e % D;
-        sQ[e] = r < rows ? TypeTraits<T>::to_f32(Q[r * a.sq.tok + c]) : 0.f;
-        sdO[e] = r < rows ? TypeTraits<T>::to_f32(dO[r * a.sdo.tok + c]) : 0.f;
-    }
-    float acc[kPerThread];
+    stage_rows<T, D>(sQ, static_cast<const T*>(a.Q) + (long long)(t.q_tok + r0) * a.sq.tok + (long long)h * a.sq.head,
+                     a.sq.tok, rows, BM);
+    stage_rows<T, D>(sdO, static_cast<const T*>(a.dO) + (long long)(t.q_tok + r0) * a.sdo.tok + (long long)h * a.sdo.head,
+                     a.sdo.tok, rows, BM);
+    float l2[TR], Di[TR], accQ[TR][NG][4];
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) acc[i] = 0.f;
+    for (int r = 0; r < TR; ++r) {
+        l2[r] = p.lse2[h * p.rows + row + ty + 16 * r];
+        Di[r] = p.D[h * p.rows + row + ty + 16 * r];
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) accQ[r][q][e] = 0.f;
+    }
     Shape sh;
     sh.S_q = S_q;
     sh.S_k = S_k;
@@ -487,40 +508,40 @@ __global__ void __launch_bounds__(kDqThreads) packed_dq_simt_kernel(const Packed
     sh.window = a.window;
     int k_lo, k_hi;
     key_range(sh, m0, m0 + rows, k_lo, k_hi);
-    for (int n0 = k_lo - k_lo % kDqKeys; n0 < k_hi; n0 += kDqKeys) {
+    for (int n0 = k_lo / BN * BN; n0 < k_hi; n0 += BN) {
+        __syncthreads();  // the previous step's reads are done
+        const int krows = min(BN, S_k - n0);
+        stage_rows<T, D>(sK, static_cast<const T*>(a.K) + (long long)(k_tok0 + n0) * a.sk.tok + (long long)hk * a.sk.head,
+                         a.sk.tok, krows, BN);
+        stage_rows<T, D>(sV, static_cast<const T*>(a.V) + (long long)(k_tok0 + n0) * a.sv.tok + (long long)hk * a.sv.head,
+                         a.sv.tok, krows, BN);
         __syncthreads();
-        for (int e = tid; e < kDqKeys * D; e += kDqThreads) {
-            const int j = n0 + e / D, c = e % D;
-            sK[e] = j < S_k ? TypeTraits<T>::to_f32(K[j * a.sk.tok + c]) : 0.f;
-            sV[e] = j < S_k ? TypeTraits<T>::to_f32(V[j * a.sv.tok + c]) : 0.f;
-        }
-        __syncthreads();
-        for (int pr = tid; pr < kDqRows * kDqKeys; pr += kDqThreads) {
-            const int r = pr / kDqKeys, jj = pr % kDqKeys;
-            const int j = n0 + jj;
-            float ds = 0.f;
-            if (r < rows && j < S_k && key_visible(m0 + r + off, j, a.causal, a.window)) {
-                float sc = 0.f, dp = 0.f;
-                for (int c = 0; c < D; ++c) {
-                    sc = fmaf(sQ[r * D + c], sK[jj * D + c], sc);
-                    dp = fmaf(sdO[r * D + c], sV[jj * D + c], dp);
-                }
-                const float pv = exp2f(fmaf(sc, sc2, -p.lse2[h * p.rows + row + r]));
-                ds = pv * (dp - p.D[h * p.rows + row + r]);
-            }
-            sdS[pr] = ds;
-        }
-        __syncthreads();
+        float accS[TR][TC], accP[TR][TC];
+        block_products<D, TR, TC>(sQ, sdO, sK, sV, ty, tx, accS, accP);
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int e = tid + i * kDqThreads, r = e / D, c = e % D;
-            for (int jj = 0; jj < kDqKeys; ++jj) acc[i] = fmaf(sdS[r * kDqKeys + jj], sK[jj * D + c], acc[i]);
+        for (int r = 0; r < TR; ++r) {
+            const int ri = ty + 16 * r;
+#pragma unroll
+            for (int c = 0; c < TC; ++c) {
+                const int j = n0 + tx + 16 * c;
+                const bool vis = ri < rows && j < S_k && key_visible(m0 + ri + off, j, a.causal, a.window);
+                sdS[ri * LP + tx + 16 * c] = vis ? exp2f(fmaf(accS[r][c], sc2, -l2[r])) * (accP[r][c] - Di[r]) : 0.f;
+            }
         }
+        __syncthreads();
+        add_ds_k<D, TR, NG, BN>(sdS, sK, ty, tx, accQ);
     }
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        const int e = tid + i * kDqThreads, r = e / D, c = e % D;
-        if (r < rows) p.dqacc[((row + r) * a.H + h) * D + c] = acc[i];
+    for (int r = 0; r < TR; ++r) {
+        const int ri = ty + 16 * r;
+        if (ri >= rows) continue;
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const int f = tx + 16 * q;
+            if (NG * 16 * 4 == D || f < D / 4)
+                *reinterpret_cast<float4*>(p.dqacc + ((row + ri) * a.H + h) * D + 4 * f) =
+                    make_float4(accQ[r][q][0], accQ[r][q][1], accQ[r][q][2], accQ[r][q][3]);
+        }
     }
 }
 
@@ -565,12 +586,11 @@ cudaError_t bwd_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t dq_ordered_t(const PackedBwd& a, const BwdPlan& p, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (2 * kDqRows * D + 2 * kDqKeys * D + kDqRows * kDqKeys);
     auto kern = packed_dq_simt_kernel<T, D>;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_smem(kern, (int)smem, ready);
+    cudaError_t e = allow_smem(kern, (int)dq_smem<D>(), ready);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(p.max_units * (kBwdTile / kDqRows)), (unsigned)a.H), kDqThreads, smem, st>>>(a, p);
+    kern<<<dim3((unsigned)(p.max_units * (kBwdTile / SCfg<D>::BM)), (unsigned)a.H), kThreads, dq_smem<D>(), st>>>(a, p);
     return cudaGetLastError();
 }
 
