@@ -20,6 +20,12 @@
 //   * the accumulator, D and the LSE copy have their rows padded to whole query tiles per
 //     sequence, so a tile's reduce-add touches its own rows only;
 //   * P stays in fp32 between the two softmax passes, so dS carries one rounding, not two.
+//
+// Bound, like the dense kernel, by the chain of products through TMEM and the bulk-copy unit (Q
+// and dO tiles in, dQ reduce-adds out); DRAM runs at half its rate.  Measured, causal bf16,
+// H = 32, H_kv = 8, d = 128: ten sequences of 7 to 2048 tokens (11390 in all) 404 us of a call's
+// 524 (980 TFLOP/s); the whole call at 4 x 4096 tokens 1346 us (1020 TFLOP/s), deterministic
+// 1707 us; H = H_kv = 16, d = 64 521 us (660 TFLOP/s), deterministic 737 us.
 #include <math.h>
 
 #include "bounded_wait.cuh"
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
     // At d = 128 the Q and dO stages are loaded and released separately: the drain stages half
     // of dQ(i) in the dO tile, and the Q tile of iteration i+2 (for S(i+2) and the P pass) need
     // not wait until TMA has read that out.  At d = 64 both tiles of an iteration share one
-    // full and one empty barrier (measured 3 % faster there).
+    // full and one empty barrier (3 % faster there in the dense kernel).
     constexpr bool kSplitRing = D == 128;
     auto full_q = [&](int s) { return bar(B_STAGE0 + s); };
     auto empty_q = [&](int s) { return bar(B_STAGE0 + C::STAGES + s); };
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
         // barriers without blocking on either.
         if (lane == 0 && !*abort_flag) {
             // K and V are read by this CTA alone: their lines go first when L2 needs room (the dQ
-            // accumulator lines the reduce-adds update stay; measured 0.6 % faster)
+            // accumulator lines the reduce-adds update stay; 0.6 % faster in the dense kernel)
             const uint64_t kv_pol = ptx::policy_evict_first();
             for (int i = 0; i < 4; ++i) tensormap_acquire(tmQ + i);  // written by the plan kernel
             ptx::mbar_arrive_expect_tx(bar(B_KV), 2 * C::kTileK_B);
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
         // ------------------------------------------------------------ MMA issuers
         // With two TMEM buffers warp 13 issues every product.  With three (d = 64) warp 13
         // issues S and dP and warp 14 dV, dQ and dK, so that no product waits behind another's
-        // inputs in one thread's program order (measured with clock64 stamps: one issuer
+        // inputs in one thread's program order (clock64 stamps in the dense kernel: one issuer
         // waiting for the dK product of iteration i-1 before S(i+1) saw P(i) ~2.4K cycles
         // late).  Every hazard between the two is on a barrier: S(i+1) into yb(i-1) waits for
         // that buffer's Y-free barrier (the dK product of iteration i-1, one barrier per
@@ -561,8 +567,8 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
             if (!(ok = wait_bar_warp(bar(B_DP_FULL), it & 1, abort_flag, err))) break;
             // The dS tile of this iteration was last used NDS iterations ago.  At d = 128 its
             // release is waited for only just before the stores below, so the dP load and the
-            // arithmetic overlap the wait (measured 335 -> 331 us on the bench shape, 1193 ->
-            // 1165 us on fp16 S = 8192; at d = 64 it made no gain and stays here).
+            // arithmetic overlap the wait (1 to 2 % faster in the dense kernel; at d = 64 it made
+            // no gain there and stays here).
             if (D != 128 && it >= NDS &&
                 !(ok = wait_bar_warp(bar(B_DS_EMPTY + dt(it)), ((it - NDS) / NDS) & 1, abort_flag, err)))
                 break;
@@ -728,8 +734,8 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
         // ------------------------------------------------------------ deterministic dQ adds
         // One thread waits for each staged dQ(i), takes the tile's turn, issues the
         // reduce-adds and passes the turn on once they are complete, so none of these waits
-        // holds up the drain (measured 9 % faster in deterministic mode than in the drain's
-        // issuer; the default mode keeps the issuer, 2-4 % faster there).
+        // holds up the drain (in the dense kernel 9 % faster in deterministic mode than in the
+        // drain's issuer; the default mode keeps the issuer, 2-4 % faster there).
         if (lane == 0 && det) {
             ptx::griddep_wait();
             ptx::fence_proxy_async_global();

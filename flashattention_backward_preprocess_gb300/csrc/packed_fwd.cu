@@ -21,12 +21,20 @@
 //     zeroed in shared memory before the P V product: P is 0 there, but 0 * inf is not;
 //   * S = Q K^T and O += P V with tcgen05.mma, P as the TMEM A operand; three S buffers
 //     (two at d = 256); eight softmax warps (two threads per row), four epilogue warps, a warp
-//     each for TMA, the S products and the P V products.  The next item's loads, S products and
-//     softmax overlap this item's epilogue.  Softmax warps whose rows are all padding (single-token steps fill
-//     g of 128 rows) only pass the barriers on;
+//     each for the loads of Q and K, the loads of V, the S products and the P V products.  The
+//     next item's loads, S products and softmax overlap this item's epilogue.  Softmax warps
+//     whose rows are all padding (single-token steps fill g of 128 rows) only pass the
+//     barriers on;
 //   * P is rounded to the inputs' 16-bit type for the product (the tensor core's operand type);
 //     the row sum adds the unrounded fp32 values;
 //   * every wait is bounded: a timeout records an error word, the roles drop out, TMEM is freed.
+//
+// Bound by the softmax on long prompts (about 1250 cycles of a key tile's 1400), by DRAM on
+// single-token steps, by latency on small calls.  Measured, causal bf16, times of a replayed
+// graph: 4 x 4096 tokens, H = 32, H_kv = 8, d = 128 401 us (1370 TFLOP/s), 8 prompts of 1 to
+// 4096 tokens (16280 in all) 333 us (1220 TFLOP/s); 4 x 4096, H = H_kv = 16, d = 64 195 us
+// (705 TFLOP/s); 2 x 4096, H = 16, H_kv = 4, d = 256 275 us (1000 TFLOP/s); 64 requests, one
+// token each, over 1.14 GB of a cache of 16-row pages 178 us (6.4 TB/s).
 #include <math.h>
 
 #include "bounded_wait.cuh"
@@ -143,8 +151,8 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 // per page and tensor brings all its columns, so a tile lies in shared memory as groups of 8
 // rows, each with its 64-column blocks one after another, instead of one block of all rows
 // after another.  Small boxes are what bounds a cache of small pages (about 60 ns a box,
-// whatever it holds): with pages of 16 rows the 64 x 4096-token step took 253 us with a box
-// per 64 columns.
+// whatever it holds): a step of 64 tokens over 4096 each in pages of 16 rows took 253 us with
+// a box per 64 columns and 175 us with one per page.
 template <typename T, int D, bool kPaged, bool kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -689,6 +697,8 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     geo.ctas = sm_count();
     geo.D = D;
     geo.min_chunk = 2;
+    // filling the pipeline and the epilogue cost about three tiles' time.  With 2 (3 for items
+    // of one tile) mixed prompts took 328 us against 333, chunks over a cache 119 against 115
     geo.overhead = 3;
     const long long units = plan_units(a, geo);
     geo.self = units <= kSelfUnits && a.N <= kSelfUnits;

@@ -1,7 +1,9 @@
 // packed_plan.cu -- work plans of the packed and paged operators, built on the device from the
 // sequence lengths so that no call has to read them back.  One block plans (prefix sums over
 // sequences and units, a few microseconds); the other blocks fill the output rows that belong
-// to no sequence when the caller asked for that.
+// to no sequence when the caller asked for that.  Bound by latency: the forward plan of few
+// sequences is made by every CTA of the forward itself instead (plan_self), which saves the
+// launch; the backward's takes about 7 us of the 524 of ten sequences (11390 tokens).
 #include "packed.cuh"
 #include "tma_map.cuh"
 

@@ -9,9 +9,12 @@
 //   table[n][have_n + i] = free_pages[first_n + i]       for i < need_n - have_n
 // The blocks of the first part write table columns >= have_n, those of the second read columns
 // < have_n and the free list, so the parts need no order.  Bound by latency: a block reads the
-// lengths of the requests before it (coalesced) and makes one or two dependent look-ups.
+// lengths of the requests before it (coalesced) and makes one or two dependent look-ups: 2.9 us
+// for 8 requests of a token each, 9.7 us for 1024 of up to 128.
 //
-// paged_write: rows of K and V to their slots, 16 bytes per access; bound by DRAM bandwidth.
+// paged_write: rows of K and V to their slots, 16 bytes per access; bound by DRAM bandwidth:
+// 16384 tokens of H_kv = 8, d = 128, bf16 (134 MB moved) take 20 us (6.7 TB/s).  Two and four
+// pieces in flight per thread took 20.2 and 24.2 us.
 #include "packed.cuh"
 #include "paged_cache.cuh"
 
