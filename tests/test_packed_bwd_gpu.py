@@ -270,3 +270,29 @@ def test_bad_lengths_leave_gradients_alone():
                 assert all((x == 4).all() for x in out)
                 with pytest.raises(fa.FaError, match="sequence lengths"):
                     fa.fa_check_device()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_offsets_past_32_bits(dtype, d):
+    """Sequences behind element 2^31 of the packed tensors give the bits that they give alone."""
+    H, lens, dt = 32, [130, 77], DT[dtype]
+    n = sum(lens)
+    T = (1 << 31) // (H * d) + 1000
+    gen = torch.Generator().manual_seed(6)
+    small = [torch.randn(n, H, d, generator=gen).to(dt).cuda() for _ in range(4)]
+    cu = _cu(lens)
+    out = []
+    for first in (0, T - n):
+        Q, K, V, dO = big = [torch.empty(first + n, H, d, dtype=dt, device="cuda") for _ in range(4)]
+        for b, x in zip(big, small):
+            b[first:] = x
+        c = cu + first
+        O, LSE = fa.fa_varlen_fwd(Q, K, V, c, c, causal=True)
+        grads = fa.fa_varlen_bwd(dO, Q, K, V, O, LSE, c, c, causal=True, deterministic=True)
+        assert first == 0 or not any(x[first - 1].any() or x[0].any() for x in (O, *grads))
+        out.append([x[first:].clone() for x in (O, *grads)] + [LSE[:, first:].clone()])
+        torch.cuda.synchronize()
+        del Q, K, V, dO, big, b, O, LSE, grads
+    fa.fa_check_device()
+    torch.cuda.empty_cache()
+    assert all(torch.equal(a, b) for a, b in zip(*out))

@@ -378,3 +378,28 @@ def test_empty_head_dimension_is_refused():
                  lambda: fa.fa_paged_fwd(q, cache, cache, table, cu, lens)):
         with pytest.raises(fa.FaError, match=" d:"):
             call()
+
+
+@pytest.mark.parametrize("dtype,page,H_kv,d", [("bf16", 16, 8, 128), ("bf16", 5, 8, 128), ("f16", 64, 4, 256)])
+def test_paged_offsets_past_32_bits(dtype, page, H_kv, d):
+    """Pages at the far end of a cache of more than 2^32 elements give what a small cache gives."""
+    pages = (1 << 32) // (page * H_kv * d) + 20
+    H, ctx, dt = 2 * H_kv, 3 * page + 2, DT[dtype]
+    gen = torch.Generator().manual_seed(5)
+    Q = torch.randn(1, H, d, generator=gen).to(dt).cuda()
+    K, V = (torch.randn(ctx, H_kv, d, generator=gen).to(dt).cuda() for _ in range(2))
+    lens, cu = torch.tensor([ctx], dtype=torch.int32, device="cuda"), _cu([1])
+    out = []
+    for n in (20, pages):
+        caches = [torch.empty(n, page, H_kv, d, dtype=dt, device="cuda") for _ in range(2)]
+        table = torch.tensor([[n - 1, n - 9, n - 2, n - 20]], dtype=torch.int32, device="cuda")
+        at = torch.arange(ctx, device="cuda")
+        slots = table[0, at // page].long() * page + at % page
+        fa.fa_paged_write(K, V, slots, *caches)
+        assert torch.equal(caches[0].view(-1, H_kv, d)[slots], K) and torch.equal(caches[1].view(-1, H_kv, d)[slots], V)
+        out.append(fa.fa_paged_fwd(Q, *caches, table, cu, lens))
+        torch.cuda.synchronize()
+        del caches
+    fa.fa_check_device()
+    torch.cuda.empty_cache()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
