@@ -2,7 +2,8 @@
 // on CUDA cores (fp32 inputs).
 //
 // Preprocess, per query row and head: D = sum_c dO_c O_c (fp32), LSE * log2 e into rows padded
-// to whole query tiles (+inf on padding rows and rows without keys, so their P is 0), and the
+// to whole query tiles (+inf on padding rows and rows without keys, so their P is 0; the NaN of a
+// row that sees one stays, and makes its P NaN), and the
 // row of the fp32 dQ accumulator set to zero.  dQ: scale times the accumulator, rounded once.
 // Both read and write each byte once and are bound by DRAM: 60 us and 38 us for 11390 bf16
 // tokens of H = 32, d = 128 (a row and head read 512 bytes, write 512 of accumulator; read 512,
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) packed_preprocess_kernel(const Packe
                 const long long row = h * p.rows + (long long)u * kBwdTile + r;
                 const float l = valid ? a.LSE[(size_t)h * a.T_q + t.q_tok + r] : -INFINITY;
                 p.D[row] = acc[b];
-                p.lse2[row] = (l == -INFINITY || isnan(l)) ? INFINITY : l * 1.4426950408889634f;
+                p.lse2[row] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
             }
         }
     }

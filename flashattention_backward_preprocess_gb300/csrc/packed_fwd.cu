@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ka;
             }
             ptx::tc_fence_after();
-            const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+            const float inv_l = inv_sum(l_run);
             const int tok = w.t.q_tok + ti, head = w.hd * g + th;
             const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
             if (warp_live) {
@@ -634,8 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (row_valid) {
                     if (whole)
-                        a.LSE[(size_t)head * a.T_q + tok] =
-                            l_run > 0.f ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+                        a.LSE[(size_t)head * a.T_q + tok] = lse_of(m_run, l_run);
                     else
                         plan.part_ml[(size_t)slot * BM + t] = make_float2(m_run, l_run);
                 }

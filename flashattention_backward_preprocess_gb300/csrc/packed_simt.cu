@@ -123,11 +123,13 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o, 16));
                 const float mn = fmaxf(m[i], rmax);
+                // no max yet: a masked score gives exp2(-inf) = 0, a NaN one (left out of the max) NaN
+                const float base = mn == -INFINITY ? 0.f : mn;
                 const float alpha = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
                 float rs = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const float pv = mn == -INFINITY ? 0.f : exp2f(sc[i][b] - mn);
+                    const float pv = exp2f(sc[i][b] - base);
                     sP[r * BN + tx * 4 + b] = pv;
                     rs += pv;
                 }
@@ -159,13 +161,11 @@ __global__ void __launch_bounds__(kThreads)
             if (r >= rows) continue;
             const int tok = w.t.q_tok + r / gh, head = head0 + r % gh;
             if (whole) {
-                const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+                const float inv = inv_sum(l[i]);
                 T* Orow = static_cast<T*>(a.O) + (long long)tok * a.o.tok + (long long)head * a.o.head;
 #pragma unroll
                 for (int cc = 0; cc < CPT; ++cc) Orow[tx + 16 * cc] = TypeTraits<T>::from_f32(acc[i][cc] * inv);
-                if (tx == 0)
-                    a.LSE[(size_t)head * a.T_q + tok] =
-                        l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+                if (tx == 0) a.LSE[(size_t)head * a.T_q + tok] = lse_of(m[i], l[i]);
             } else {
                 float* Prow = plan.part_o + ((size_t)slot * BM + r) * D;
 #pragma unroll
