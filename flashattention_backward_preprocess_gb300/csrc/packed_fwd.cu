@@ -589,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ptx::tc_fence_after();
             const float inv_l = inv_sum(l_run);
+            // its accumulator is 0 times V, which an infinity in V makes NaN
+            const bool keyless = __any_sync(0xffffffffu, l_run == 0.f);
             const int tok = w.t.q_tok + ti, head = w.hd * g + th;
             const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
             if (warp_live) {
@@ -606,6 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) ptx::mbar_arrive(bar(P_OFREE));
                         }
                     } else {
+#pragma unroll
+                        for (int kk = 0; kk < 32; ++kk) o[kk] = 0u;
+                    }
+                    if (keyless && l_run == 0.f) {
 #pragma unroll
                         for (int kk = 0; kk < 32; ++kk) o[kk] = 0u;
                     }

@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(kThreads)
                 const float inv = inv_sum(l[i]);
                 T* Orow = static_cast<T*>(a.O) + (long long)tok * a.o.tok + (long long)head * a.o.head;
 #pragma unroll
-                for (int cc = 0; cc < CPT; ++cc) Orow[tx + 16 * cc] = TypeTraits<T>::from_f32(acc[i][cc] * inv);
+                for (int cc = 0; cc < CPT; ++cc)  // without a key acc is 0 times V, NaN where V is infinite
+                    Orow[tx + 16 * cc] = TypeTraits<T>::from_f32(l[i] == 0.f ? 0.f : acc[i][cc] * inv);
                 if (tx == 0) a.LSE[(size_t)head * a.T_q + tok] = lse_of(m[i], l[i]);
             } else {
                 float* Prow = plan.part_o + ((size_t)slot * BM + r) * D;

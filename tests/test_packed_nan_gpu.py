@@ -1,6 +1,6 @@
 """NaN inside a sequence: rows that see one are NaN in O, LSE and the gradients, whether their item is
-whole or cut into parts, and no other row is touched.  Rows that see no NaN are held to the bounds of
-tests/packed_ref.py on the clean data."""
+whole or cut into parts, and no other row is touched; a row without keys stays 0 and -inf whatever V
+holds.  Rows that see no NaN are held to the bounds of tests/packed_ref.py on the clean data."""
 import math
 
 import pytest
@@ -74,6 +74,22 @@ def test_paged_fwd_keeps_nan(dtype, page, where):
     O, LSE = fa.fa_paged_fwd(Q, K, V, table, _cu(new), lens)
     k, v = torch.cat([clean[1][0], clean[1][2]]), torch.cat([clean[1][1], clean[1][3]])
     _check_rows(O, LSE, hit, (clean[0], k, v), new, total, True, dt)
+
+
+@pytest.mark.parametrize("dtype,H,H_kv,d", PATHS[:5])
+@pytest.mark.parametrize("lq,lk", [([4, 9], [2, 9]), ([300], [200]), ([3], [1])])
+def test_rows_without_keys_stay_zero(dtype, H, H_kv, d, lq, lk):
+    """Causal, more queries than keys: the first rows see nothing, so no infinity of V reaches them."""
+    dt = DT[dtype]
+    Q, K, V = _packed(9, lq, lk, H, H_kv, d, dt)
+    V[0] = math.inf
+    O, LSE = fa.fa_varlen_fwd(Q, K, V, _cu(lq), _cu(lk), causal=True)
+    torch.cuda.synchronize()
+    fa.fa_check_device()
+    none = lq[0] - lk[0]
+    assert (O[:none] == 0).all() and (LSE[:, :none] == -math.inf).all()
+    assert torch.isfinite(LSE[:, none:]).all()
+    assert not torch.isfinite(O[none:lq[0]]).any()  # key 0 is seen by every row that sees one
 
 
 @pytest.mark.parametrize("dtype,H,H_kv,d", PATHS[:5])
