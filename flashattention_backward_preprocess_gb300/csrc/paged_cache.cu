@@ -8,7 +8,8 @@
 //   first_n = free_start + sum_{m < n} (need_m - have_m)
 //   table[n][have_n + i] = free_pages[first_n + i]       for i < need_n - have_n
 // The blocks of the first part write table columns >= have_n, those of the second read columns
-// < have_n and the free list, so the parts need no order.  Bound by latency: a block reads the
+// < have_n and the free list, so the parts need no order.  Every block looks at the lengths of all
+// requests first: if any does not fit, no block hands anything out.  Bound by latency: a block reads the
 // lengths of the requests before it (coalesced) and makes one or two dependent look-ups: 2.9 us
 // for 8 requests of a token each, 9.7 us for 1024 of up to 128.
 //
@@ -29,15 +30,51 @@ struct Req {
     int ctx, fresh, have, taken;
 };
 
-// One request's numbers; false (and an empty request) when its lengths make no sense.
-__device__ __forceinline__ bool request(const PageSlots& a, int n, Req& r) {
-    const int c0 = a.cu_q[n], c1 = a.cu_q[n + 1], ctx = a.ctx_lens[n];
-    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && ctx >= 0 && ctx <= (1 << 30);
-    r.ctx = ok ? ctx : 0;
-    r.fresh = ok ? c1 - c0 : 0;
-    r.have = ceil_div(r.ctx, a.page_size);
-    r.taken = ceil_div(r.ctx + r.fresh, a.page_size) - r.have;
-    return ok;
+// One request's numbers, for lengths that fit.
+__device__ __forceinline__ Req request(const PageSlots& a, int ctx, int fresh) {
+    const int have = ceil_div(ctx, a.page_size);
+    return {ctx, fresh, have, ceil_div(ctx + fresh, a.page_size) - have};
+}
+__device__ __forceinline__ Req request(const PageSlots& a, int n) {
+    return request(a, a.ctx_lens[n], a.cu_q[n + 1] - a.cu_q[n]);
+}
+
+// What a block needs to know of all requests, in one pass over their lengths.
+struct Before {
+    int count, taken;  // requests before the block's own, and the pages they take
+    int bad;           // whether the lengths of some request, before or behind, do not fit
+};
+
+// is_before(n, end of n's rows): whether request n comes before the block's own.
+template <typename F>
+__device__ __forceinline__ Before look_over(const PageSlots& a, Before* sums, F is_before) {
+    Before b = {0, 0, 0};
+#pragma unroll 4
+    for (int n = threadIdx.x; n < a.N; n += kT) {
+        const int c0 = a.cu_q[n], c1 = a.cu_q[n + 1], ctx = a.ctx_lens[n];
+        if (!(c0 >= 0 && c1 >= c0 && c1 <= a.T && ctx >= 0 && ctx <= (1 << 30))) {
+            b.bad = 1;
+        } else if (is_before(n, c1)) {
+            ++b.count;
+            b.taken += request(a, ctx, c1 - c0).taken;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        b.count += __shfl_xor_sync(0xffffffffu, b.count, o);
+        b.taken += __shfl_xor_sync(0xffffffffu, b.taken, o);
+        b.bad |= __shfl_xor_sync(0xffffffffu, b.bad, o);
+    }
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = b;
+    __syncthreads();
+    b = {0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kT / 32; ++w) {
+        b.count += sums[w].count;
+        b.taken += sums[w].taken;
+        b.bad |= sums[w].bad;
+    }
+    return b;
 }
 
 __device__ __forceinline__ int block_sum(int v, int* sums) {
@@ -79,24 +116,25 @@ __device__ __forceinline__ int take(const PageSlots& a, long long i) {
 __global__ void __launch_bounds__(kT) page_slots_kernel(const PageSlots a, int req_blocks) {
     __shared__ int s_sum[kT / 32];
     __shared__ int s_cu[kT + 1], s_ctx[kT], s_first[kT];
+    __shared__ Before s_before[kT / 32];
     const int tid = threadIdx.x;
     const long long start = *a.free_start;
     if ((int)blockIdx.x < req_blocks) {
         // ---- requests: table entries, lengths, where the free list goes on
-        const int r0 = blockIdx.x * kT;
-        int before = 0;
-        for (int n = tid; n < r0; n += kT) {
-            Req r;
-            request(a, n, r);
-            before += r.taken;
+        const int r0 = blockIdx.x * kT, n = r0 + tid;
+        const Before b = look_over(a, s_before, [&](int m, int) { return m < r0; });
+        if (b.bad) {  // nothing is handed out: the requests hold what they held
+            if (n < a.N) a.seq_lens[n] = a.ctx_lens[n];
+            if (n == 0) {
+                *a.free_next = (int)start;
+                atomicOr(a.err, kErrLengths);
+            }
+            return;
         }
-        before = block_sum(before, s_sum);
-        const int n = r0 + tid;
         Req r = {0, 0, 0, 0};
-        bool bad = false;
-        if (n < a.N) bad = !request(a, n, r);
-        const int at = before + block_scan(r.taken, s_sum);
-        unsigned e = bad ? kErrLengths : 0u;
+        if (n < a.N) r = request(a, n);
+        const int at = b.taken + block_scan(r.taken, s_sum);
+        unsigned e = 0u;
         if (n < a.N) {
             a.seq_lens[n] = r.ctx + r.fresh;
             if (n == a.N - 1) *a.free_next = (int)(start + at + r.taken);
@@ -123,27 +161,20 @@ __global__ void __launch_bounds__(kT) page_slots_kernel(const PageSlots a, int r
     // ---- tokens: position and slot of rows [t0, t0 + kT)
     const int t0 = (blockIdx.x - req_blocks) * kT, t = t0 + tid;
     // the first request that ends behind t0, and the pages taken before it
-    int count = 0, before = 0;
-    for (int n = tid; n < a.N; n += kT)
-        if (a.cu_q[n + 1] <= t0) {
-            Req r;
-            request(a, n, r);
-            ++count;
-            before += r.taken;
-        }
-    int n0 = block_sum(count, s_sum);
-    before = block_sum(before, s_sum);
+    const Before b = look_over(a, s_before, [&](int, int end) { return end <= t0; });
+    int n0 = b.count, before = b.taken;
     const int t_end = min(t0 + kT, a.T);
     bool done = t >= a.T;
     if (t < a.T) {
         a.slots[t] = -1;  // rows behind the last request
         a.positions[t] = -1;
     }
+    if (b.bad) return;  // no row has a slot
     // windows of kT requests until one ends behind the block's last token
     while (n0 < a.N) {
         const int n = n0 + tid;
         Req r = {0, 0, 0, 0};
-        if (n < a.N) request(a, n, r);
+        if (n < a.N) r = request(a, n);
         const int at = before + block_scan(r.taken, s_sum);
         const int live = min(kT, a.N - n0);
         s_first[tid] = at;

@@ -217,6 +217,7 @@ size_t fa_bwd_workspace_bytes(int B, int H, int S_q, int d);
  * replays with whatever lengths the arrays hold then.  Lengths that do not fit
  * the tensors (decreasing, negative, past T_q / T_k or the table) make the call
  * compute nothing; fa_check_device then reports FA_ERR_INVALID_ARG.
+ * (fa_page_slots, whose outputs steer a cache, says below what it leaves then.)
  */
 
 /*
@@ -292,7 +293,10 @@ size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page
  *   seq_lens    : [N] int32 out, ctx_lens plus the new tokens
  *   free_next   : [1] int32 out, free_start[0] plus the pages taken
  * When the free list or the table has no room, the entries and slots concerned
- * are -1 and fa_check_device reports FA_ERR_INVALID_ARG.  The call changes
+ * are -1 and fa_check_device reports FA_ERR_INVALID_ARG.  Lengths that do not fit
+ * (cu_q decreasing, negative or past T; ctx_lens negative or above 2^30) hand
+ * nothing out: slots and positions are all -1, seq_lens is ctx_lens, free_next is
+ * free_start[0], the table is left alone, and the check reports it.  The call changes
  * neither free_pages nor free_start, so running it again gives the same result;
  * an output that overlaps an input is refused.
  */
