@@ -394,14 +394,16 @@ __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.f 
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
+// The max of a part with the sum's NaN: the max itself leaves NaN out (-inf where all scores are NaN).
+__device__ __forceinline__ float part_max(float m, float l) { return isnan(l) ? l : m; }
 
 // packed_plan.cu
 cudaError_t launch_fwd_plan(const PackedFwd& a, const FwdGeom& g, const FwdPlan& p, cudaStream_t st);
 
 // Joins the parts of one cut item (kThreads threads, all of them past the barrier that follows
 // the last part's arrival): O = sum_k O_k 2^(m_k - M) / sum_k l_k 2^(m_k - M), parts in the order
-// of their keys.  A row sees no key in a part when its l_k is 0; m_k does not tell (the max leaves
-// NaN out, so scores that are all NaN have m_k = -inf and l_k = NaN, which must reach the result).
+// of their keys.  m_k = -inf is a row that sees no key in a part, m_k = NaN one whose scores there hold
+// a NaN (part_max), which reaches the result.
 // s_row: `rows` float2 of shared memory; sync: a barrier of those threads.
 template <typename T, int kThreads, int kRowsLd, int kD, int kBatch, typename Sync>
 __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p, const FwdTile& t, int head0, int g,
@@ -412,11 +414,10 @@ __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p,
 #pragma unroll 4
         for (int k = 0; k < count; ++k) {
             const float2 ml = __ldcg(&p.part_ml[slot(k) + r]);
-            if (ml.y == 0.f) continue;
             if (ml.x > M) {
                 L = L * exp2f(M - ml.x) + ml.y;
                 M = ml.x;
-            } else {
+            } else if (ml.x != -INFINITY) {
                 L += ml.y * exp2f(ml.x - M);
             }
         }
@@ -432,21 +433,21 @@ __device__ __forceinline__ void join_parts(const PackedFwd& a, const FwdPlan& p,
         for (int b = 0; b < kBatch; ++b) s[b] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < count; ++k) {
             float4 o[kBatch];
-            float2 w[kBatch];
+            float w[kBatch];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 const int e = e0 + b * kThreads, r = e / C4;
                 if (r < rows) {
                     o[b] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) + r) * kD) + e % C4);
-                    w[b] = __ldcg(&p.part_ml[slot(k) + r]);
+                    w[b] = __ldcg(&p.part_ml[slot(k) + r]).x;
                 }
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 const int r = (e0 + b * kThreads) / C4;
                 // a part in which the row sees no key adds nothing
-                if (r < rows && w[b].y != 0.f) {
-                    const float f = exp2f(w[b].x - s_row[r].x);
+                if (r < rows && w[b] != -INFINITY) {
+                    const float f = exp2f(w[b] - s_row[r].x);
                     s[b].x += o[b].x * f, s[b].y += o[b].y * f, s[b].z += o[b].z * f, s[b].w += o[b].w * f;
                 }
             }

@@ -589,8 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ptx::tc_fence_after();
             const float inv_l = inv_sum(l_run);
-            // its accumulator is 0 times V, which an infinity in V makes NaN
-            const bool keyless = __any_sync(0xffffffffu, l_run == 0.f);
             const int tok = w.t.q_tok + ti, head = w.hd * g + th;
             const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
             if (warp_live) {
@@ -608,10 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) ptx::mbar_arrive(bar(P_OFREE));
                         }
                     } else {
-#pragma unroll
-                        for (int kk = 0; kk < 32; ++kk) o[kk] = 0u;
-                    }
-                    if (keyless && l_run == 0.f) {
 #pragma unroll
                         for (int kk = 0; kk < 32; ++kk) o[kk] = 0u;
                     }
@@ -642,7 +636,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (whole)
                         a.LSE[(size_t)head * a.T_q + tok] = lse_of(m_run, l_run);
                     else
-                        plan.part_ml[(size_t)slot * BM + t] = make_float2(m_run, l_run);
+                        plan.part_ml[(size_t)slot * BM + t] = make_float2(part_max(m_run, l_run), l_run);
+                    // without a key the accumulator is 0 times V, which an infinity in V makes NaN
+                    if (whole && has && l_run == 0.f)
+#pragma unroll 1
+                        for (int c = 0; c < a.d; c += 8) *reinterpret_cast<uint4*>(Orow + c) = make_uint4(0u, 0u, 0u, 0u);
                 }
             } else if (has && lane == 0) {
                 ptx::mbar_arrive(bar(P_OFREE));

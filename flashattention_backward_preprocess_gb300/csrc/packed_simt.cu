@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads)
                 float* Prow = plan.part_o + ((size_t)slot * BM + r) * D;
 #pragma unroll
                 for (int cc = 0; cc < CPT; ++cc) Prow[tx + 16 * cc] = acc[i][cc];
-                if (tx == 0) plan.part_ml[(size_t)slot * BM + r] = make_float2(m[i], l[i]);
+                if (tx == 0) plan.part_ml[(size_t)slot * BM + r] = make_float2(part_max(m[i], l[i]), l[i]);
             }
         }
         if (!whole) {  // the last part to arrive joins the item
