@@ -23,8 +23,10 @@ class PagedKVCache:
     block_table [rows, max_pages], lens [rows] (tokens held), free_pages and free_start (the next
     unused entry of it) are device tensors; positions [tokens] of the step's new tokens are there
     after begin().  A request row that brings no token in a step (cu_q does not move) costs
-    nothing.  When the pages run out fa_check_device() raises, and the tokens without a page are
-    not cached.
+    nothing.  When the pages run out, or a request outgrows max_pages, fa_check_device() raises, at
+    every step until the row is released.  The tokens without a page are not cached: the row's later
+    tokens see zeros in the place of those that found no page, and nothing of those behind the
+    table's last column.  The other rows go on as ever.
     """
 
     def __init__(self, layers: int, num_pages: int, page_size: int, H_kv: int, d: int, rows: int, max_pages: int,

@@ -54,7 +54,7 @@ struct alignas(16) FwdTile {
     int n_tok;    // query tokens of the unit
     int pos0;     // key position of the first token
     int k_base;   // packed: first key row of the sequence
-    int S_k;      // keys of the sequence
+    int S_k;      // keys of the sequence (paged: of those the table has room for)
     int n_first;  // first key tile that a row sees
     int n_cnt;    // key tiles [n_first, n_first + n_cnt) hold every key a row sees
 };
@@ -238,7 +238,11 @@ struct Seq {
     int q0, nq, k0, nk;
 };
 
-// Lengths of sequence n; false (and empty) if they do not fit the tensors.
+// Keys that a request's row of the table has room for.
+__device__ __forceinline__ long long table_room(const PackedFwd& a) { return (long long)a.max_pages * a.page_size; }
+
+// Lengths of sequence n; false (and empty) if they do not fit the tensors.  A request may be longer
+// than its row of the table: the keys behind it are not in the cache and not seen (make_tile).
 __device__ __forceinline__ bool seq_at(const PackedFwd& a, int n, Seq& s) {
     const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1];
     bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T_q;
@@ -252,13 +256,17 @@ __device__ __forceinline__ bool seq_at(const PackedFwd& a, int n, Seq& s) {
         ok = ok && okk;
     } else {
         const int nk = a.seq_lens[n];
-        // longer than its table, or than positions are kept for, is refused
-        const bool okk = nk >= 0 && nk <= (1 << 28) && nk <= (long long)a.max_pages * a.page_size;
+        const bool okk = nk >= 0 && nk <= (1 << 28);  // what positions are kept for
         s.k0 = 0;
         s.nk = okk ? nk : 0;
         ok = ok && okk;
     }
     return ok;
+}
+
+// Whether a request with new tokens is longer than its row of the table; to be reported.
+__device__ __forceinline__ bool past_table(const PackedFwd& a, const Seq& s) {
+    return a.cu_k == nullptr && s.nq > 0 && s.nk > table_room(a);
 }
 
 // Largest n with first[n] <= u (first is non-decreasing, first[N] > u).
@@ -284,7 +292,7 @@ __device__ __forceinline__ int make_tile(const PackedFwd& a, const FwdGeom& g, i
     t.n_tok = min(g.tpt, s.nq - i0);
     t.pos0 = i0 + s.nk - s.nq;
     t.k_base = s.k0;
-    t.S_k = s.nk;
+    t.S_k = a.cu_k == nullptr ? (int)min((long long)s.nk, table_room(a)) : s.nk;
     Shape sh;
     sh.S_q = s.nq;
     sh.S_k = s.nk;
@@ -292,6 +300,7 @@ __device__ __forceinline__ int make_tile(const PackedFwd& a, const FwdGeom& g, i
     sh.window = a.window;
     int lo, hi;
     key_range(sh, i0, i0 + t.n_tok, lo, hi);
+    hi = min(hi, t.S_k);
     t.n_first = hi > lo ? lo / g.bn : 0;
     t.n_cnt = hi > lo ? (hi + g.bn - 1) / g.bn - t.n_first : 0;
     return max(t.n_cnt, 1) + g.overhead;
@@ -339,6 +348,7 @@ __device__ __forceinline__ void plan_self(const PackedFwd& a, const FwdGeom& g, 
         const int n = n0 + tid;
         Seq q = {0, 0, 0, 0};
         if (n < a.N && !seq_at(a, n, q)) bad = true;
+        if (past_table(a, q) && cta == 0) atomicOr(a.err, kErrLengths);
         int total;
         const int at = block_excl_scan((q.nq + g.tpt - 1) / g.tpt, s->isum, &total);
         if (n < a.N) s->first[n] = U + at;

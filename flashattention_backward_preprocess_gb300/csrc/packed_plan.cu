@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fwd_plan_kernel(const PackedF
         if (n < a.N) {
             Seq s;
             if (!seq_at(a, n, s)) bad = true;
+            if (past_table(a, s)) atomicOr(a.err, kErrLengths);
             units = (s.nq + g.tpt - 1) / g.tpt;
         }
         int total;

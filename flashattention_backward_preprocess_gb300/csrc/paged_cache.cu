@@ -4,7 +4,8 @@
 // (cu_q), the pages it needs, taken from a free list in request order, and for every new token
 // its position and its slot (page * page_size + row).  One launch, no atomics: every block sums
 // the pages taken by the requests before its own, so the outcome depends on the lengths alone.
-//   need_n = ceil((ctx_n + new_n) / page_size),  have_n = ceil(ctx_n / page_size)
+//   need_n = ceil((ctx_n + new_n) / page_size),  have_n = ceil(ctx_n / page_size),
+//            both max_pages at most: a page without a column stays in the free list
 //   first_n = free_start + sum_{m < n} (need_m - have_m)
 //   table[n][have_n + i] = free_pages[first_n + i]       for i < need_n - have_n
 // The blocks of the first part write table columns >= have_n, those of the second read columns
@@ -32,8 +33,8 @@ struct Req {
 
 // One request's numbers, for lengths that fit.
 __device__ __forceinline__ Req request(const PageSlots& a, int ctx, int fresh) {
-    const int have = ceil_div(ctx, a.page_size);
-    return {ctx, fresh, have, ceil_div(ctx + fresh, a.page_size) - have};
+    const int have = min(ceil_div(ctx, a.page_size), a.max_pages);
+    return {ctx, fresh, have, min(ceil_div(ctx + fresh, a.page_size), a.max_pages) - have};
 }
 __device__ __forceinline__ Req request(const PageSlots& a, int n) {
     return request(a, a.ctx_lens[n], a.cu_q[n + 1] - a.cu_q[n]);
@@ -135,9 +136,18 @@ __global__ void __launch_bounds__(kT) page_slots_kernel(const PageSlots a, int r
         if (n < a.N) r = request(a, n);
         const int at = b.taken + block_scan(r.taken, s_sum);
         unsigned e = 0u;
-        if (n < a.N) {
-            a.seq_lens[n] = r.ctx + r.fresh;
-            if (n == a.N - 1) *a.free_next = (int)(start + at + r.taken);
+        const bool last = n == a.N - 1;
+        if (n < a.N) a.seq_lens[n] = r.ctx + r.fresh;
+        if (last) *a.free_next = (int)(start + at + r.taken);
+        if (__syncthreads_or(last && start + at + r.taken > a.n_free)) {
+            // the list ran out: how far it falls short of all that the tokens ask for
+            int asked = 0;
+            for (int m = tid; m < a.N; m += kT) {
+                const Req q = request(a, m);
+                asked += ceil_div(q.ctx + q.fresh, a.page_size) - ceil_div(q.ctx, a.page_size);
+            }
+            asked = block_sum(asked, s_sum);
+            if (last) *a.free_next = (int)(start + asked);
         }
         // one warp writes one request's entries at a time
         s_first[tid] = at;
@@ -151,8 +161,8 @@ __global__ void __launch_bounds__(kT) page_slots_kernel(const PageSlots a, int r
             for (int i = lane; i < s_ctx[q]; i += 32) {
                 const int col = s_cu[q] + i;
                 const int id = take(a, start + s_first[q] + i);
-                if (col >= a.max_pages || id < 0) e |= kErrPool;
-                if (col < a.max_pages) row[col] = id;
+                if (id < 0) e |= kErrPool;
+                row[col] = id;
             }
         }
         if (e) atomicOr(a.err, e);

@@ -215,7 +215,7 @@ size_t fa_bwd_workspace_bytes(int B, int H, int S_q, int d);
  *                may overlap (graphs replayed side by side included).
  * All lengths are read on the device: no call synchronizes, and a captured call
  * replays with whatever lengths the arrays hold then.  Lengths that do not fit
- * the tensors (decreasing, negative, past T_q / T_k or the table) make the call
+ * the tensors (decreasing, negative, past T_q / T_k or 2^28 tokens) make the call
  * compute nothing; fa_check_device then reports FA_ERR_INVALID_ARG.
  * (fa_page_slots, whose outputs steer a cache, says below what it leaves then.)
  */
@@ -261,7 +261,10 @@ int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, c
  *   cu_q             : [N + 1] int32, the new tokens of request n are rows
  *                      [cu_q[n], cu_q[n+1]) of Q
  *   seq_lens         : [N] int32 tokens in the cache, the new ones included;
- *                      query i sits at position seq_lens[n] - S_q + i
+ *                      query i sits at position seq_lens[n] - S_q + i.  A request
+ *                      longer than max_pages * page_size sees only the tokens that
+ *                      its row of the table has room for; fa_check_device reports
+ *                      it (FA_ERR_INVALID_ARG), the other requests are not touched
  *   strides          : {Q token, Q head, K page, K row, K head, V page, V row,
  *                      V head, O token, O head}
  * F16/BF16 caches whose page_size is a multiple of 8 that divides 128 or is a
@@ -291,9 +294,11 @@ size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page
  *                 rows of no request
  *   positions   : [T] int32 out, position of each token in its request, or -1
  *   seq_lens    : [N] int32 out, ctx_lens plus the new tokens
- *   free_next   : [1] int32 out, free_start[0] plus the pages taken
+ *   free_next   : [1] int32 out, free_start[0] plus the pages taken (plus the pages
+ *                 that the new tokens ask for, when the free list runs out)
  * When the free list or the table has no room, the entries and slots concerned
- * are -1 and fa_check_device reports FA_ERR_INVALID_ARG.  Lengths that do not fit
+ * are -1 and fa_check_device reports FA_ERR_INVALID_ARG; a page that would stand
+ * behind the table's last column is not taken.  Lengths that do not fit
  * (cu_q decreasing, negative or past T; ctx_lens negative or above 2^30) hand
  * nothing out: slots and positions are all -1, seq_lens is ctx_lens, free_next is
  * free_start[0], the table is left alone, and the check reports it.  The call changes
