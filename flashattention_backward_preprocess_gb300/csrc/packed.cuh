@@ -621,7 +621,7 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 }
 
 // packed_api.cu: reads the error word of the packed and paged calls on the current device into
-// *word and clears it.  Returns an fa_status.
+// *word and clears it, so that no bit set meanwhile is lost.  Returns an fa_status.
 int packed_take_error_word(unsigned int* word);
 
 // ---------------------------------------------------------------- page lookup

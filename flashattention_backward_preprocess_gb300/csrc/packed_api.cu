@@ -14,8 +14,13 @@ namespace {
 constexpr int kMaxDevices = 64;
 }
 
-// Error word of the packed and paged calls on each device (zero when the library is loaded).
+// Error word of the packed and paged calls on each device (zero when the library is loaded), and
+// behind it what take_word_kernel last took out of it.
 static __device__ unsigned int g_packed_err[4];
+
+// One step on the device: kernels of other streams may be setting bits meanwhile, and a bit set
+// between a copy and a memset would be cleared unseen.
+static __global__ void take_word_kernel() { g_packed_err[1] = atomicExch(&g_packed_err[0], 0u); }
 
 namespace fa {
 namespace {
@@ -164,8 +169,10 @@ int packed_take_error_word(unsigned int* word) {
     e = cudaMemcpy(word, g_err_ptr[dev], sizeof(unsigned int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_bad("cudaMemcpy", e);
     if (*word != 0) {
-        e = cudaMemset(g_err_ptr[dev], 0, sizeof(unsigned int));
-        if (e != cudaSuccess) return cuda_bad("cudaMemset", e);
+        take_word_kernel<<<1, 1>>>();  // on the stream of the copies
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_bad("take_word launch", e);
+        e = cudaMemcpy(word, g_err_ptr[dev] + 1, sizeof(unsigned int), cudaMemcpyDeviceToHost);
+        if (e != cudaSuccess) return cuda_bad("cudaMemcpy", e);
     }
     return FA_OK;
 }
