@@ -311,11 +311,10 @@ __device__ __forceinline__ long long share_of(long long W, const FwdGeom& g) {
     return c < g.min_chunk ? g.min_chunk : c;
 }
 
-// Rows before the first and behind the last sequence: O = 0, LSE = -inf.
+// Rows before the first and behind the last sequence, or (all) every row: O = 0, LSE = -inf.
 template <typename T>
-__device__ __forceinline__ void fill_rows(const PackedFwd& a, long long first, long long step) {
-    const int lo = a.cu_q[0], hi = a.cu_q[a.N];
-    if (lo < 0 || hi < lo || hi > a.T_q) return;  // reported with the plan
+__device__ __forceinline__ void fill_rows(const PackedFwd& a, bool all, long long first, long long step) {
+    const int lo = all ? 0 : a.cu_q[0], hi = all ? 0 : a.cu_q[a.N];
     const int per = a.d * (int)sizeof(T) / 16;
     const long long n = (long long)(lo + a.T_q - hi) * a.H * per;
     for (long long e = first; e < n; e += step) {

@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         plan_self<kThreads>(a, geo, plan, max_units, sp);
         share = sp->share;
         ptx::fence_proxy_async_smem();
-        if (a.fill) fill_rows<T>(a, blockIdx.x * kThreads + threadIdx.x, (long long)gridDim.x * kThreads);
+        // without any work (lengths that do not fit, say) no row belongs to a sequence
+        if (a.fill) fill_rows<T>(a, share.W == 0, blockIdx.x * kThreads + threadIdx.x, (long long)gridDim.x * kThreads);
         __syncthreads();
     } else {
         share.read(plan, blockIdx.x);

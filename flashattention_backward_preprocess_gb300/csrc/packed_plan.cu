@@ -14,15 +14,38 @@ constexpr int kPlanThreads = 1024;
 
 constexpr int kSmemSeqs = 4096;  // sequences whose unit offsets are also kept in shared memory
 
+// Lengths of sequence n of a backward; false (and empty) if they do not fit the tensors.
+__device__ __forceinline__ bool seq_at(const PackedBwd& a, int n, Seq& s) {
+    const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1], k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T_q && k0 >= 0 && k1 >= k0 && k1 <= a.T_k;
+    s.q0 = q0;
+    s.nq = ok ? q1 - q0 : 0;
+    s.k0 = k0;
+    s.nk = ok ? k1 - k0 : 0;
+    return ok;
+}
+
+// Whether the lengths of any sequence do not fit the tensors (asked by a whole block).
+template <typename A>
+__device__ __forceinline__ bool any_bad(const A& a) {
+    bool bad = false;
+    for (int n = threadIdx.x; n < a.N; n += blockDim.x) {
+        Seq s;
+        bad |= !seq_at(a, n, s);
+    }
+    return __syncthreads_or(bad);
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1) fwd_plan_kernel(const PackedFwd a, const FwdGeom g, const FwdPlan p) {
     ptx::griddep_launch_dependents();
     if (blockIdx.x > 0) {
         const long long first = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
         const long long step = (long long)(gridDim.x - 1) * blockDim.x;
+        const bool all = any_bad(a);  // nothing is computed then: no row is left unset
         if (a.dtype == FA_F32)
-            fill_rows<float>(a, first, step);
+            fill_rows<float>(a, all, first, step);
         else
-            fill_rows<__half>(a, first, step);
+            fill_rows<__half>(a, all, first, step);
         return;
     }
     __shared__ int s_first[kSmemSeqs + 1];
@@ -113,7 +136,6 @@ __device__ __forceinline__ void write_map(CUtensorMap* dst, const CUtensorMap* s
 // rows [0, lo) and [hi, T) of a gradient
 template <typename T>
 __device__ void zero_rows(void* X, RowStride s, int heads, int d, int lo, int hi, int T_all, int part, int parts) {
-    if (lo < 0 || hi < lo || hi > T_all) return;  // reported by the planning block
     const int per = d * (int)sizeof(T) / 16;
     const long long n = (long long)(lo + T_all - hi) * heads * per;
     for (long long e = (long long)part * blockDim.x + threadIdx.x; e < n; e += (long long)parts * blockDim.x) {
@@ -125,20 +147,12 @@ __device__ void zero_rows(void* X, RowStride s, int heads, int d, int lo, int hi
 }
 
 template <typename T>
-__device__ void fill_grads(const PackedBwd& a, int part, int parts) {
-    zero_rows<T>(a.dQ, a.sdq, a.H, a.d, a.cu_q[0], a.cu_q[a.N], a.T_q, part, parts);
-    zero_rows<T>(a.dK, a.sdk, a.H_kv, a.d, a.cu_k[0], a.cu_k[a.N], a.T_k, part, parts);
-    zero_rows<T>(a.dV, a.sdv, a.H_kv, a.d, a.cu_k[0], a.cu_k[a.N], a.T_k, part, parts);
-}
-
-__device__ __forceinline__ bool seq_at(const PackedBwd& a, int n, Seq& s) {
-    const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1], k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T_q && k0 >= 0 && k1 >= k0 && k1 <= a.T_k;
-    s.q0 = q0;
-    s.nq = ok ? q1 - q0 : 0;
-    s.k0 = k0;
-    s.nk = ok ? k1 - k0 : 0;
-    return ok;
+__device__ void fill_grads(const PackedBwd& a, bool all, int part, int parts) {
+    const int q_lo = all ? 0 : a.cu_q[0], q_hi = all ? 0 : a.cu_q[a.N];
+    const int k_lo = all ? 0 : a.cu_k[0], k_hi = all ? 0 : a.cu_k[a.N];
+    zero_rows<T>(a.dQ, a.sdq, a.H, a.d, q_lo, q_hi, a.T_q, part, parts);
+    zero_rows<T>(a.dK, a.sdk, a.H_kv, a.d, k_lo, k_hi, a.T_k, part, parts);
+    zero_rows<T>(a.dV, a.sdv, a.H_kv, a.d, k_lo, k_hi, a.T_k, part, parts);
 }
 
 constexpr int kBuckets = 2048;
@@ -152,10 +166,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     const int tid = threadIdx.x;
     if ((int)blockIdx.x > map_blocks) {
         const int part = blockIdx.x - 1 - map_blocks, parts = gridDim.x - 1 - map_blocks;
+        const bool all = any_bad(a);  // nothing is computed then: no row is left unset
         if (a.dtype == FA_F32)
-            fill_grads<float>(a, part, parts);
+            fill_grads<float>(a, all, part, parts);
         else
-            fill_grads<__half>(a, part, parts);
+            fill_grads<__half>(a, all, part, parts);
         return;
     }
     if (blockIdx.x > 0) {

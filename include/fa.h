@@ -208,7 +208,8 @@ size_t fa_bwd_workspace_bytes(int B, int H, int S_q, int d);
  *                multiple of 16 bytes, every tensor 16-byte aligned, so the
  *                slices of a joint QKV projection can be passed as they are.
  *   fill       : rows of no sequence (before cu_q[0], from cu_q[N] on) are
- *                0 = left as they were, 1 = set to O = 0 and LSE = -inf.
+ *                0 = left as they were, 1 = set to O = 0 and LSE = -inf (every
+ *                row, where the call computes nothing because of its lengths).
  *   workspace  : caller's scratch, 256-byte aligned, of at least the bytes that
  *                the matching *_workspace_bytes function gives.  It needs no
  *                initialisation and must not be shared by calls whose GPU work
