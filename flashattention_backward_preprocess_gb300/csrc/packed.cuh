@@ -510,9 +510,10 @@ struct PackedBwd {
 };
 
 constexpr int kBwdTile = 128;  // query rows and key rows of a plan tile
+constexpr int kSeqMaps = 5;    // tensor maps of a sequence
 
-// A 128-row query tile: rows q_tok .. q_tok + rows - 1 of Q; its place in the list is its place
-// in the padded rows of the accumulator, D and the LSE copy.
+// A 128-row query tile: rows q_tok .. q_tok + rows - 1 of Q and of the accumulator; its place in the
+// list is its place in the padded rows of D and the LSE copy.
 struct QueryTile {
     int q_tok, rows;
 };
@@ -524,7 +525,7 @@ struct alignas(16) KeyTile {
     int S_q, S_k;
     int unit0;  // first query tile of the sequence
     int its;    // query tiles that see a key of this tile
-    int pad;
+    int q_tok;  // first query row of the sequence (row of Q)
 };
 // What one CTA does of a key tile (for one key/value head): share `part` of `parts` of its
 // (query tile, query head) iterations.  A tile with more iterations than an even share of the
@@ -542,10 +543,10 @@ struct BwdPlan {
     KeyWork* cut;         // [max_cut] tiles with more than one part (slot: the first part's)
     float* part;          // [max_slots][H_kv][2: dV, dK][128][d] fp32 sums of the parts
     int *seq_q, *seq_k;   // [N + 1] first query / key tile of each sequence
-    CUtensorMap* maps;    // [N][4] of each sequence: Q, dO, K, V (tensor-core kernel)
+    CUtensorMap* maps;    // [N][kSeqMaps] of each sequence: Q, dO, K, V, accumulator (tensor cores)
     unsigned *sem, *ticket;  // deterministic: turn counters [H][max_units], start-order ticket
     float *lse2, *D;      // [H][rows]
-    float* dqacc;         // [rows][H][d] fp32, not scaled
+    float* dqacc;         // [T_q][H][d] fp32, not scaled
     long long rows;       // max_units * 128
     int max_units, max_keys, max_work, max_cut, max_slots;
     int shares;           // CTAs the iterations are spread over
@@ -590,10 +591,10 @@ inline size_t bwd_plan_layout(const PackedBwd& a, bool tensor_cores, void* ws, B
     q.part = reinterpret_cast<float*>(take((size_t)q.max_slots * a.H_kv * 2 * kBwdTile * a.d * 4));
     q.seq_q = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
     q.seq_k = reinterpret_cast<int*>(take(((size_t)a.N + 1) * 4));
-    q.maps = reinterpret_cast<CUtensorMap*>(take(tensor_cores ? (size_t)a.N * 4 * sizeof(CUtensorMap) : 0));
+    q.maps = reinterpret_cast<CUtensorMap*>(take(tensor_cores ? (size_t)a.N * kSeqMaps * sizeof(CUtensorMap) : 0));
     q.lse2 = reinterpret_cast<float*>(take((size_t)q.rows * a.H * 4));
     q.D = reinterpret_cast<float*>(take((size_t)q.rows * a.H * 4));
-    q.dqacc = reinterpret_cast<float*>(take((size_t)q.rows * a.H * a.d * 4));
+    q.dqacc = reinterpret_cast<float*>(take((size_t)a.T_q * a.H * a.d * 4));
     if (p) *p = q;
     return at;
 }
@@ -610,9 +611,6 @@ cudaError_t launch_packed_bwd_simt(const PackedBwd& a, const BwdPlan& p, cudaStr
 // packed_bwd_simt.cu: the accumulator in deterministic mode where the main kernel leaves it out
 // (f32, head dim 256)
 cudaError_t launch_packed_dq_ordered(const PackedBwd& a, const BwdPlan& p, cudaStream_t st);
-
-// Map of the fp32 accumulator [rows][H][d]: boxes of 32 columns, one head, 128 rows.
-bool bwd_acc_map(CUtensorMap* m, const PackedBwd& a, const BwdPlan& p);
 
 // Orders this thread's later uses of a tensor map after its writes (by an earlier kernel).
 __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {

@@ -17,8 +17,9 @@
 //     from the call's maps (tensormap.replace of base and length): the rows behind its end,
 //     which belong to the next sequence or to nobody, read as zeros, so neither the products'
 //     contractions nor a NaN there can carry over;
-//   * the accumulator, D and the LSE copy have their rows padded to whole query tiles per
-//     sequence, so a tile's reduce-add touches its own rows only;
+//   * the reduce-adds go through a map of the sequence's rows of the accumulator as well, which
+//     clips a box that reaches past its end: a tile touches its own rows only, and the accumulator
+//     has no more rows than Q.  D and the LSE copy have their rows padded to whole query tiles;
 //   * P stays in fp32 between the two softmax passes, so dS carries one rounding, not two.
 //
 // Bound, like the dense kernel, by the chain of products through TMEM and the bulk-copy unit (Q
@@ -143,7 +144,7 @@ static_assert(B_STAGE0 == 23, "Cfg::kNumBars counts 23 named barriers before the
 
 template <typename T, int D, bool kDet>
 __global__ void __launch_bounds__(threads_for(kDet, D), 1)
-    packed_bwd_kernel(const __grid_constant__ CUtensorMap tmdQ, const __grid_constant__ Params p) {
+    packed_bwd_kernel(const __grid_constant__ Params p) {
     using C = Cfg<D>;
     constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -225,9 +226,9 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
     const int it0 = (int)((long long)all_it * work.part / work.parts);
     const int n_it = (int)((long long)all_it * (work.part + 1) / work.parts) - it0;
     // tensor maps of this sequence alone: rows past its ends read as zeros
-    const CUtensorMap* tmQ = p.plan.maps + (size_t)kt.n * 4;
-    const CUtensorMap *tmdO = tmQ + 1, *tmK = tmQ + 2, *tmV = tmQ + 3;
-    const long long acc_rows = p.plan.rows;  // rows of the fp32 dQ accumulator and of D / LSE per head
+    const CUtensorMap* tmQ = p.plan.maps + (size_t)kt.n * kSeqMaps;
+    const CUtensorMap *tmdO = tmQ + 1, *tmK = tmQ + 2, *tmV = tmQ + 3, *tmdQ = tmQ + 4;
+    const long long pad_rows = p.plan.rows;  // rows of D / LSE per head
 
     // Buffer roles.  Iteration i computes S(i) -> P(i) -> dQ(i) in buffer xb(i) and
     // dP(i) -> dS(i) in buffer yb(i); dP(i+1) always goes into xb(i) once dQ(i) left it.
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
         h = hk * g + (it0 + it) % g;
         m0 = (m_end - 1 - (it0 + it) / g) * BM;
     };
-    auto acc_row = [&](int m0) { return kt.unit0 * BM + m0; };  // of the accumulator, D and LSE
+    auto pad_row = [&](int m0) { return kt.unit0 * BM + m0; };  // of D and LSE
     // Bulk reduce-adds of the dQ tile staged for iteration it (one thread), then the
     // releases once TMA has read each staging area: the dS tile (B_DS_EMPTY) and, at
     // d = 128, the dO stage, whose second arrival (after the MMA warp's, once the dK
@@ -262,9 +263,9 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
                 // the accumulator lines stay in L2 ahead of the Q / dO stream: the
                 // finalise pass then reads much of dQacc from L2
                 const uint64_t pol = ptx::policy_evict_last();
-                if (h * 64 < a.d) ptx::tma_reduce_add_3d_hint(&tmdQ, area, h * 64, head, acc_row(m0), pol);
+                if (h * 64 < a.d) ptx::tma_reduce_add_3d_hint(tmdQ, area, h * 64, head, m0, pol);
                 if (h * 64 + 32 < a.d)
-                    ptx::tma_reduce_add_3d_hint(&tmdQ, area + BM * 128, h * 64 + 32, head, acc_row(m0), pol);
+                    ptx::tma_reduce_add_3d_hint(tmdQ, area + BM * 128, h * 64 + 32, head, m0, pol);
             }
             ptx::bulk_commit_group();
         }
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
                     ptx::tma_load_3d(sbase + (is_q ? C::OFF_Q : C::OFF_DO) + s * C::kTileQ_B + x * C::kBoxQ_B,
                                      is_q ? tmQ : tmdO, x * 64, h, m0, full);
                 if (is_q) {
-                    const size_t row0 = (size_t)(h * acc_rows + acc_row(m0));
+                    const size_t row0 = (size_t)(h * pad_rows + pad_row(m0));
                     ptx::bulk_load(sbase + C::OFF_LSE + s * BM * 4, p.plan.lse2 + row0, BM * 4, full);
                     ptx::bulk_load(sbase + C::OFF_DD + s * BM * 4, p.plan.D + row0, BM * 4, full);
                 }
@@ -684,6 +685,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         ptx::griddep_wait();  // the accumulator was zeroed by the preprocess pass
         ptx::fence_proxy_async_global();
+        if (!det && t == 0 && n_it > 0) tensormap_acquire(tmdQ);  // written by the plan kernel
         bool ok = !*abort_flag;
         for (int it = 0; ok && it < n_it; ++it) {
             const int s = it % C::STAGES;
@@ -739,6 +741,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
         if (lane == 0 && det) {
             ptx::griddep_wait();
             ptx::fence_proxy_async_global();
+            if (n_it > 0) tensormap_acquire(tmdQ);
             bool ok = !*abort_flag;
             unsigned int* prev_sem = nullptr;  // turn to pass on once complete
             unsigned int prev_turn = 0;
@@ -759,7 +762,7 @@ __global__ void __launch_bounds__(threads_for(kDet, D), 1)
                 int k_lo, k_hi;
                 key_range(sh, m0, min(m0 + BM, S_q), k_lo, k_hi);
                 const unsigned int turn = (unsigned int)(n0 / BN - k_lo / BN);
-                unsigned int* sem = p.plan.sem + (size_t)h * (acc_rows / BM) + acc_row(m0) / BM;
+                unsigned int* sem = p.plan.sem + (size_t)h * (pad_rows / BM) + pad_row(m0) / BM;
                 const bool go = wait_counter(sem, turn, abort_flag, err);
                 ptx::fence_proxy_async_global();  // the earlier turns' adds before ours
                 reduce_staged(s, dt(it), h, m0, go);
@@ -792,8 +795,6 @@ cudaError_t launch_t(const PackedBwd& a, const BwdPlan& plan, cudaStream_t st) {
     using C = Cfg<D>;
     static_assert(C::SMEM <= 232448, "shared memory budget");
     if (plan.max_keys == 0) return cudaSuccess;  // no key rows
-    CUtensorMap tdq;
-    if (!bwd_acc_map(&tdq, a, plan)) return cudaErrorInvalidValue;
     Params p;
     p.a = a;
     p.plan = plan;
@@ -812,7 +813,7 @@ cudaError_t launch_t(const PackedBwd& a, const BwdPlan& plan, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tdq, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const long long row0 = (long long)kt.unit0 * kBwdTile;  // of the sequence in the padded rows
     // tensor maps of this sequence alone: rows past its ends read as zeros
-    const CUtensorMap* tmQ = p.plan.maps + (size_t)kt.n * 4;
+    const CUtensorMap* tmQ = p.plan.maps + (size_t)kt.n * kSeqMaps;
     const CUtensorMap *tmdO = tmQ + 1, *tmK = tmQ + 2, *tmV = tmQ + 3;
 
     if (threadIdx.x == 0) {
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int h, m0;
             iter_coords(it, h, m0);
             const bool a_ok = m0 + ra < S_q, b_ok = m0 + rb < S_q;
-            float* ga = p.plan.dqacc + ((row0 + m0 + ra) * a.H + h) * D + c0;
+            float* ga = p.plan.dqacc + (((long long)kt.q_tok + m0 + ra) * a.H + h) * D + c0;
             float* gb = ga + 8ll * a.H * D;
 #pragma unroll 1
             for (int hc = 0; hc < 2; ++hc) {

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) packed_preprocess_kernel(const Packe
         for (int b = 0; b < kBatch; ++b) {
             const int e = e0 + b * G + threadIdx.x / LPR, r = r0 + e / a.H, h = e % a.H;
             const bool valid = e < total && r < t.rows;
-            float* z = p.dqacc + (((long long)u * kBwdTile + r) * a.H + h) * D;
+            float* z = p.dqacc + (((long long)t.q_tok + r) * a.H + h) * D;
             acc[b] = 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq_kernel(const PackedBwd a, 
             const int e = e0 + b * kThreads;
             if (e < total) {
                 // rows of the block are consecutive in the accumulator
-                const float4* s = reinterpret_cast<const float4*>(p.dqacc + ((long long)u * kBwdTile + r0) * a.H * D) + 2ll * e;
+                const float4* s = reinterpret_cast<const float4*>(p.dqacc + ((long long)t.q_tok + r0) * a.H * D) + 2ll * e;
                 x[b] = __ldcs(s);
                 y[b] = __ldcs(s + 1);
             }
@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
     query_range(sh, n0, min(n0 + BN, S_k), i_begin, i_end);
     const int m_first = i_begin / BM * BM;
     const int nq = i_end > i_begin ? (i_end - m_first + BM - 1) / BM : 0;
-    const long long q_tok0 = nq > 0 ? p.query[kt.unit0].q_tok : 0;  // first query row of the sequence
-    const long long row0 = (long long)kt.unit0 * kBwdTile;          // and in the padded rows
+    const long long q_tok0 = kt.q_tok;                      // first query row of the sequence
+    const long long row0 = (long long)kt.unit0 * kBwdTile;  // and in the padded rows
     // this CTA's share of the iterations (all of them unless the tile is cut)
     const int it_lo = (int)((long long)g * nq * work.part / work.parts);
     const int it_hi = (int)((long long)g * nq * (work.part + 1) / work.parts);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) packed_bwd_simt_kernel(const PackedB
                     for (int q = 0; q < NG; ++q) {
                         const int f = tx + 16 * q;
                         if (NG * 16 * 4 == D || f < D / 4)
-                            ptx::red_add_v4(p.dqacc + ((row0 + m0 + ri) * a.H + h) * D + 4 * f, accQ[r][q][0],
+                            ptx::red_add_v4(p.dqacc + ((q_tok0 + m0 + ri) * a.H + h) * D + 4 * f, accQ[r][q][0],
                                             accQ[r][q][1], accQ[r][q][2], accQ[r][q][3]);
                     }
                 }
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(const PackedBw
         for (int q = 0; q < NG; ++q) {
             const int f = tx + 16 * q;
             if (NG * 16 * 4 == D || f < D / 4)
-                *reinterpret_cast<float4*>(p.dqacc + ((row + ri) * a.H + h) * D + 4 * f) =
+                *reinterpret_cast<float4*>(p.dqacc + (((long long)t.q_tok + r0 + ri) * a.H + h) * D + 4 * f) =
                     make_float4(accQ[r][q][0], accQ[r][q][1], accQ[r][q][2], accQ[r][q][3]);
         }
     }

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fwd_plan_kernel(const PackedF
 
 // ---------------------------------------------------------------- backward
 struct BwdMaps {
-    CUtensorMap m[4];  // Q, dO, K, V of the whole call
+    CUtensorMap m[kSeqMaps];  // Q, dO, K, V, accumulator of the whole call
 };
 
 // The maps of sequence n: the call's, based at its first row and as long as the sequence.
@@ -177,17 +177,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         __shared__ __align__(128) uint32_t s_map[kPlanThreads / 32][32];
         const int lane = tid & 31, w = tid >> 5;
         const long long i = (long long)(blockIdx.x - 1) * (blockDim.x / 32) + w;
-        const int n = (int)(i >> 2), which = (int)(i & 3);
-        if (n >= a.N) return;
+        const int n = (int)(i / kSeqMaps), which = (int)(i % kSeqMaps);
+        if (n >= a.N || (which == 4 && a.d == 256)) return;  // that kernel adds without a map
         Seq s;
         seq_at(a, n, s);
-        const bool q = which < 2;
+        const bool q = which < 2 || which == 4;
         const int len = q ? s.nq : s.nk;
         if (len == 0) return;  // never loaded
-        const RowStride str = which == 0 ? a.sq : which == 1 ? a.sdo : which == 2 ? a.sk : a.sv;
-        const void* base = which == 0 ? a.Q : which == 1 ? a.dO : which == 2 ? a.K : a.V;
+        const void* base = which == 0 ? a.Q : which == 1 ? a.dO : which == 2 ? a.K : which == 3 ? a.V : p.dqacc;
+        // bytes from a row to the next
+        const long long row = which == 4 ? (long long)a.H * a.d * 4
+                                         : (which == 0 ? a.sq : which == 1 ? a.sdo : which == 2 ? a.sk : a.sv).tok * 2;
         write_map(p.maps + i, &maps.m[which], ptx::smem_u32(s_map[w]), s_map[w],
-                  static_cast<const char*>(base) + (long long)(q ? s.q0 : s.k0) * str.tok * 2, len, lane);
+                  static_cast<const char*>(base) + (q ? s.q0 : s.k0) * row, len, lane);
         return;
     }
     __shared__ long long s_sum[33];
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         int lo, hi;
         query_range(sh, t.n0, min(t.n0 + kBwdTile, s.nk), lo, hi);
         t.its = hi > lo ? (hi + kBwdTile - 1) / kBwdTile - lo / kBwdTile : 0;
-        t.pad = 0;
+        t.q_tok = s.q0;
         p.key[v] = t;
         if (v == tid) mine = t.its;
         its += t.its;
@@ -347,11 +349,6 @@ bool row_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es, i
 
 }  // namespace
 
-bool bwd_acc_map(CUtensorMap* m, const PackedBwd& a, const BwdPlan& p) {
-    return row_map(m, p.dqacc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.d, a.H, p.rows > 0 ? p.rows : 1, a.d,
-                   (long long)a.H * a.d, kBwdTile);
-}
-
 cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_cores, cudaStream_t st) {
     static_assert(kBuckets % kPlanThreads == 0 && kBuckets % kSmallPlan == 0, "whole buckets a thread");
     const bool small = a.N <= kSmallPlan && p.max_units <= kSmallPlan && p.max_keys <= kSmallPlan;
@@ -372,7 +369,11 @@ cudaError_t launch_bwd_plan(const PackedBwd& a, const BwdPlan& p, bool tensor_co
             !row_map(&maps.m[2], k, dt, 2, a.d, a.H_kv, 1, a.sk.head, a.sk.tok, rows) ||
             !row_map(&maps.m[3], v, dt, 2, a.d, a.H_kv, 1, a.sv.head, a.sv.tok, rows))
             return cudaErrorInvalidValue;
-        map_blocks = (int)(((long long)a.N * 4 + threads / 32 - 1) / (threads / 32));
+        // the accumulator: boxes of 32 fp32 columns
+        if (a.d <= 128 && !row_map(&maps.m[4], p.dqacc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.d, a.H, 1, a.d,
+                                   (long long)a.H * a.d, kBwdTile))
+            return cudaErrorInvalidValue;
+        map_blocks = (int)(((long long)a.N * kSeqMaps + threads / 32 - 1) / (threads / 32));
     }
     bwd_plan_kernel<<<1 + map_blocks + (a.fill ? 32 : 0), threads, 0, st>>>(a, p, maps, map_blocks);
     return cudaGetLastError();

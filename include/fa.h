@@ -233,7 +233,9 @@ int fa_varlen_fwd(const void* Q, const void* K, const void* V, void* O, float* L
                   int dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of fa_varlen_fwd (backward = 0) or fa_varlen_bwd (backward = 1);
- * 0 for arguments those calls refuse. */
+ * 0 for arguments those calls refuse.  A backward's is 4 T_q H d bytes for dQ in fp32,
+ * 1028 H for each 128-row tile of queries (T_q / 128 + N of them at most), 2048 d
+ * (SMs + H_kv) at most for parts of long key tiles, and about 700 of plan per sequence. */
 size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d, int dtype,
                                  int backward);
 
