@@ -39,6 +39,14 @@ def _refuse(name, reason):
     raise FaError(1, f"{name}: {reason}")
 
 
+def _int32(name, v):
+    """v as the C int it is passed as (ctypes would wrap it around)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        _refuse(name, f"must fit 32 bits, got {v}")
+    return v
+
+
 def _type(t):
     dt = _DT.get(t.dtype)
     if dt is None:
@@ -161,7 +169,7 @@ def fa_varlen_fwd(Q, K, V, cu_q, cu_k, scale: float | None = None, causal: bool 
             N, T_q, T_k, H, H_kv, d,
             None if Q.is_contiguous() and K.is_contiguous() and V.is_contiguous() and o.is_contiguous() else
             _strides(("Q", Q), ("K", K), ("V", V), ("O", o)),
-            _scale(scale, d), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
+            _scale(scale, d), int(bool(causal)), _int32("window_size", window_size), fill, dt, ws.data_ptr(),
             need, st))
         return o, lse
 
@@ -200,7 +208,7 @@ def fa_varlen_bwd(dO, Q, K, V, O, LSE, cu_q, cu_k, scale: float | None = None, c
             gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), N, T_q, T_k, H, H_kv, d,
             None if all(map(_Tensor.is_contiguous, (dO, Q, K, V, O, gq, gk, gv))) else
             _strides(("dO", dO), ("Q", Q), ("K", K), ("V", V), ("O", O), ("dQ", gq), ("dK", gk), ("dV", gv)),
-            _scale(scale, d), int(bool(causal)), int(window_size), int(bool(deterministic)),
+            _scale(scale, d), int(bool(causal)), _int32("window_size", window_size), int(bool(deterministic)),
             fill, dt, ws.data_ptr(), need, st))
         return gq, gk, gv
 
@@ -244,7 +252,7 @@ def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float 
             cu_q.data_ptr(), seq_lens.data_ptr(), N, T_q, pages, page, cols, H, H_kv, d,
             None if Q.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous() and o.is_contiguous() else
             _strides(("Q", Q), ("K_cache", K_cache), ("V_cache", V_cache), ("O", o)),
-            _scale(scale, d), int(bool(causal)), int(window_size), fill, dt, ws.data_ptr(),
+            _scale(scale, d), int(bool(causal)), _int32("window_size", window_size), fill, dt, ws.data_ptr(),
             need, st))
         return o, lse
 
@@ -262,7 +270,7 @@ def fa_page_slots(ctx_lens, cu_q, block_table, free_pages, free_start, page_size
     n_free = free_pages.numel()
     _ints("free_pages", free_pages, (n_free,))
     _ints("free_start", free_start, (1,))
-    tokens = int(tokens)
+    tokens, page_size = _int32("tokens", tokens), _int32("page_size", page_size)
     if tokens < 0:
         _refuse("tokens", f"must be >= 0, got {tokens}")
     dev = _device(ctx_lens, cu_q, block_table, free_pages, free_start, slots, positions, seq_lens, free_next)
@@ -279,7 +287,7 @@ def fa_page_slots(ctx_lens, cu_q, block_table, free_pages, free_start, page_size
         _check(load_library().fa_page_slots(
             ctx_lens.data_ptr(), cu_q.data_ptr(), free_pages.data_ptr(), free_start.data_ptr(), block_table.data_ptr(),
             out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), N, tokens, n_free,
-            int(page_size), cols, st))
+            page_size, cols, st))
         return out
 
     return _call(dev, stream, body)
