@@ -15,6 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import packed
+from .binding import FaError
 
 
 class PagedKVCache:
@@ -53,6 +54,8 @@ class PagedKVCache:
 
     def attend(self, layer: int, Q, K, V, scale: float | None = None, window_size: int = 0):
         """Caches K and V [tokens, H_kv, d] of the step and returns (O, LSE) of Q [tokens, H, d]."""
+        if self.slots is None:
+            raise FaError(1, "slots: attend() before the first begin()")
         packed.fa_paged_write(K, V, self.slots, self.K[layer], self.V[layer])
         return packed.fa_paged_fwd(Q, self.K[layer], self.V[layer], self.block_table, self.cu_q, self.lens, scale=scale,
                                    causal=True, window_size=window_size)
