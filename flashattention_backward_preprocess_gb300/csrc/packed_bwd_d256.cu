@@ -447,12 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
         const int ra = 16 * qd + (lane >> 2), rb = ra + 8;
         const int c0 = 2 * (lane & 3);
+        float* const acc = p.plan.dqacc + ((long long)kt.q_tok + ra) * a.H * D + c0;  // the thread's first row
         bool ok = !*abort_flag && !skip_dq;
         for (int it = 0; ok && it < n_it; ++it) {
             int h, m0;
             iter_coords(it, h, m0);
             const bool a_ok = m0 + ra < S_q, b_ok = m0 + rb < S_q;
-            float* ga = p.plan.dqacc + (((long long)kt.q_tok + m0 + ra) * a.H + h) * D + c0;
+            float* ga = acc + ((long long)m0 * a.H + h) * D;
             float* gb = ga + 8ll * a.H * D;
 #pragma unroll 1
             for (int hc = 0; hc < 2; ++hc) {

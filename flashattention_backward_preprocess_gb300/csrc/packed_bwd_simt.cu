@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(const PackedBw
     const int h = blockIdx.y, hk = h / (a.H / a.H_kv);
     const int off = S_k - S_q;
     const float sc2 = a.scale * 1.4426950408889634f;
-    const long long row = (long long)u * kBwdTile + r0;
+    const long long row = (long long)u * kBwdTile + r0;  // in the padded rows
+    float* const acc = p.dqacc + (((long long)t.q_tok + r0) * a.H + h) * D;
     stage_rows<T, D>(sQ, static_cast<const T*>(a.Q) + (long long)(t.q_tok + r0) * a.sq.tok + (long long)h * a.sq.head,
                      a.sq.tok, rows, BM);
     stage_rows<T, D>(sdO, static_cast<const T*>(a.dO) + (long long)(t.q_tok + r0) * a.sdo.tok + (long long)h * a.sdo.head,
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(const PackedBw
         for (int q = 0; q < NG; ++q) {
             const int f = tx + 16 * q;
             if (NG * 16 * 4 == D || f < D / 4)
-                *reinterpret_cast<float4*>(p.dqacc + (((long long)t.q_tok + r0 + ri) * a.H + h) * D + 4 * f) =
+                *reinterpret_cast<float4*>(acc + (long long)ri * a.H * D + 4 * f) =
                     make_float4(accQ[r][q][0], accQ[r][q][1], accQ[r][q][2], accQ[r][q][3]);
         }
     }
