@@ -24,9 +24,11 @@
 //
 // Bound, like the dense kernel, by the chain of products through TMEM and the bulk-copy unit (Q
 // and dO tiles in, dQ reduce-adds out); DRAM runs at half its rate.  Measured, causal bf16,
-// H = 32, H_kv = 8, d = 128: ten sequences of 7 to 2048 tokens (11390 in all) 404 us of a call's
-// 524 (980 TFLOP/s); the whole call at 4 x 4096 tokens 1346 us (1020 TFLOP/s), deterministic
-// 1707 us; H = H_kv = 16, d = 64 521 us (660 TFLOP/s), deterministic 737 us.
+// H = 32, H_kv = 8, d = 128: ten sequences of 7 to 2048 tokens (11390 in all) 405 us of a call's
+// 521 (980 TFLOP/s); the whole call at 4 x 4096 tokens 1362 us (1010 TFLOP/s), deterministic
+// 1728 us; H = H_kv = 16, d = 64 524 us (656 TFLOP/s), deterministic 745 us.  Maps of the
+// accumulator in device memory instead of one in the parameters cost d = 64 3 us of the 524 and
+// spared d = 128 4 of the 525 (no padded rows).
 #include <math.h>
 
 #include "bounded_wait.cuh"

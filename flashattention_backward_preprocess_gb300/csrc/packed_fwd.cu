@@ -29,12 +29,14 @@
 //     the row sum adds the unrounded fp32 values;
 //   * every wait is bounded: a timeout records an error word, the roles drop out, TMEM is freed.
 //
-// Bound by the softmax on long prompts (about 1250 cycles of a key tile's 1400), by DRAM on
-// single-token steps, by latency on small calls.  Measured, causal bf16, times of a replayed
-// graph: 4 x 4096 tokens, H = 32, H_kv = 8, d = 128 401 us (1370 TFLOP/s), 8 prompts of 1 to
-// 4096 tokens (16280 in all) 333 us (1220 TFLOP/s); 4 x 4096, H = H_kv = 16, d = 64 195 us
-// (705 TFLOP/s); 2 x 4096, H = 16, H_kv = 4, d = 256 275 us (1000 TFLOP/s); 64 requests, one
-// token each, over 1.14 GB of a cache of 16-row pages 178 us (6.4 TB/s).
+// Bound by the softmax on long prompts (about 1250 cycles of a key tile's 1400) and nearly as much by
+// the products (1310 from the first to the last of a tile, in which the tensor pipe itself is active
+// 53 to 60 % of the time: it waits for operands too), by DRAM on single-token steps, by latency on
+// small calls.  Measured, causal bf16, times of a replayed graph: 4 x 4096 tokens, H = 32, H_kv =
+// 8, d = 128 401 us (1370 TFLOP/s), 8 prompts of 1 to 4096 tokens (16280 in all) 333 us (1220
+// TFLOP/s); 4 x 4096, H = H_kv = 16, d = 64 195 us (705 TFLOP/s); 2 x 4096, H = 16, H_kv = 4,
+// d = 256 274 us (1000 TFLOP/s); 64 requests, one token each, over 1.14 GB of a cache of 16-row
+// pages 178 us (6.4 TB/s).
 #include <math.h>
 
 #include "bounded_wait.cuh"

@@ -3,7 +3,7 @@
 // sequences and units, a few microseconds); the other blocks fill the output rows that belong
 // to no sequence when the caller asked for that.  Bound by latency: the forward plan of few
 // sequences is made by every CTA of the forward itself instead (plan_self), which saves the
-// launch; the backward's takes about 7 us of the 524 of ten sequences (11390 tokens).
+// launch; the backward's takes about 7 us of the 521 of ten sequences (11390 tokens).
 #include "packed.cuh"
 #include "tma_map.cuh"
 

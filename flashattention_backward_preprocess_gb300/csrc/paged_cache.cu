@@ -11,8 +11,8 @@
 // The blocks of the first part write table columns >= have_n, those of the second read columns
 // < have_n and the free list, so the parts need no order.  Every block looks at the lengths of all
 // requests first: if any does not fit, no block hands anything out.  Bound by latency: a block reads the
-// lengths of the requests before it (coalesced) and makes one or two dependent look-ups: 2.9 us
-// for 8 requests of a token each, 9.7 us for 1024 of up to 128.
+// lengths of all requests (coalesced) and makes one or two dependent look-ups: 2.8 us for 8
+// requests of a token each, 10.1 us for 1024 of up to 128 (9.9 without a look at those behind it).
 //
 // paged_write: rows of K and V to their slots, 16 bytes per access; bound by DRAM bandwidth:
 // 16384 tokens of H_kv = 8, d = 128, bf16 (134 MB moved) take 20 us (6.7 TB/s).  Two and four

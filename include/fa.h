@@ -200,8 +200,10 @@ size_t fa_bwd_workspace_bytes(int B, int H, int S_q, int d);
  * inside each sequence, with the alignment, causal mask and window of fa_fwd_ex
  * for that sequence's S_q and S_k.  Sequences may be empty on either side: a
  * query that sees no key gets O = 0 and LSE = -inf; one whose visible scores hold
- * a NaN gets NaN in both, and in its gradients.  The pages have no counterpart of
- * these entry points.
+ * a NaN gets NaN in both, and in its gradients.  Nothing crosses from one sequence
+ * to another; inside a sequence a hidden pair counts as weight 0 times its value, so
+ * an infinite or NaN row of K or V may also show in rows that do not see it.  The
+ * pages have no counterpart of these entry points.
  *
  *   strides    : element strides in host memory, or NULL for dense tensors; the
  *                head dimension itself is contiguous.  Every stride is > 0 and a
