@@ -1,6 +1,7 @@
 """GB300 (sm_103a) FlashAttention-2 backward: preprocess D = rowsum(dO * O),
 then dQ, dK, dV from a tcgen05 tensor-core kernel; the same over packed sequences of
-different lengths, and the forward over paged key/value caches (``packed``).
+different lengths, and the forward over paged key/value caches, of the queries' type or in 8
+bits, for causal steps and for trees of drafted tokens (``packed``, ``cache``).
 
 The compute lives in the C-ABI library ``_build/libfa.so`` (include/fa.h);
 this package is the thin Python binding over it (argument marshalling only,
@@ -39,8 +40,13 @@ from .autograd import (  # noqa: F401
 )
 from .packed import (  # noqa: F401
     fa_page_slots,
+    fa_page_trim,
     fa_paged_fwd,
+    fa_paged_keep,
+    fa_paged_read_q8,
     fa_paged_write,
+    fa_paged_write_q8,
+    fa_tree_mask,
     fa_varlen_bwd,
     fa_varlen_fwd,
 )

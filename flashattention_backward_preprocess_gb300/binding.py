@@ -32,7 +32,8 @@ EXPORTS = ("fa_bwd", "fa_bwd_ex", "fa_bwd_noalloc", "fa_bwd_preprocess", "fa_fwd
            "fa_check_device", "fa_profile", "fa_profile_read", "fa_selftest_timeout",
            "fa_last_error", "fa_shutdown", "fa_version",
            "fa_varlen_fwd", "fa_varlen_bwd", "fa_varlen_workspace_bytes", "fa_paged_fwd", "fa_paged_workspace_bytes",
-           "fa_page_slots", "fa_paged_write")
+           "fa_page_slots", "fa_paged_write", "fa_paged_fwd_ex", "fa_paged_workspace_bytes_ex", "fa_paged_write_q8",
+           "fa_paged_read_q8", "fa_tree_mask", "fa_paged_keep", "fa_page_trim")
 
 
 class FaError(RuntimeError):
@@ -98,6 +99,18 @@ def load_library(path: str | None = None):
         lib.fa_page_slots.restype = I
         lib.fa_paged_write.argtypes = [V] * 5 + [I] * 5 + [V, I, V]
         lib.fa_paged_write.restype = I
+        lib.fa_paged_fwd_ex.argtypes = [V] * 11 + [I] * 9 + [V, F, I, I, I, I, V, Z, V]
+        lib.fa_paged_fwd_ex.restype = I
+        lib.fa_paged_workspace_bytes_ex.argtypes = [I] * 8
+        lib.fa_paged_workspace_bytes_ex.restype = Z
+        lib.fa_paged_write_q8.argtypes = lib.fa_paged_read_q8.argtypes = [V] * 7 + [I] * 5 + [V, I, V]
+        lib.fa_paged_write_q8.restype = lib.fa_paged_read_q8.restype = I
+        lib.fa_tree_mask.argtypes = [V] * 5 + [I] * 3 + [V]
+        lib.fa_tree_mask.restype = I
+        lib.fa_paged_keep.argtypes = [V] * 9 + [I] * 8 + [V, I, V]
+        lib.fa_paged_keep.restype = I
+        lib.fa_page_trim.argtypes = [V] * 8 + [I] * 4 + [V]
+        lib.fa_page_trim.restype = I
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_version.restype = ctypes.c_char_p
         lib.fa_shutdown.restype = None

@@ -576,7 +576,8 @@ int fa_check_device(void* stream) {
                     std::string("a packed or paged call was given") +
                         (na_word & kErrLengths ? " sequence lengths that do not fit its tensors;" : "") +
                         (na_word & kErrPage ? " a page or slot outside the cache;" : "") +
-                        (na_word & kErrPool ? " too few free pages or table columns;" : ""));
+                        (na_word & kErrPool ? " too few free pages or table columns;" : "") +
+                        (na_word & kErrTree ? " a parent or path that is none of its request's;" : ""));
     if (status != FA_OK)
         return fail(status, "device", "kernel error word " + std::to_string(words[0] | na_word));
     return FA_OK;

@@ -15,8 +15,9 @@ enum : unsigned int {
     kErrLengths = 4u,  // sequence lengths that do not fit the tensors; nothing was computed
     kErrPage = 8u,     // a table entry or slot outside the cache; read as zeros or not written
     kErrPool = 16u,    // the free list ran out of pages, or a request out of table columns
+    kErrTree = 32u,    // a parent, a path of accepted tokens or a number of them that does not fit its request
 };
-constexpr unsigned kErrArgs = kErrLengths | kErrPage | kErrPool;
+constexpr unsigned kErrArgs = kErrLengths | kErrPage | kErrPool | kErrTree;
 
 // Status for the error words of one check: `ws_word` is the word of the stream's
 // workspace (fa_bwd, fa_fwd, fa_selftest_timeout), `na_word` the word of the

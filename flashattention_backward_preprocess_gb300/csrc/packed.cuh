@@ -36,8 +36,24 @@ struct PackedFwd {
     float scale;
     int causal, window, fill, dtype;
     unsigned int* err;
+    // 8-bit cache: K and V hold e4m3 numbers, these the exponent bytes [pages, H_kv, page_size];
+    // null: K and V have the type of Q
+    const uint8_t *k_exp, *v_exp;
+    // tree of new tokens (paged, causal, no window): bit k of row t (tree_words 64-bit words) says
+    // whether the new token in row t sees its request's k-th new token; null: plain causal
+    const unsigned long long* tree;
+    int tree_words;
     bool paged() const { return cu_k == nullptr; }
+    bool q8() const { return k_exp != nullptr; }
 };
+
+// Value of an exponent byte, 2^(b - 127).  (0 stands for 0; fa_paged_write_q8 writes 97 to 157.)
+__device__ __forceinline__ float exp_value(uint8_t b) { return __uint_as_float((unsigned)b << 23); }
+
+// Whether the new token in row `tok` of Q sees its request's k-th new token, k >= 0.
+__device__ __forceinline__ bool tree_sees(const PackedFwd& a, int tok, int k) {
+    return k < 64 * a.tree_words && (a.tree[(size_t)tok * a.tree_words + (k >> 6)] >> (k & 63) & 1ull);
+}
 
 // ---------------------------------------------------------------- forward plan
 // A unit is `tpt` consecutive query tokens of one sequence; the g query heads of a key/value
@@ -491,8 +507,9 @@ inline cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) 
 }
 
 // Forward launchers: with ws == nullptr only *bytes (the workspace they need) is set.
-// packed_fwd.cu: tensor cores (f16 / bf16)
+// packed_fwd.cu, packed_tree.cu (a.tree set): tensor cores (f16 / bf16)
 cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
+cudaError_t launch_packed_tree(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 // packed_simt.cu: CUDA cores (f32, and layouts that TMA cannot address)
 cudaError_t launch_packed_fwd_simt(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 

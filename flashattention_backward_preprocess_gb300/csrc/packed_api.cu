@@ -31,6 +31,7 @@ unsigned int* g_err_ptr[kMaxDevices] = {};
 // Longest packed axis and longest request: positions, tile numbers and windows stay far from
 // the ends of 32 bits.
 constexpr int kMaxTokens = 1 << 28;
+constexpr int kMaxTreeWords = 1024;  // 64 new tokens of a request each
 
 int bad(const char* arg, const std::string& reason) { return set_error(FA_ERR_INVALID_ARG, arg, reason.c_str()); }
 int cuda_bad(const char* where, cudaError_t e) { return set_error(FA_ERR_CUDA, where, cudaGetErrorString(e)); }
@@ -92,19 +93,40 @@ int check_common(int N, int H, int H_kv, int d, float scale, int causal, int win
     return FA_OK;
 }
 
-// Element strides `s` (n of them): positive, whole 16-byte pieces.
-int check_strides(const long long* s, int n, int dtype) {
-    const int es = dtype == FA_F32 ? 4 : 2;
-    for (int i = 0; i < n; ++i)
-        if (s[i] <= 0 || s[i] * es % 16 != 0 || s[i] >= (1ll << 38))
+int elem_bytes(int dtype) { return dtype == FA_F32 ? 4 : 2; }
+
+// Element strides `s` (n of them): positive, whole 16-byte pieces.  Entries [q8_first, q8_last) are
+// those of an 8-bit cache.
+int check_strides(const long long* s, int n, int dtype, int q8_first = 0, int q8_last = 0) {
+    for (int i = 0; i < n; ++i) {
+        const int es = i >= q8_first && i < q8_last ? 1 : elem_bytes(dtype);
+        if (s[i] <= 0 || s[i] >= (1ll << 38) || s[i] * es % 16 != 0)
             return bad("strides", "entry " + std::to_string(i) + " (" + std::to_string(s[i]) +
                                       ") must be > 0 and a multiple of 16 bytes");
+    }
+    return FA_OK;
+}
+
+// A call's outputs may overlap none of its inputs: blocks read and write at no set time.
+struct Span {
+    const char* name;
+    const void* p;
+    long long bytes;
+};
+template <int kIn, int kOut>
+int check_apart(const Span (&in)[kIn], const Span (&out)[kOut]) {
+    for (const Span& o : out)
+        for (const Span& i : in) {
+            const uintptr_t op = reinterpret_cast<uintptr_t>(o.p), ip = reinterpret_cast<uintptr_t>(i.p);
+            if (op < ip + i.bytes && ip < op + o.bytes)
+                return bad(o.name, std::string("must not overlap ") + i.name);
+        }
     return FA_OK;
 }
 
 // Whether the tensor-core kernel's TMA boxes can address the call.
 bool use_tensor_cores(const PackedFwd& a) {
-    if (a.dtype == FA_F32 || a.H / a.H_kv > 128) return false;
+    if (a.dtype == FA_F32 || a.q8() || a.H / a.H_kv > 128) return false;
     if (!a.paged()) return true;
     const int bn = a.d == 256 ? 64 : 128;  // keys per tile
     // pages of whole 8-row swizzle atoms that divide a tile, or are made of whole tiles
@@ -197,11 +219,17 @@ size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d
     return fwd_bytes(a);
 }
 
-size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype) {
+size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype, int quantised) {
     if (check_common(N, H, H_kv, d, 1.f, 0, 0, 0, dtype) != FA_OK || T_q < 0 || page_size <= 0) return 0;
     PackedFwd a = {};
+    static const uint8_t some = 0;
+    if (quantised) a.k_exp = a.v_exp = &some;
     a.N = N, a.T_q = T_q, a.H = H, a.H_kv = H_kv, a.d = d, a.dtype = dtype, a.page_size = page_size;
     return fwd_bytes(a);
+}
+
+size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype) {
+    return fa_paged_workspace_bytes_ex(N, T_q, H, H_kv, d, page_size, dtype, 0);
 }
 
 int fa_varlen_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q, const int* cu_k,
@@ -276,10 +304,11 @@ int fa_varlen_bwd(const void* dO, const void* Q, const void* K, const void* V, c
     return FA_OK;
 }
 
-int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* O, float* LSE, const int* block_table,
-                 const int* cu_q, const int* seq_lens, int N, int T_q, int num_pages, int page_size, int max_pages, int H,
-                 int H_kv, int d, const long long* strides, float scale, int causal, int window_size, int fill, int dtype,
-                 void* workspace, size_t workspace_bytes, void* stream) {
+int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp, void* O,
+                    float* LSE, const int* block_table, const int* cu_q, const int* seq_lens, const long long* tree,
+                    int tree_words, int N, int T_q, int num_pages, int page_size, int max_pages, int H, int H_kv, int d,
+                    const long long* strides, float scale, int causal, int window_size, int fill, int dtype,
+                    void* workspace, size_t workspace_bytes, void* stream) {
     clear_error();
     int rc;
     if ((rc = check_common(N, H, H_kv, d, scale, causal, window_size, fill, dtype))) return rc;
@@ -287,6 +316,13 @@ int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* 
         (rc = check_count("page_size", page_size, 1, kMaxTokens)) ||
         (rc = check_count("max_pages", max_pages, 1, kMaxTokens)))
         return rc;
+    if ((K_exp == nullptr) != (V_exp == nullptr))
+        return bad(K_exp ? "V_exp" : "K_exp", "an 8-bit cache has exponents for both K and V");
+    if (tree != nullptr) {
+        if (causal != 1) return bad("causal", "must be 1 with a tree");
+        if (window_size != 0) return bad("window_size", "must be 0 with a tree");
+        if ((rc = check_count("tree_words", tree_words, 1, kMaxTreeWords)) || (rc = check_ptr(tree, "tree", 8))) return rc;
+    }
     if ((rc = check_ptr(block_table, "block_table", 4)) || (rc = check_ptr(cu_q, "cu_q", 4)) ||
         (rc = check_ptr(seq_lens, "seq_lens", 4)))
         return rc;
@@ -297,15 +333,26 @@ int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* 
     const long long kr = (long long)H_kv * d, qr = (long long)H * d;
     const long long dense[10] = {qr, d, kr * page_size, kr, d, kr * page_size, kr, d, qr, d};
     const long long* s = strides ? strides : dense;
-    if ((rc = check_strides(s, 10, dtype))) return rc;
+    if ((rc = check_strides(s, 10, dtype, 2, K_exp ? 8 : 2))) return rc;
     PackedFwd a = {};
     a.Q = Q, a.K = K_cache, a.V = V_cache, a.O = O, a.LSE = LSE;
+    a.k_exp = static_cast<const uint8_t*>(K_exp), a.v_exp = static_cast<const uint8_t*>(V_exp);
+    a.tree = reinterpret_cast<const unsigned long long*>(tree), a.tree_words = tree ? tree_words : 0;
     a.cu_q = cu_q, a.seq_lens = seq_lens, a.table = block_table;
     a.N = N, a.T_q = T_q, a.H = H, a.H_kv = H_kv, a.d = d;
     a.pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
     a.q = {s[0], s[1]}, a.k_page = s[2], a.k = {s[3], s[4]}, a.v_page = s[5], a.v = {s[6], s[7]}, a.o = {s[8], s[9]};
     a.scale = scale, a.causal = causal, a.window = window_size, a.fill = fill, a.dtype = dtype;
     return run_fwd(a, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* O, float* LSE, const int* block_table,
+                 const int* cu_q, const int* seq_lens, int N, int T_q, int num_pages, int page_size, int max_pages, int H,
+                 int H_kv, int d, const long long* strides, float scale, int causal, int window_size, int fill, int dtype,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    return fa_paged_fwd_ex(Q, K_cache, V_cache, nullptr, nullptr, O, LSE, block_table, cu_q, seq_lens, nullptr, 0, N, T_q,
+                           num_pages, page_size, max_pages, H, H_kv, d, strides, scale, causal, window_size, fill, dtype,
+                           workspace, workspace_bytes, stream);
 }
 
 int fa_page_slots(const int* ctx_lens, const int* cu_q, const int* free_pages, const int* free_start, int* block_table,
@@ -324,22 +371,11 @@ int fa_page_slots(const int* ctx_lens, const int* cu_q, const int* free_pages, c
         return rc;
     if (num_free > 0 && (rc = check_ptr(free_pages, "free_pages", 4))) return rc;
     if (T > 0 && ((rc = check_ptr(slots, "slots", 8)) || (rc = check_ptr(positions, "positions", 4)))) return rc;
-    // every block reads the inputs of the requests before its own, at no set time
-    struct Span {
-        const char* name;
-        const void* p;
-        long long bytes;
-    };
     const Span in[] = {{"ctx_lens", ctx_lens, 4ll * N}, {"cu_q", cu_q, 4ll * (N + 1)},
                        {"free_pages", free_pages, 4ll * num_free}, {"free_start", free_start, 4}};
     const Span out[] = {{"slots", slots, 8ll * T}, {"positions", positions, 4ll * T}, {"seq_lens", seq_lens, 4ll * N},
                         {"free_next", free_next, 4}, {"block_table", block_table, 4ll * N * max_pages}};
-    for (const Span& o : out)
-        for (const Span& i : in) {
-            const uintptr_t op = reinterpret_cast<uintptr_t>(o.p), ip = reinterpret_cast<uintptr_t>(i.p);
-            if (op < ip + i.bytes && ip < op + o.bytes)
-                return bad(o.name, std::string("must not overlap ") + i.name);
-        }
+    if ((rc = check_apart(in, out))) return rc;
     PageSlots a = {};
     a.ctx_lens = ctx_lens, a.cu_q = cu_q, a.free_pages = free_pages, a.free_start = free_start;
     a.table = block_table, a.slots = slots, a.positions = positions, a.seq_lens = seq_lens, a.free_next = free_next;
@@ -375,6 +411,160 @@ int fa_paged_write(const void* K, const void* V, const long long* slots, void* K
     if ((rc = err_word(&a.err))) return rc;
     const cudaError_t e = launch_paged_write(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_bad("paged_write launch", e);
+    return FA_OK;
+}
+
+// The arguments that writing an 8-bit cache and reading it back share.
+static int q8_args(PagedQ8& a, const void* K, const void* V, const void* K_cache, const void* V_cache, const void* K_exp,
+                   const void* V_exp, const long long* slots, int T, int num_pages, int page_size, int H_kv, int d,
+                   const long long* strides, int dtype) {
+    int rc;
+    if ((rc = check_common(1, H_kv, H_kv, d, 1.f, 0, 0, 0, dtype))) return rc;
+    if ((rc = check_count("T", T, 0, kMaxTokens)) || (rc = check_count("num_pages", num_pages, 1, kMaxTokens)) ||
+        (rc = check_count("page_size", page_size, 1, kMaxTokens)))
+        return rc;
+    if (T == 0) return FA_OK;
+    if ((rc = check_ptr(K, "K", 16)) || (rc = check_ptr(V, "V", 16)) || (rc = check_ptr(slots, "slots", 8)) ||
+        (rc = check_ptr(K_cache, "K_cache", 16)) || (rc = check_ptr(V_cache, "V_cache", 16)) ||
+        (rc = check_ptr(K_exp, "K_exp", 1)) || (rc = check_ptr(V_exp, "V_exp", 1)))
+        return rc;
+    const long long kr = (long long)H_kv * d;
+    const long long dense[10] = {kr, d, kr, d, kr * page_size, kr, d, kr * page_size, kr, d};
+    const long long* s = strides ? strides : dense;
+    if ((rc = check_strides(s, 10, dtype, 4, 10))) return rc;
+    const long long es = elem_bytes(dtype);
+    a.K = const_cast<void*>(K), a.V = const_cast<void*>(V);
+    a.K_cache = const_cast<void*>(K_cache), a.V_cache = const_cast<void*>(V_cache), a.slots = slots;
+    a.k_exp = static_cast<uint8_t*>(const_cast<void*>(K_exp)), a.v_exp = static_cast<uint8_t*>(const_cast<void*>(V_exp));
+    a.T = T, a.H_kv = H_kv, a.d = d, a.pages = num_pages, a.page_size = page_size, a.dtype = dtype;
+    a.k = {s[0] * es, s[1] * es}, a.v = {s[2] * es, s[3] * es};
+    a.kc_page = s[4], a.kc = {s[5], s[6]}, a.vc_page = s[7], a.vc = {s[8], s[9]};
+    return err_word(&a.err);
+}
+
+int fa_paged_write_q8(const void* K, const void* V, const long long* slots, void* K_cache, void* V_cache, void* K_exp,
+                      void* V_exp, int T, int num_pages, int page_size, int H_kv, int d, const long long* strides,
+                      int dtype, void* stream) {
+    clear_error();
+    PagedQ8 a = {};
+    const int rc = q8_args(a, K, V, K_cache, V_cache, K_exp, V_exp, slots, T, num_pages, page_size, H_kv, d, strides, dtype);
+    if (rc != FA_OK || T == 0) return rc;
+    const cudaError_t e = launch_paged_write_q8(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_bad("paged_write_q8 launch", e);
+    return FA_OK;
+}
+
+int fa_paged_read_q8(const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp, const long long* slots,
+                     void* K, void* V, int T, int num_pages, int page_size, int H_kv, int d, const long long* strides,
+                     int dtype, void* stream) {
+    clear_error();
+    PagedQ8 a = {};
+    const int rc = q8_args(a, K, V, K_cache, V_cache, K_exp, V_exp, slots, T, num_pages, page_size, H_kv, d, strides, dtype);
+    if (rc != FA_OK || T == 0) return rc;
+    const cudaError_t e = launch_paged_read_q8(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_bad("paged_read_q8 launch", e);
+    return FA_OK;
+}
+
+int fa_tree_mask(const int* parents, const int* cu_q, const int* ctx_lens, long long* tree, int* positions, int N, int T,
+                 int words, void* stream) {
+    clear_error();
+    int rc;
+    if ((rc = check_count("N", N, 1, kMaxTokens)) || (rc = check_count("T", T, 0, kMaxTokens)) ||
+        (rc = check_count("words", words, 1, kMaxTreeWords)))
+        return rc;
+    if ((rc = check_ptr(cu_q, "cu_q", 4)) || (rc = check_ptr(ctx_lens, "ctx_lens", 4))) return rc;
+    if (T == 0) return FA_OK;
+    if ((rc = check_ptr(parents, "parents", 4)) || (rc = check_ptr(tree, "tree", 8)) ||
+        (rc = check_ptr(positions, "positions", 4)))
+        return rc;
+    const Span in[] = {{"parents", parents, 4ll * T}, {"cu_q", cu_q, 4ll * (N + 1)}, {"ctx_lens", ctx_lens, 4ll * N}};
+    const Span out[] = {{"tree", tree, 8ll * T * words}, {"positions", positions, 4ll * T}};
+    if ((rc = check_apart(in, out))) return rc;
+    TreeMask a = {};
+    a.parents = parents, a.cu_q = cu_q, a.ctx_lens = ctx_lens;
+    a.tree = reinterpret_cast<unsigned long long*>(tree), a.positions = positions;
+    a.N = N, a.T = T, a.words = words;
+    if ((rc = err_word(&a.err))) return rc;
+    const cudaError_t e = launch_tree_mask(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_bad("tree_mask launch", e);
+    return FA_OK;
+}
+
+int fa_paged_keep(const int* path, const int* count, const int* cu_q, const int* seq_lens, const int* block_table,
+                  void* const* K_caches, void* const* V_caches, void* const* K_exps, void* const* V_exps, int layers,
+                  int N, int T, int num_pages, int page_size, int max_pages, int H_kv, int d, const long long* strides,
+                  int dtype, void* stream) {
+    clear_error();
+    int rc;
+    if ((rc = check_common(N, H_kv, H_kv, d, 1.f, 0, 0, 0, dtype))) return rc;
+    if ((rc = check_count("T", T, 0, kMaxTokens)) || (rc = check_count("layers", layers, 1, 65536)) ||
+        (rc = check_count("num_pages", num_pages, 1, kMaxTokens)) ||
+        (rc = check_count("page_size", page_size, 1, kMaxTokens)) ||
+        (rc = check_count("max_pages", max_pages, 1, kMaxTokens)))
+        return rc;
+    if ((rc = check_ptr(count, "count", 4)) || (rc = check_ptr(cu_q, "cu_q", 4)) ||
+        (rc = check_ptr(seq_lens, "seq_lens", 4)) || (rc = check_ptr(block_table, "block_table", 4)) ||
+        (rc = check_ptr(K_caches, "K_caches", 8)) || (rc = check_ptr(V_caches, "V_caches", 8)))
+        return rc;
+    if ((K_exps == nullptr) != (V_exps == nullptr))
+        return bad(K_exps ? "V_exps" : "K_exps", "an 8-bit cache has exponents for both K and V");
+    if (T == 0) return FA_OK;
+    if ((rc = check_ptr(path, "path", 4))) return rc;
+    for (int i = 0; i < layers; ++i)
+        if ((rc = check_ptr(K_caches[i], "K_caches", 16)) || (rc = check_ptr(V_caches[i], "V_caches", 16)) ||
+            (K_exps && ((rc = check_ptr(K_exps[i], "K_exps", 1)) || (rc = check_ptr(V_exps[i], "V_exps", 1)))))
+            return rc;
+    const long long kr = (long long)H_kv * d;
+    const long long dense[6] = {kr * page_size, kr, d, kr * page_size, kr, d};
+    const long long* s = strides ? strides : dense;
+    if ((rc = check_strides(s, 6, dtype, 0, K_exps ? 6 : 0))) return rc;
+    const long long es = K_exps ? 1 : elem_bytes(dtype);
+    PagedKeep a = {};
+    a.path = path, a.count = count, a.cu_q = cu_q, a.seq_lens = seq_lens, a.table = block_table;
+    a.N = N, a.T = T, a.H_kv = H_kv, a.cpr = (int)(d * es / 16);
+    a.pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
+    a.kc_page = s[0] * es, a.kc = {s[1] * es, s[2] * es}, a.vc_page = s[3] * es, a.vc = {s[4] * es, s[5] * es};
+    if ((rc = err_word(&a.err))) return rc;
+    for (int l0 = 0; l0 < layers; l0 += kKeepLayers) {
+        a.layers = layers - l0 < kKeepLayers ? layers - l0 : kKeepLayers;
+        for (int i = 0; i < a.layers; ++i) {
+            a.K[i] = K_caches[l0 + i], a.V[i] = V_caches[l0 + i];
+            a.k_exp[i] = K_exps ? static_cast<uint8_t*>(K_exps[l0 + i]) : nullptr;
+            a.v_exp[i] = V_exps ? static_cast<uint8_t*>(V_exps[l0 + i]) : nullptr;
+        }
+        const cudaError_t e = launch_paged_keep(a, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_bad("paged_keep launch", e);
+    }
+    return FA_OK;
+}
+
+int fa_page_trim(const int* count, const int* cu_q, const int* seq_lens, const int* block_table, int* free_pages,
+                 const int* free_start, int* lens, int* free_next, int N, int num_free, int page_size, int max_pages,
+                 void* stream) {
+    clear_error();
+    int rc;
+    if ((rc = check_count("N", N, 1, kMaxTokens)) || (rc = check_count("num_free", num_free, 0, kMaxTokens)) ||
+        (rc = check_count("page_size", page_size, 1, kMaxTokens)) ||
+        (rc = check_count("max_pages", max_pages, 1, kMaxTokens)))
+        return rc;
+    if ((rc = check_ptr(count, "count", 4)) || (rc = check_ptr(cu_q, "cu_q", 4)) ||
+        (rc = check_ptr(seq_lens, "seq_lens", 4)) || (rc = check_ptr(block_table, "block_table", 4)) ||
+        (rc = check_ptr(free_start, "free_start", 4)) || (rc = check_ptr(lens, "lens", 4)) ||
+        (rc = check_ptr(free_next, "free_next", 4)))
+        return rc;
+    if (num_free > 0 && (rc = check_ptr(free_pages, "free_pages", 4))) return rc;
+    const Span in[] = {{"count", count, 4ll * N}, {"cu_q", cu_q, 4ll * (N + 1)}, {"seq_lens", seq_lens, 4ll * N},
+                       {"block_table", block_table, 4ll * N * max_pages}, {"free_start", free_start, 4}};
+    const Span out[] = {{"free_pages", free_pages, 4ll * num_free}, {"lens", lens, 4ll * N}, {"free_next", free_next, 4}};
+    if ((rc = check_apart(in, out))) return rc;
+    PageTrim a = {};
+    a.count = count, a.cu_q = cu_q, a.seq_lens = seq_lens, a.table = block_table, a.free_start = free_start;
+    a.free_pages = free_pages, a.lens = lens, a.free_next = free_next;
+    a.N = N, a.n_free = num_free, a.page_size = page_size, a.max_pages = max_pages;
+    if ((rc = err_word(&a.err))) return rc;
+    const cudaError_t e = launch_page_trim(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_bad("page_trim launch", e);
     return FA_OK;
 }
 

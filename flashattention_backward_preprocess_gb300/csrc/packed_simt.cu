@@ -1,10 +1,12 @@
 // packed_simt.cu -- attention forward over packed sequences or a paged cache on CUDA cores:
 // fp32 inputs, and 16-bit ones whose strides, page size or head group the tensor-core kernel's
-// TMA boxes cannot address.  The same plan and the same joining of cut items as there; a tile
-// is 64 rows (query tokens x heads of one key/value head, packed) by 64 keys, a thread of the
-// 16 x 16 grid owns a 4 x 4 block of scores.  fp32 throughout; the online softmax per row.  Bound by the FMA
-// pipe's shared-memory operands: 4 x 2048 fp32 tokens, H = 16, d = 64, causal 1.6 ms (21
-// TFLOP/s).
+// TMA boxes cannot address; 8-bit caches (e4m3 numbers and an exponent byte per row, made fp32
+// when a tile is loaded) and trees of new tokens alike.  The same plan and the same joining of
+// cut items as there; a tile is 64 rows (query tokens x heads of one key/value head, packed) by 64
+// keys, a thread of the 16 x 16 grid owns a 4 x 4 block of scores.  fp32 throughout; the online
+// softmax per row.  Bound by the FMA pipe's shared-memory operands: 4 x 2048 fp32 tokens, H = 16,
+// d = 64, causal 1.6 ms (21 TFLOP/s).
+#include <cuda_fp8.h>
 #include <math.h>
 
 #include "packed.cuh"
@@ -17,7 +19,8 @@ constexpr int kThreads = 256;
 constexpr int KT_LD = BN + 4;
 constexpr int kOverhead = 1;  // a tile takes longer than the rest of its item
 
-template <typename T, int D>
+// KV: element type of K and V, T or e4m3 with an exponent byte per row.  kTree: masks of a tree.
+template <typename T, typename KV, int D, bool kTree>
 __global__ void __launch_bounds__(kThreads)
     packed_fwd_simt_kernel(const PackedFwd a, const FwdPlan plan, int hsub) {
     extern __shared__ float smem[];
@@ -32,8 +35,9 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int CPT = D / 16;
     const int g = a.H / a.H_kv;
     const T* Q = static_cast<const T*>(a.Q);
-    const T* K = static_cast<const T*>(a.K);
-    const T* V = static_cast<const T*>(a.V);
+    constexpr bool kQ8 = sizeof(KV) == 1;
+    const KV* K = static_cast<const KV*>(a.K);
+    const KV* V = static_cast<const KV*>(a.V);
     FwdShare share;
     share.read(plan, blockIdx.x);
     FwdWalk w;
@@ -60,6 +64,8 @@ __global__ void __launch_bounds__(kThreads)
         }
         const int nt = w.tiles();
         const int k_lo = a.window > 0 ? w.t.pos0 - a.window + 1 : 0;  // no row sees an earlier key
+        // tokens of the request before its new ones
+        const int ctx = kTree ? w.t.pos0 - (w.t.q_tok - a.cu_q[w.t.n]) : 0;
         for (int jt = 0; jt < nt; ++jt) {
             const int n0 = (w.t.n_first + w.j0 + jt) * BN;
             __syncthreads();
@@ -69,6 +75,7 @@ __global__ void __launch_bounds__(kThreads)
                 float kf = 0.f, vf = 0.f;
                 if (j < w.t.S_k && j >= k_lo) {
                     long long ko, vo;
+                    [[maybe_unused]] long long eo = 0;
                     bool bad = false;
                     if (a.cu_k == nullptr) {
                         const long long pg = page_of(a.table + (size_t)w.t.n * a.max_pages, j, a.page_size,
@@ -76,12 +83,16 @@ __global__ void __launch_bounds__(kThreads)
                         const long long in = j % a.page_size;
                         ko = pg * a.k_page + in * a.k.tok;
                         vo = pg * a.v_page + in * a.v.tok;
+                        if constexpr (kQ8) eo = (pg * a.H_kv + hk) * a.page_size + in;
                     } else {
                         ko = (long long)(w.t.k_base + j) * a.k.tok;
                         vo = (long long)(w.t.k_base + j) * a.v.tok;
                     }
                     if (bad) {
                         if (c == 0) atomicOr(a.err, kErrPage);
+                    } else if constexpr (kQ8) {
+                        kf = static_cast<float>(K[ko + (long long)hk * a.k.head + c]) * exp_value(a.k_exp[eo]);
+                        vf = static_cast<float>(V[vo + (long long)hk * a.v.head + c]) * exp_value(a.v_exp[eo]);
                     } else {
                         kf = TypeTraits<T>::to_f32(K[ko + (long long)hk * a.k.head + c]);
                         vf = TypeTraits<T>::to_f32(V[vo + (long long)hk * a.v.head + c]);
@@ -116,7 +127,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const int j = n0 + tx * 4 + b;
-                    const bool vis = j < w.t.S_k && key_visible(p, j, a.causal, a.window);
+                    bool vis = j < w.t.S_k && key_visible(p, j, a.causal, a.window);
+                    if (kTree && vis && j >= ctx) vis = r < rows && tree_sees(a, w.t.q_tok + r / gh, j - ctx);
                     sc[i][b] = vis ? sc[i][b] * sl2 : -INFINITY;
                     rmax = fmaxf(rmax, sc[i][b]);
                 }
@@ -190,10 +202,10 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+template <typename T, typename KV, int D, bool kTree>
+cudaError_t launch_kv(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     const size_t smem = sizeof(float) * (BM * D + D * KT_LD + BN * D + BM * BN);
-    auto kern = packed_fwd_simt_kernel<T, D>;
+    auto kern = packed_fwd_simt_kernel<T, KV, D, kTree>;
     const int g = a.H / a.H_kv;
     const int hsub = (g + BM - 1) / BM;
     FwdGeom geo;
@@ -216,6 +228,14 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     if (e != cudaSuccess) return e;
     kern<<<geo.ctas, kThreads, smem, st>>>(a, plan, hsub);
     return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+    if (a.q8())
+        return a.tree ? launch_kv<T, __nv_fp8_e4m3, D, true>(a, ws, bytes, st)
+                      : launch_kv<T, __nv_fp8_e4m3, D, false>(a, ws, bytes, st);
+    return a.tree ? launch_kv<T, T, D, true>(a, ws, bytes, st) : launch_kv<T, T, D, false>(a, ws, bytes, st);
 }
 
 }  // namespace

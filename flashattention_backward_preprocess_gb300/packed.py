@@ -2,6 +2,8 @@
 take sequences of different lengths, as torch calls.
 
 Tensors are token major: Q [T, H, d], K and V [T, H_kv, d], caches [pages, page_size, H_kv, d].
+An 8-bit cache is a float8_e4m3fn tensor of that shape with uint8 exponents [pages, H_kv, page_size]
+beside it; a tree of new tokens is an int64 tensor of masks [T, words].
 Any strides that are whole 16-byte pieces are taken as they are (slices of a joint QKV
 projection, transposed caches); the head dimension is contiguous.  Lengths stay on the device:
 no call here waits for the GPU.  Outputs that the caller does not pass are allocated, with the
@@ -22,7 +24,7 @@ import torch
 
 from .binding import _DT, FaError, _check, load_library
 
-_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+_I32, _I64, _F32, _U8, _F8 = torch.int32, torch.int64, torch.float32, torch.uint8, torch.float8_e4m3fn
 _empty, _empty_like, _Tensor = torch.empty, torch.empty_like, torch.Tensor
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
@@ -121,7 +123,7 @@ def _varlen_ws(dev, *a):
 
 @functools.lru_cache(maxsize=4096)
 def _paged_ws(dev, *a):
-    return max(int(load_library().fa_paged_workspace_bytes(*a)), 1)
+    return max(int(load_library().fa_paged_workspace_bytes_ex(*a)), 1)
 
 
 def _shape3(name, t):
@@ -222,6 +224,21 @@ def _caches(K_cache, V_cache, dtype):
     return K_cache.shape
 
 
+def _exps(K_exp, V_exp, shape):
+    """Exponents of 8-bit caches of `shape`."""
+    for name, t in (("K_exp", K_exp), ("V_exp", V_exp)):
+        if t is None:
+            _refuse(name, "an 8-bit cache has exponents for both K and V")
+        _ints(name, t, (shape[0], shape[2], shape[1]), _U8)
+
+
+def _tree(t, T):
+    if t.dim() != 2:
+        _refuse("tree", f"must be 2-D [T, words], got shape {tuple(t.shape)}")
+    _ints("tree", t, (T, t.shape[1]), _I64)
+    return t.shape[1]
+
+
 def _table(t, N):
     if t.dim() != 2:
         _refuse("block_table", f"must be 2-D [N, max_pages], got shape {tuple(t.shape)}")
@@ -230,10 +247,15 @@ def _table(t, N):
 
 
 def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float | None = None, causal: bool = True,
-                 window_size: int = 0, O=None, LSE=None, stream=None):
-    """(O, LSE) of each request's newest tokens over its pages; see include/fa.h (fa_paged_fwd)."""
+                 window_size: int = 0, O=None, LSE=None, stream=None, K_exp=None, V_exp=None, tree=None):
+    """(O, LSE) of each request's newest tokens over its pages; see include/fa.h (fa_paged_fwd, and
+    fa_paged_fwd_ex for 8-bit caches (K_exp, V_exp) and trees of new tokens)."""
     T_q, H, d = _shape3("Q", Q)
-    pages, page, H_kv, dk = _caches(K_cache, V_cache, Q.dtype)
+    q8 = K_exp is not None or V_exp is not None
+    pages, page, H_kv, dk = _caches(K_cache, V_cache, _F8 if q8 else Q.dtype)
+    if q8:
+        _exps(K_exp, V_exp, K_cache.shape)
+    words = 0 if tree is None else _tree(tree, T_q)
     if dk != d:
         _refuse("K_cache", f"shape {tuple(K_cache.shape)} incompatible with Q {tuple(Q.shape)}")
     N = cu_q.numel() - 1
@@ -241,15 +263,16 @@ def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float 
     _ints("seq_lens", seq_lens, (N,))
     cols = _table(block_table, N)
     dt = _type(Q)
-    dev = _device(Q, K_cache, V_cache, block_table, cu_q, seq_lens, O, LSE)
-    need = _paged_ws(dev.index, N, T_q, H, H_kv, d, page, dt)
+    dev = _device(Q, K_cache, V_cache, block_table, cu_q, seq_lens, O, LSE, K_exp, V_exp, tree)
+    need = _paged_ws(dev.index, N, T_q, H, H_kv, d, page, dt, int(q8))
 
     def body(st):
         o, lse, fill = _outputs(Q, T_q, H, O, LSE)
         ws = _empty(need, dtype=_U8, device=dev)
-        _check(load_library().fa_paged_fwd(
-            Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), o.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-            cu_q.data_ptr(), seq_lens.data_ptr(), N, T_q, pages, page, cols, H, H_kv, d,
+        _check(load_library().fa_paged_fwd_ex(
+            Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), K_exp.data_ptr() if q8 else None,
+            V_exp.data_ptr() if q8 else None, o.data_ptr(), lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+            seq_lens.data_ptr(), None if tree is None else tree.data_ptr(), words, N, T_q, pages, page, cols, H, H_kv, d,
             None if Q.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous() and o.is_contiguous() else
             _strides(("Q", Q), ("K_cache", K_cache), ("V_cache", V_cache), ("O", o)),
             _scale(scale, d), int(bool(causal)), _int32("window_size", window_size), fill, dt, ws.data_ptr(),
@@ -310,5 +333,153 @@ def fa_paged_write(K, V, slots, K_cache, V_cache, stream=None):
             None if K.is_contiguous() and V.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous() else
             _strides(("K", K), ("V", V), ("K_cache", K_cache), ("V_cache", V_cache)), dt, st))
         return K_cache, V_cache
+
+    return _call(dev, stream, body)
+
+
+def _q8_strides(K, V, K_cache, V_cache):
+    if K.is_contiguous() and V.is_contiguous() and K_cache.is_contiguous() and V_cache.is_contiguous():
+        return None
+    return _strides(("K", K), ("V", V), ("K_cache", K_cache), ("V_cache", V_cache))
+
+
+def fa_paged_write_q8(K, V, slots, K_cache, V_cache, K_exp, V_exp, stream=None):
+    """Quantises K and V rows into their slots of the 8-bit caches, in place; see include/fa.h (fa_paged_write_q8)."""
+    T, H_kv, d = _shape3("K", K)
+    _same("V", V, K.shape, K.dtype)
+    pages, page, hc, dc = _caches(K_cache, V_cache, _F8)
+    if hc != H_kv or dc != d:
+        _refuse("K_cache", f"shape {tuple(K_cache.shape)} incompatible with K {tuple(K.shape)}")
+    _exps(K_exp, V_exp, K_cache.shape)
+    _ints("slots", slots, (T,), _I64)
+    dt = _type(K)
+    dev = _device(K, V, slots, K_cache, V_cache, K_exp, V_exp)
+
+    def body(st):
+        _check(load_library().fa_paged_write_q8(
+            K.data_ptr(), V.data_ptr(), slots.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), K_exp.data_ptr(),
+            V_exp.data_ptr(), T, pages, page, H_kv, d, _q8_strides(K, V, K_cache, V_cache), dt, st))
+        return K_cache, V_cache, K_exp, V_exp
+
+    return _call(dev, stream, body)
+
+
+def fa_paged_read_q8(K_cache, V_cache, K_exp, V_exp, slots, dtype=torch.bfloat16, K=None, V=None, stream=None):
+    """(K, V) [T, H_kv, d] of `dtype`: rows of the 8-bit caches; see include/fa.h (fa_paged_read_q8)."""
+    dt = _DT.get(dtype)
+    if dt is None:
+        _refuse("dtype", f"unsupported dtype {dtype}")
+    pages, page, H_kv, d = _caches(K_cache, V_cache, _F8)
+    _exps(K_exp, V_exp, K_cache.shape)
+    T = slots.numel()
+    _ints("slots", slots, (T,), _I64)
+    for name, t in (("K", K), ("V", V)):
+        if t is not None:
+            _same(name, t, (T, H_kv, d), dtype)
+    dev = _device(K_cache, V_cache, K_exp, V_exp, slots, K, V)
+
+    def body(st):
+        k, v = (_empty((T, H_kv, d), dtype=dtype, device=dev) if t is None else t for t in (K, V))
+        _check(load_library().fa_paged_read_q8(
+            K_cache.data_ptr(), V_cache.data_ptr(), K_exp.data_ptr(), V_exp.data_ptr(), slots.data_ptr(), k.data_ptr(),
+            v.data_ptr(), T, pages, page, H_kv, d, _q8_strides(k, v, K_cache, V_cache), dt, st))
+        return k, v
+
+    return _call(dev, stream, body)
+
+
+def fa_tree_mask(parents, cu_q, ctx_lens, words: int = 1, tree=None, positions=None, stream=None):
+    """(tree [T, words], positions [T]) of trees of new tokens; see include/fa.h (fa_tree_mask)."""
+    T, N = parents.numel(), cu_q.numel() - 1
+    _ints("parents", parents, (T,))
+    _ints("cu_q", cu_q, (N + 1,))
+    _ints("ctx_lens", ctx_lens, (N,))
+    words = _int32("words", words)
+    if words < 1:
+        _refuse("words", f"must be >= 1, got {words}")
+    if tree is not None:
+        _ints("tree", tree, (T, words), _I64)
+    if positions is not None:
+        _ints("positions", positions, (T,))
+    dev = _device(parents, cu_q, ctx_lens, tree, positions)
+
+    def body(st):
+        out = (_empty((T, words), dtype=_I64, device=dev) if tree is None else tree,
+               _empty(T, dtype=_I32, device=dev) if positions is None else positions)
+        _check(load_library().fa_tree_mask(parents.data_ptr(), cu_q.data_ptr(), ctx_lens.data_ptr(), out[0].data_ptr(),
+                                           out[1].data_ptr(), N, T, words, st))
+        return out
+
+    return _call(dev, stream, body)
+
+
+def fa_paged_keep(path, count, cu_q, seq_lens, block_table, K_caches, V_caches, K_exps=None, V_exps=None, stream=None):
+    """Moves the rows of the accepted tokens up in the caches of all layers (lists of tensors of one
+    shape and stride), in place; see include/fa.h (fa_paged_keep)."""
+    layers, N, T = len(K_caches), cu_q.numel() - 1, path.numel()
+    if layers == 0 or len(V_caches) != layers:
+        _refuse("V_caches", f"expected one per layer, got {layers} and {len(V_caches)}")
+    _ints("path", path, (T,))
+    _ints("cu_q", cu_q, (N + 1,))
+    _ints("count", count, (N,))
+    _ints("seq_lens", seq_lens, (N,))
+    cols = _table(block_table, N)
+    q8 = K_exps is not None or V_exps is not None
+    k0, v0 = K_caches[0], V_caches[0]
+    pages, page, H_kv, d = _caches(k0, v0, _F8 if q8 else k0.dtype)
+    for name, first, ts in (("K_caches", k0, K_caches), ("V_caches", v0, V_caches)):
+        for t in ts:
+            _same(name, t, first.shape, first.dtype)
+            if t.stride() != first.stride():
+                _refuse(name, f"expected strides {first.stride()} in every layer, got {t.stride()}")
+    exps = []
+    if q8:
+        if K_exps is None or V_exps is None or len(K_exps) != layers or len(V_exps) != layers:
+            _refuse("K_exps", "an 8-bit cache has exponents for both K and V of every layer")
+        for a, b in zip(K_exps, V_exps):
+            _exps(a, b, k0.shape)
+        exps = [*K_exps, *V_exps]
+    dt = 0 if q8 else _type(k0)
+    dev = _device(path, count, cu_q, seq_lens, block_table, *K_caches, *V_caches, *exps)
+
+    def pointers(ts):
+        return (ctypes.c_void_p * layers)(*[t.data_ptr() for t in ts])
+
+    def body(st):
+        _check(load_library().fa_paged_keep(
+            path.data_ptr(), count.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+            pointers(K_caches), pointers(V_caches), pointers(K_exps) if q8 else None, pointers(V_exps) if q8 else None,
+            layers, N, T, pages, page, cols, H_kv, d,
+            None if k0.is_contiguous() and v0.is_contiguous() else _strides(("K_caches", k0), ("V_caches", v0)), dt, st))
+        return K_caches, V_caches
+
+    return _call(dev, stream, body)
+
+
+def fa_page_trim(count, cu_q, seq_lens, block_table, free_pages, free_start, page_size: int, lens=None, free_next=None,
+                 stream=None):
+    """(lens, free_next) once `count` of each request's new tokens are kept; the pages behind them are
+    entered into free_pages in place; see include/fa.h (fa_page_trim)."""
+    N = cu_q.numel() - 1
+    _ints("cu_q", cu_q, (N + 1,))
+    _ints("count", count, (N,))
+    _ints("seq_lens", seq_lens, (N,))
+    cols = _table(block_table, N)
+    n_free = free_pages.numel()
+    _ints("free_pages", free_pages, (n_free,))
+    _ints("free_start", free_start, (1,))
+    page_size = _int32("page_size", page_size)
+    if lens is not None:
+        _ints("lens", lens, (N,))
+    if free_next is not None:
+        _ints("free_next", free_next, (1,))
+    dev = _device(count, cu_q, seq_lens, block_table, free_pages, free_start, lens, free_next)
+
+    def body(st):
+        out = (_empty_like(seq_lens) if lens is None else lens, _empty_like(free_start) if free_next is None else free_next)
+        _check(load_library().fa_page_trim(
+            count.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+            free_start.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), N, n_free, page_size, cols, st))
+        return out
 
     return _call(dev, stream, body)

@@ -288,6 +288,29 @@ int fa_paged_fwd(const void* Q, const void* K_cache, const void* V_cache, void* 
 size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype);
 
 /*
+ * fa_paged_fwd_ex -- fa_paged_fwd over an 8-bit cache, and for trees of new tokens.
+ *   K_exp, V_exp : NULL, or the exponent bytes [num_pages, H_kv, page_size] of an 8-bit cache
+ *                  written by fa_paged_write_q8: K_cache and V_cache then hold e4m3 numbers, the
+ *                  strides of their entries count those, and the call attends to the values they
+ *                  stand for.  `dtype` is that of Q and O.
+ *   tree         : NULL, or masks [T_q, tree_words] of 64-bit words (fa_tree_mask makes them): bit k
+ *                  of a row says whether that new token sees the k-th new token of its request (k up
+ *                  to its own place; tokens past 64 * tree_words are seen by none).  All tokens
+ *                  before the new ones are seen.  causal must be 1 and window_size 0.
+ *   tree_words   : 1 to 1024
+ * A row that sees nothing gets O = 0 and LSE = -inf.  Kernels as for fa_paged_fwd; an 8-bit cache
+ * runs the FFMA kernel.
+ */
+int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp,
+                    void* O, float* LSE, const int* block_table, const int* cu_q, const int* seq_lens,
+                    const long long* tree, int tree_words, int N, int T_q, int num_pages, int page_size, int max_pages,
+                    int H, int H_kv, int d, const long long* strides, float scale, int causal, int window_size, int fill,
+                    int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_paged_fwd_ex (quantised: with K_exp and V_exp); 0 for arguments it refuses. */
+size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype, int quantised);
+
+/*
  * fa_page_slots -- pages and slots of a step's new tokens, on the device.
  *   ctx_lens    : [N] int32 tokens each request holds already
  *   cu_q        : [N + 1] int32 new tokens, as in fa_paged_fwd
@@ -325,6 +348,86 @@ int fa_page_slots(const int* ctx_lens, const int* cu_q, const int* free_pages, c
 int fa_paged_write(const void* K, const void* V, const long long* slots, void* K_cache, void* V_cache,
                    int T, int num_pages, int page_size, int H_kv, int d, const long long* strides,
                    int dtype, void* stream);
+
+/*
+ * fa_paged_write_q8 -- K and V rows [T, H_kv, d] of new tokens, quantised, to their slots of an 8-bit
+ * cache (slots as in fa_paged_write).  A row of one token and head becomes d e4m3 numbers and one
+ * exponent byte b, its values being number * 2^(b - 127):
+ *   b - 127 : the smallest whole number e with max |x| <= 448 * 2^e, between -30 and 30 (-15 and 8
+ *             for F16)
+ *   numbers : x * 2^-e rounded to nearest, halves to even; magnitudes above 448 * 2^30 (F16: 61440)
+ *             become that, infinities and NaN become NaN and do not count for the exponent
+ * so an element is off by 2^-4 of itself or 2^-10 * 2^e at most.
+ *   K_cache, V_cache : [num_pages, page_size, H_kv, d] bytes, 16-byte aligned
+ *   K_exp, V_exp     : [num_pages, H_kv, page_size] bytes, dense
+ *   strides          : as in fa_paged_write, the cache's in bytes
+ *   dtype            : of K and V
+ */
+int fa_paged_write_q8(const void* K, const void* V, const long long* slots, void* K_cache, void* V_cache, void* K_exp,
+                      void* V_exp, int T, int num_pages, int page_size, int H_kv, int d, const long long* strides,
+                      int dtype, void* stream);
+
+/*
+ * fa_paged_read_q8 -- the values of T slots of an 8-bit cache, as rows K and V [T, H_kv, d] of `dtype`
+ * (exact for rows that were written from that type or from a narrower one).  The same slot may be
+ * asked for more than once; a negative one gives a row of zeros, so does one past the cache, which
+ * fa_check_device reports (FA_ERR_INVALID_ARG).  strides: as in fa_paged_write_q8.
+ */
+int fa_paged_read_q8(const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp,
+                     const long long* slots, void* K, void* V, int T, int num_pages, int page_size, int H_kv, int d,
+                     const long long* strides, int dtype, void* stream);
+
+/*
+ * fa_tree_mask -- masks and positions of trees of new tokens (fa_paged_fwd_ex, tree).
+ *   parents   : [T] int32; the new token in row cu_q[n] + i follows the new token parents[..] < i of
+ *               its request, or at -1 the tokens that the request holds already
+ *   cu_q      : [N + 1] int32 new tokens, as in fa_paged_fwd
+ *   ctx_lens  : [N] int32 tokens each request holds already
+ *   tree      : [T, words] out, bit k of row cu_q[n] + i: k is i or an ancestor of i (0 for rows of no
+ *               request)
+ *   positions : [T] int32 out, ctx_lens[n] plus the number of ancestors, or -1
+ * A request with more than 64 * words new tokens (their bits are left out), and a parent that is not
+ * an earlier token (taken as -1), are reported by fa_check_device (FA_ERR_INVALID_ARG); with lengths
+ * that do not fit every row is one of no request.  An output that overlaps an input is refused.
+ */
+int fa_tree_mask(const int* parents, const int* cu_q, const int* ctx_lens, long long* tree, int* positions, int N, int T,
+                 int words, void* stream);
+
+/*
+ * fa_paged_keep -- moves the cache rows of accepted new tokens up, in all layers: for request n and
+ * i < count[n] the row of token seq_lens[n] - S + path[cu_q[n] + i] to the place of token seq_lens[n]
+ * - S + i, S = cu_q[n + 1] - cu_q[n] being the request's new tokens.
+ *   path      : [T] int32, rising within the first count[n] entries of each request, below S
+ *   count     : [N] int32, 0 to S
+ *   seq_lens  : [N] int32 tokens in the cache, the new ones included
+ *   K_caches, V_caches : host arrays of `layers` device pointers, caches of one shape and stride
+ *   K_exps, V_exps     : NULL, or the same of the exponents of 8-bit caches
+ *   strides   : {K page, K row, K head, V page, V row, V head} or NULL
+ * A request whose path or count does not fit is left alone, a row on a page outside the cache stays
+ * where it is; fa_check_device reports both (FA_ERR_INVALID_ARG).
+ */
+int fa_paged_keep(const int* path, const int* count, const int* cu_q, const int* seq_lens, const int* block_table,
+                  void* const* K_caches, void* const* V_caches, void* const* K_exps, void* const* V_exps, int layers,
+                  int N, int T, int num_pages, int page_size, int max_pages, int H_kv, int d, const long long* strides,
+                  int dtype, void* stream);
+
+/*
+ * fa_page_trim -- lengths after count[n] of each request's new tokens are kept, and the pages that
+ * only the others used back to the free list.
+ *   lens       : [N] int32 out, seq_lens[n] - S + count[n]
+ *   free_pages : [num_free] int32, the pages given back are entered in front of entry free_start[0],
+ *                in the order of the requests and of their tokens
+ *   free_next  : [1] int32 out, free_start[0] if no page is given back, else that (num_free if that
+ *                is less) minus the pages given back
+ * The table is not changed: its entries behind a request's last page are not read.  count as in
+ * fa_paged_keep; with one, or lengths, that do not fit lens is seq_lens and no page is given back,
+ * and fa_check_device reports it (FA_ERR_INVALID_ARG), as it does more pages than free_start[0] has
+ * room for (none is given back then).  Running the call again gives the same result; an output that
+ * overlaps an input is refused.
+ */
+int fa_page_trim(const int* count, const int* cu_q, const int* seq_lens, const int* block_table, int* free_pages,
+                 const int* free_start, int* lens, int* free_next, int N, int num_free, int page_size, int max_pages,
+                 void* stream);
 
 /* Synchronizes `stream`, then returns FA_ERR_TIMEOUT if a kernel of this
  * library on that stream, or an fa_bwd_noalloc call on this device, recorded
