@@ -510,6 +510,8 @@ inline cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) 
 // packed_fwd.cu, packed_tree.cu (a.tree set): tensor cores (f16 / bf16)
 cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 cudaError_t launch_packed_tree(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
+// packed_q8.cu: tensor cores, 8-bit cache (f16 / bf16 queries, any page size)
+cudaError_t launch_packed_q8(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 // packed_simt.cu: CUDA cores (f32, and layouts that TMA cannot address)
 cudaError_t launch_packed_fwd_simt(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 

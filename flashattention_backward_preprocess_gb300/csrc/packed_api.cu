@@ -126,8 +126,8 @@ int check_apart(const Span (&in)[kIn], const Span (&out)[kOut]) {
 
 // Whether the tensor-core kernel's TMA boxes can address the call.
 bool use_tensor_cores(const PackedFwd& a) {
-    if (a.dtype == FA_F32 || a.q8() || a.H / a.H_kv > 128) return false;
-    if (!a.paged()) return true;
+    if (a.dtype == FA_F32 || a.H / a.H_kv > 128) return false;
+    if (!a.paged() || a.q8()) return true;
     const int bn = a.d == 256 ? 64 : 128;  // keys per tile
     // pages of whole 8-row swizzle atoms that divide a tile, or are made of whole tiles
     return a.page_size % 8 == 0 && (bn % a.page_size == 0 || a.page_size % bn == 0);

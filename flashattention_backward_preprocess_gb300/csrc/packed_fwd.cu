@@ -18,6 +18,7 @@ cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+    if (a.q8()) return launch_packed_q8(a, ws, bytes, st);
     if (a.tree) return launch_packed_tree(a, ws, bytes, st);
     return a.dtype == FA_F16 ? launch_d<__half>(a, ws, bytes, st) : launch_d<__nv_bfloat16>(a, ws, bytes, st);
 }

@@ -43,6 +43,7 @@
 
 #include "bounded_wait.cuh"
 #include "packed.cuh"
+#include "packed_q8.cuh"
 #include "tma_map.cuh"
 
 namespace fa {
@@ -51,20 +52,27 @@ namespace {
 constexpr int BM = 128;  // rows per tile
 // warps 0-7 softmax, 8-11 epilogue, 12 loads of Q and K, 13 S products and TMEM, 14 P V products,
 // 15 loads of V
-constexpr int kThreads = 512;
-constexpr int kWarpEpi = 8, kWarpLoadK = 12, kWarpMma = 13, kWarpPv = 14, kWarpLoadV = 15;
-// registers per thread of the two softmax warpgroups, the epilogue and the last one: together
-// 4 x 128, what the block is launched with
-constexpr int kRegsSoft = 152, kRegsEpi = 120, kRegsOther = 88;
+// 8-bit caches: 12 loads Q, 15 does nothing, 16-19 load and convert K and V
+constexpr int kWarpEpi = 8, kWarpLoadK = 12, kWarpMma = 13, kWarpPv = 14, kWarpLoadV = 15, kWarpConv = 16;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMaxSum = 16384.f;    // of a tile's half row before the running max is looked at again
 constexpr uint32_t kEpiBarrier = 1;   // the epilogue's four warps
 constexpr uint32_t kPairBarrier = 2;  // + lane quadrant: the two softmax warps of a row
 
-template <int D>
+template <int D, bool kQ8>
 struct PCfg {
+    static constexpr int THREADS = kQ8 ? 640 : 512;
+    // registers per thread of the two softmax warpgroups, the epilogue, the last one and the
+    // converting one: together what the block is launched with, 4 x 128 or (65536 / 640, a whole
+    // multiple of 8) 5 x 96
+    static constexpr int REGS_SOFT = kQ8 ? 144 : 152, REGS_EPI = kQ8 ? 72 : 120, REGS_OTHER = kQ8 ? 48 : 88, REGS_CONV = 72;
+    static_assert(2 * REGS_SOFT + REGS_EPI + REGS_OTHER + (kQ8 ? REGS_CONV : 0) == (kQ8 ? 5 * 96 : 4 * 128), "see above");
     static constexpr int BN = D <= 128 ? 128 : 64;
-    static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 2);
+    // slots of the K and of the V ring, and of the ring of 8-bit tiles (K and V in turn)
+    static constexpr int KST = kQ8 ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
+    static constexpr int VST = kQ8 ? 2 : KST;
+    static constexpr int S8 = kQ8 ? (D <= 128 ? 5 : 3) : 0;
+    static constexpr int AHEAD = (S8 + 1) / 2;  // tiles whose rows are looked up before they are converted
     static constexpr int NBUF = D <= 128 ? 3 : 2;
     static constexpr int BOXES = D / 64;
     static constexpr uint32_t kTileQ_B = BM * D * 2;
@@ -73,14 +81,26 @@ struct PCfg {
     static constexpr uint32_t kBoxKV_B = BN * 128;
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = OFF_Q + kTileQ_B;
-    static constexpr uint32_t OFF_V = OFF_K + STAGES * kTileKV_B;
+    static constexpr uint32_t OFF_V = OFF_K + KST * kTileKV_B;
+    static constexpr uint32_t kTile8_B = BN * D;
+    static constexpr uint32_t OFF_8 = OFF_V + VST * kTileKV_B;
     // float2 per row: two slots of the rows' max and sum; then a float per row that a row's two
     // softmax threads exchange
-    static constexpr uint32_t OFF_ROW = OFF_V + STAGES * kTileKV_B;
+    static constexpr uint32_t OFF_ROW = OFF_8 + S8 * kTile8_B;
     static constexpr uint32_t OFF_XCH = OFF_ROW + 2 * BM * 8;
-    static constexpr uint32_t OFF_BAR = OFF_XCH + BM * 4;
-    // V(j)'s slot is past V(j - STAGES) once S(j) is complete (the softmax warps' rare waits for V)
-    static_assert(STAGES >= NBUF, "see above");
+    // 8-bit caches.  Of a tile's rows: where they lie in K and V (4 slots), their exponents (2 slots);
+    // of a tile: its largest exponents by warp (2 slots) and in all (8 slots); of an item's rows: the
+    // inverse of the power of two that Q was scaled by (4 slots)
+    static constexpr uint32_t OFF_AT = OFF_XCH + BM * 4;
+    static constexpr uint32_t OFF_EXP = OFF_AT + (kQ8 ? 4 * BN * 16 : 0);
+    static constexpr uint32_t OFF_PART = OFF_EXP + (kQ8 ? 2 * BN * 2 : 0);
+    static constexpr uint32_t OFF_TOP = OFF_PART + (kQ8 ? 2 * 4 * 4 : 0);
+    static constexpr uint32_t OFF_QS = OFF_TOP + (kQ8 ? 8 * 4 : 0);
+    static constexpr uint32_t OFF_BAR = OFF_QS + (kQ8 ? 4 * BM * 4 : 0);
+    // V(j)'s slot is past V(j - VST) once S(j) is complete (the softmax warps' rare waits for V)
+    static_assert(kQ8 || VST >= NBUF, "see above");
+    // what the softmax reads of a tile's or item's slot is read before the slot is written again
+    static_assert(KST + NBUF < 8, "see above");
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
@@ -96,8 +116,15 @@ enum {
     P_OFREE,               // O of an item read (4 epilogue warps)
     P_ML0,                 // max and sum of an item's rows written (4 softmax warps), 2 slots
     P_MR0 = P_ML0 + 2,     // and read by the epilogue (4 warps), 2 slots
-    P_SLOT0 = P_MR0 + 2    // STAGES "full" and STAGES "empty" of the K ring, then of the V ring
+    P_SLOT0 = P_MR0 + 2    // KST "full" and KST "empty" of the K ring, VST of each of the V ring, and
+                           // for 8-bit caches: Q made fp16 (4 converting warps)
 };
+
+// Whether the converting warps arrive at barrier P_SLOT0 + i: K, V or Q is there.
+template <typename C>
+__device__ __forceinline__ bool conv_arrives(int i) {
+    return (i >= 0 && i < C::KST) || (i >= 2 * C::KST && i < 2 * C::KST + C::VST) || i == 2 * (C::KST + C::VST);
+}
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
@@ -167,20 +194,23 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 // after another.  Small boxes are what bounds a cache of small pages (about 60 ns a box,
 // whatever it holds): a step of 64 tokens over 4096 each in pages of 16 rows took 253 us with
 // a box per 64 columns and 175 us with one per page.
-// kTree (paged): new tokens see each other by the call's masks.
-template <typename T, int D, bool kPaged, bool kGroup, bool kTree>
-__global__ void __launch_bounds__(kThreads, 1)
+// kTree (paged): new tokens see each other by the call's masks.  kQ8 (paged): an 8-bit cache
+// (packed_q8.cuh), whose tiles the converting warps load.
+template <typename T, int D, bool kPaged, bool kGroup, bool kTree, bool kQ8>
+__global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PackedFwd a, const FwdPlan plan, const FwdGeom geo, int max_units) {
-    using C = PCfg<D>;
-    constexpr int BN = C::BN, NB = C::NBUF;
+    using C = PCfg<D, kQ8>;
+    constexpr int BN = C::BN, NB = C::NBUF, kThreads = C::THREADS;
     // K / V tile layout: bytes from a 64-column block to the next, and from 8 rows to the next 8
     constexpr uint32_t kBlk = kGroup ? 1024 : C::kBoxKV_B;
     constexpr uint32_t kRow8 = kGroup ? 1024 * C::BOXES : 1024;
     constexpr int kPerPage = kGroup ? 1 : C::BOXES;          // boxes per page of K or V
     constexpr int kPieces = (BN / 8 * kPerPage + 31) / 32;  // and tile per producer lane (pages of 8 rows)
     constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
-    constexpr int kNumBars = P_SLOT0 + 4 * C::STAGES;
+    constexpr bool kOpBF16 = kBF16 && !kQ8;  // operands of the products
+    constexpr bool kConvQ = kBF16 && kQ8;    // Q is made fp16
+    constexpr int kNumBars = P_SLOT0 + 2 * C::KST + 2 * C::VST + (kQ8 ? 1 : 0);
     constexpr uint32_t OFF_MISC = C::OFF_BAR + kNumBars * 8;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
@@ -191,9 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
     // a ring each for K and V: a K slot is free once S is computed, well before V's
     auto k_full = [&](int s) { return bar(P_SLOT0 + s); };
-    auto k_empty = [&](int s) { return bar(P_SLOT0 + C::STAGES + s); };
-    auto v_full = [&](int s) { return bar(P_SLOT0 + 2 * C::STAGES + s); };
-    auto v_empty = [&](int s) { return bar(P_SLOT0 + 3 * C::STAGES + s); };
+    auto k_empty = [&](int s) { return bar(P_SLOT0 + C::KST + s); };
+    auto v_full = [&](int s) { return bar(P_SLOT0 + 2 * C::KST + s); };
+    auto v_empty = [&](int s) { return bar(P_SLOT0 + 2 * C::KST + C::VST + s); };
+    [[maybe_unused]] const uint32_t q_conv = bar(P_SLOT0 + 2 * C::KST + 2 * C::VST);
     const int g = a.H / a.H_kv;
     unsigned int* err = a.err;
 
@@ -201,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((sbase & 1023u) != 0) atomicOr(err, kErrSmemAlign);
         *abort_flag = (sbase & 1023u) != 0;
         for (int i = 0; i < kNumBars; ++i)
-            ptx::mbar_init(bar(i), i >= P_P0 && i < P_P0 + 3 ? 8u : i >= P_OFREE && i < P_SLOT0 ? 4u : 1u);
+            ptx::mbar_init(bar(i), i >= P_P0 && i < P_P0 + 3 ? 8u
+                                   : (i >= P_OFREE && i < P_SLOT0) || (kQ8 && conv_arrives<C>(i - P_SLOT0)) ? 4u
+                                                                                                           : 1u);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -229,8 +262,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
     // CTA (jg), per-item ones its segments with work (ka).
-    if (warp >= kWarpLoadK) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (kQ8 && warp >= kWarpConv) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
+        if constexpr (kQ8) {
+            if (!(sbase & 1023u))
+                convert_tiles<C, T, D, kConvQ>(a, share, geo, smem, abort_flag, k_full(0), k_empty(0), v_full(0), v_empty(0),
+                                            bar(P_Q), q_conv);
+        }
+    } else if (warp >= kWarpLoadK) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+    if (kQ8 && (warp == kWarpLoadK || warp == kWarpLoadV)) {
+        // ------------------------------------------------------------ Q tiles (8-bit caches)
+        if (warp == kWarpLoadK && !*abort_flag) {
+            int ka = 0;
+            FwdWalk w;
+            for (bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead); more; more = w.next()) {
+                if (w.tiles() == 0) continue;
+                if (lane < C::BOXES) tma_prefetch_3d(&tmQ, lane * 64, w.hd * g, w.t.q_tok);
+                if (ka > 0 && !wait_bar_warp(bar(P_QE), (ka - 1) & 1, abort_flag, err)) break;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(geo.tpt * g) * 128u * C::BOXES);
+                __syncwarp();
+                if (lane < C::BOXES)
+                    ptx::tma_load_3d(sbase + C::OFF_Q + lane * C::kBoxQ_B, &tmQ, lane * 64, w.hd * g, w.t.q_tok, bar(P_Q));
+                ++ka;
+            }
+            __syncwarp();
+            if (lane == 0 && ka > 0) drain_wait(bar(P_Q), (ka - 1) & 1);
+        }
+        __syncwarp();
+    } else
     if (warp == kWarpLoadK || warp == kWarpLoadV) {
         // ------------------------------------------------------------ producers
         // One warp loads the Q tile of each item (once the previous item's S products are done)
@@ -275,10 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tma_load_3d(sbase + C::OFF_Q + lane * C::kBoxQ_B, &tmQ, lane * 64, w.hd * g, w.t.q_tok, bar(P_Q));
                 ++q_act;
             }
-            const int s = jg % C::STAGES;
+            const int s = jg % C::KST;
             const uint32_t full = is_v ? v_full(s) : k_full(s);
-            if (jg >= C::STAGES &&
-                !(ok = wait_bar_warp(is_v ? v_empty(s) : k_empty(s), (jg / C::STAGES - 1) & 1, abort_flag, err)))
+            if (jg >= C::KST &&
+                !(ok = wait_bar_warp(is_v ? v_empty(s) : k_empty(s), (jg / C::KST - 1) & 1, abort_flag, err)))
                 break;
             const int tile = w.t.n_first + j;
             const uint32_t dst = ring + s * C::kTileKV_B;
@@ -323,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // never leave copies in flight into shared memory that is about to be released
         if (lane == 0) {
             if (q_act > 0) drain_wait(bar(P_Q), (q_act - 1) & 1);
-            for (int k = jg - C::STAGES < 0 ? 0 : jg - C::STAGES; k < jg; ++k)
-                drain_wait(is_v ? v_full(k % C::STAGES) : k_full(k % C::STAGES), (k / C::STAGES) & 1);
+            for (int k = jg - C::KST < 0 ? 0 : jg - C::KST; k < jg; ++k)
+                drain_wait(is_v ? v_full(k % C::KST) : k_full(k % C::KST), (k / C::KST) & 1);
         }
         __syncwarp();
     } else if (warp == kWarpMma || warp == kWarpPv) {
@@ -333,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // of tile jg goes into buffer jg % NB once the P V product of tile jg - NB has read P
         // out of it; the P V product runs once the softmax has packed P.
         if (lane == 0 && !*abort_flag) {
-            constexpr uint32_t ID_S = ptx::idesc_f16(BM, BN, kBF16, false, false);
-            constexpr uint32_t ID_PV = ptx::idesc_f16(BM, D, kBF16, false, true);
+            constexpr uint32_t ID_S = ptx::idesc_f16(BM, BN, kOpBF16, false, false);
+            constexpr uint32_t ID_PV = ptx::idesc_f16(BM, D, kOpBF16, false, true);
             auto desc_add = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
             bool ok = true;
             int jg = 0, ka = 0;
@@ -346,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (; ok && more; more = w.next()) {
                     const int nt = w.tiles();
                     if (nt == 0) continue;
-                    if (!(ok = wait_bar(bar(P_Q), ka & 1, abort_flag, err))) break;
+                    if (!(ok = wait_bar(kConvQ ? q_conv : bar(P_Q), ka & 1, abort_flag, err))) break;
                     for (int j = 0; j < nt; ++j, ++jg) {
-                        const int s = jg % C::STAGES;
-                        if (!(ok = wait_bar(k_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
+                        const int s = jg % C::KST;
+                        if (!(ok = wait_bar(k_full(s), (jg / C::KST) & 1, abort_flag, err))) break;
                         if (jg >= NB && !(ok = wait_bar(bar(P_PV0 + jg % NB), (jg / NB - 1) & 1, abort_flag, err)))
                             break;
                         ptx::tc_fence_after();
@@ -376,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nt = w.tiles();
                     if (nt == 0) continue;
                     for (int j = 0; j < nt; ++j, ++jg) {
-                        const int s = jg % C::STAGES;
-                        if (!(ok = wait_bar(v_full(s), (jg / C::STAGES) & 1, abort_flag, err))) break;
+                        const int s = jg % C::VST;
+                        if (!(ok = wait_bar(v_full(s), (jg / C::VST) & 1, abort_flag, err))) break;
                         if (!(ok = wait_bar(bar(P_P0 + jg % NB), (jg / NB) & 1, abort_flag, err))) break;
                         // the first product of an item overwrites O: the epilogue of the
                         // previous item must have read it
@@ -414,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // threads agree that it did not with one barrier.  S stays in TMEM until P replaces it.
         // A timeout never leaves the loop, so that the partner is not left at a barrier: all
         // waits return at once then.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
         constexpr int HN = BN / 2;  // columns of a thread
         const int hf = warp >> 2, qd = warp & 3;
         const int t = qd * 32 + lane;  // TMEM lane == row of the tile
@@ -439,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ctx = w.t.pos0 - (w.t.q_tok - a.cu_q[w.t.n]);
                 sees = a.tree + (size_t)(w.t.q_tok + (row_valid ? ti : 0)) * a.tree_words;
             }
+            [[maybe_unused]] float scale_row = scale_log2;
             float m_run = -INFINITY;  // reference of the row's exponentials, in units of s * log2(e)
             float l_run = 0.f;        // sum of exp2(x - m_run) over this thread's columns
             for (int j = 0; j < nt; ++j, ++jg) {
@@ -457,10 +518,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kTree)
                     if (treed) see = tree_columns<HN>(sees, a.tree_words, n0 + hf * HN - ctx);
                 wait_bar_warp(bar(P_S0 + jg % NB), (jg / NB) & 1, abort_flag, err);
-                if (k_live < BN) {
+                [[maybe_unused]] float scale_tile = 0.f, v_exp = 0.f, v_unit = 1.f;
+                if constexpr (kQ8) {
+                    // what Q's row was multiplied by is taken out of the scores again
+                    if (kConvQ && j == 0)
+                        scale_row = scale_log2 * reinterpret_cast<volatile const float*>(smem + C::OFF_QS)[(ka & 3) * BM + t];
+                    // K = K' 2^ek, V = V' 2^ev of the tile's operands K', V': the scores take 2^ek, and the
+                    // exponentials, which stand for P 2^ev, ev
+                    const uint32_t top = *reinterpret_cast<volatile const uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4);
+                    scale_tile = scale_row * __uint_as_float((top & 0xffu) << 23);
+                    v_exp = (float)((int)(top >> 8) - 127);
+                    v_unit = __uint_as_float((254u - (top >> 8)) << 23);  // 2^-ev
+                }
+                if (!kQ8 && k_live < BN) {
                     // V rows behind the last key: zeros, once the loads have landed
-                    const int s = jg % C::STAGES;
-                    wait_bar_warp(v_full(s), (jg / C::STAGES) & 1, abort_flag, err);
+                    const int s = jg % C::VST;
+                    wait_bar_warp(v_full(s), (jg / C::VST) & 1, abort_flag, err);
                     if (hf == 0 && t < BN && t >= k_live) {
 #pragma unroll
                         for (int x = 0; x < C::BOXES; ++x)
@@ -496,8 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     auto exps = [&](const uint32_t* r) {
                         const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                        const float2 sc2 = make_float2(scale_log2, scale_log2);
-                        const float2 nm2 = make_float2(-m_use, -m_use);
+                        const float sc = kQ8 ? scale_tile : scale_log2, nm = kQ8 ? v_exp - m_use : -m_use;
+                        const float2 sc2 = make_float2(sc, sc);
+                        const float2 nm2 = make_float2(nm, nm);
                         float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                           make_float2(0.f, 0.f)};
 #pragma unroll
@@ -506,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nm2);
                             const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
                             sum2[(c >> 1) & 3] = __fadd2_rn(sum2[(c >> 1) & 3], pp);
-                            Pp[c / 2] = pack2<kBF16>(pp.x, pp.y);
+                            Pp[c / 2] = pack2<kOpBF16>(pp.x, pp.y);
                         }
                         const float2 s2 = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
                         sum = s2.x + s2.y;
@@ -539,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         ptx::named_bar_sync(pair, 64);
                         if (hf == 1) mx = *xch;
-                        mx = mx == -INFINITY ? -INFINITY : mx * scale_log2;
+                        mx = mx == -INFINITY ? -INFINITY : kQ8 ? fmaf(mx, scale_tile, v_exp) : mx * scale_log2;
                         rescale = mx > m_run;
                         if (rescale) {
                             alpha = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - mx);
@@ -547,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         exps(r);
                     }
-                    l_run = l_run * alpha + sum;
+                    l_run = l_run * alpha + (kQ8 ? sum * v_unit : sum);
 #pragma unroll
                     for (int c = 0; c < HN / 2; c += 16) ptx::tmem_st16(buf + c, *reinterpret_cast<uint32_t(*)[16]>(Pp + c));
                     // rescale the O row before the next P V product accumulates into it (each
@@ -593,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O = acc / l and LSE = (m + log2 l) ln 2 of a whole item; of a cut one the raw
         // accumulator with (m, l), and the last part to arrive joins them.  Meanwhile the
         // softmax warps are at the next item; its first P V product waits for O to be read.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
         const int t = threadIdx.x - kWarpEpi * 32;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const int ti = t / g, th = t - ti * g;  // token and head of the row
@@ -721,10 +795,10 @@ bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, 
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool kPaged, bool kGroup, bool kTree>
+template <typename T, int D, bool kPaged, bool kGroup, bool kTree, bool kQ8 = false>
 cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
-    using C = PCfg<D>;
-    constexpr uint32_t kSmem = C::OFF_BAR + (P_SLOT0 + 4 * C::STAGES) * 8 + 16;
+    using C = PCfg<D, kQ8>;
+    constexpr uint32_t kSmem = C::OFF_BAR + (P_SLOT0 + 2 * C::KST + 2 * C::VST + (kQ8 ? 1 : 0)) * 8 + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
     const int g = a.H / a.H_kv;
     FwdGeom geo;
@@ -746,7 +820,7 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     plan.tag = next_tag();
     const CUtensorMapDataType dt =
         TypeTraits<T>::kId == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk = {}, tv = {};
     bool ok;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.T_q};
@@ -760,7 +834,7 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
         RowStride s;
         long long page;
     } kv[2] = {{&tk, a.K, a.k, a.k_page}, {&tv, a.V, a.v, a.v_page}};
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 && !kQ8; ++i) {
         if constexpr (kGroup) {
             // columns of a head (its offset is part of the column coordinate), 8 rows, 64-column
             // blocks, groups of 8 rows, pages
@@ -787,13 +861,13 @@ cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t e;
     if (!geo.self && (e = launch_fwd_plan(a, geo, plan, st)) != cudaSuccess) return e;
-    auto kern = packed_fwd_kernel<T, D, kPaged, kGroup, kTree>;
+    auto kern = packed_fwd_kernel<T, D, kPaged, kGroup, kTree, kQ8>;
     static std::atomic<uint64_t> ready{0};
     if ((e = allow_smem(kern, (int)kSmem, ready)) != cudaSuccess) return e;
     // programmatic dependent launch: barriers and TMEM are set up while the kernel before runs
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)geo.ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
