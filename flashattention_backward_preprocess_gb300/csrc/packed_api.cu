@@ -330,6 +330,7 @@ int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, con
     if ((rc = check_ptr(Q, "Q", 16)) || (rc = check_ptr(K_cache, "K_cache", 16)) ||
         (rc = check_ptr(V_cache, "V_cache", 16)) || (rc = check_ptr(O, "O", 16)) || (rc = check_ptr(LSE, "LSE", 4)))
         return rc;
+    if (K_exp && ((rc = check_ptr(K_exp, "K_exp", 16)) || (rc = check_ptr(V_exp, "V_exp", 16)))) return rc;
     const long long kr = (long long)H_kv * d, qr = (long long)H * d;
     const long long dense[10] = {qr, d, kr * page_size, kr, d, kr * page_size, kr, d, qr, d};
     const long long* s = strides ? strides : dense;
@@ -426,7 +427,7 @@ static int q8_args(PagedQ8& a, const void* K, const void* V, const void* K_cache
     if (T == 0) return FA_OK;
     if ((rc = check_ptr(K, "K", 16)) || (rc = check_ptr(V, "V", 16)) || (rc = check_ptr(slots, "slots", 8)) ||
         (rc = check_ptr(K_cache, "K_cache", 16)) || (rc = check_ptr(V_cache, "V_cache", 16)) ||
-        (rc = check_ptr(K_exp, "K_exp", 1)) || (rc = check_ptr(V_exp, "V_exp", 1)))
+        (rc = check_ptr(K_exp, "K_exp", 16)) || (rc = check_ptr(V_exp, "V_exp", 16)))
         return rc;
     const long long kr = (long long)H_kv * d;
     const long long dense[10] = {kr, d, kr, d, kr * page_size, kr, d, kr * page_size, kr, d};
@@ -513,7 +514,7 @@ int fa_paged_keep(const int* path, const int* count, const int* cu_q, const int*
     if ((rc = check_ptr(path, "path", 4))) return rc;
     for (int i = 0; i < layers; ++i)
         if ((rc = check_ptr(K_caches[i], "K_caches", 16)) || (rc = check_ptr(V_caches[i], "V_caches", 16)) ||
-            (K_exps && ((rc = check_ptr(K_exps[i], "K_exps", 1)) || (rc = check_ptr(V_exps[i], "V_exps", 1)))))
+            (K_exps && ((rc = check_ptr(K_exps[i], "K_exps", 16)) || (rc = check_ptr(V_exps[i], "V_exps", 16)))))
             return rc;
     const long long kr = (long long)H_kv * d;
     const long long dense[6] = {kr * page_size, kr, d, kr * page_size, kr, d};

@@ -5,6 +5,13 @@
 namespace fa {
 namespace {
 
+// Steps over an 8-bit cache whose requests have 16 rows (tokens x heads of a group) or fewer on
+// average, on pages of whole 16-key pieces: packed_q8_rows.cu.
+bool few_rows(const PackedFwd& a) {
+    const long long g = a.H / a.H_kv;
+    return a.d <= 128 && g <= 16 && a.page_size % 16 == 0 && a.T_q * g <= 16ll * a.N;
+}
+
 template <typename T>
 cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     if (a.paged()) return launch_paged<T, false>(a, ws, bytes, st);
@@ -18,7 +25,7 @@ cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
-    if (a.q8()) return launch_packed_q8(a, ws, bytes, st);
+    if (a.q8()) return few_rows(a) ? launch_q8_rows(a, ws, bytes, st) : launch_packed_q8(a, ws, bytes, st);
     if (a.tree) return launch_packed_tree(a, ws, bytes, st);
     return a.dtype == FA_F16 ? launch_d<__half>(a, ws, bytes, st) : launch_d<__nv_bfloat16>(a, ws, bytes, st);
 }

@@ -52,27 +52,31 @@ namespace {
 constexpr int BM = 128;  // rows per tile
 // warps 0-7 softmax, 8-11 epilogue, 12 loads of Q and K, 13 S products and TMEM, 14 P V products,
 // 15 loads of V
-// 8-bit caches: 12 loads Q, 15 does nothing, 16-19 load and convert K and V
+// 8-bit caches: 12 and 15 look rows of K and V up, 16-23 load and convert them, 13 loads Q as well
 constexpr int kWarpEpi = 8, kWarpLoadK = 12, kWarpMma = 13, kWarpPv = 14, kWarpLoadV = 15, kWarpConv = 16;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMaxSum = 16384.f;    // of a tile's half row before the running max is looked at again
+// 8-bit caches: P is fp16 whatever Q's type, so it is kept 2^8 above the reference: its fixed step
+// below 2^-14 is 2^-33 of the largest P then (for bf16 queries 2^-25 would show)
+constexpr float kQ8Lift = 8.f, kQ8MaxSum = 57344.f;
 constexpr uint32_t kEpiBarrier = 1;   // the epilogue's four warps
 constexpr uint32_t kPairBarrier = 2;  // + lane quadrant: the two softmax warps of a row
 
 template <int D, bool kQ8>
 struct PCfg {
-    static constexpr int THREADS = kQ8 ? 640 : 512;
-    // registers per thread of the two softmax warpgroups, the epilogue, the last one and the
-    // converting one: together what the block is launched with, 4 x 128 or (65536 / 640, a whole
-    // multiple of 8) 5 x 96
-    static constexpr int REGS_SOFT = kQ8 ? 144 : 152, REGS_EPI = kQ8 ? 72 : 120, REGS_OTHER = kQ8 ? 48 : 88, REGS_CONV = 72;
-    static_assert(2 * REGS_SOFT + REGS_EPI + REGS_OTHER + (kQ8 ? REGS_CONV : 0) == (kQ8 ? 5 * 96 : 4 * 128), "see above");
+    static constexpr int THREADS = kQ8 ? 768 : 512;
+    // registers per thread of the two softmax warpgroups, the epilogue, the last one and the two
+    // converting ones: together what the block is launched with, 4 x 128 or (65536 / 768, a whole
+    // multiple of 8) 6 x 80
+    static constexpr int REGS_SOFT = kQ8 ? 104 : 152, REGS_EPI = kQ8 ? 88 : 120, REGS_OTHER = kQ8 ? 56 : 88, REGS_CONV = 64;
+    static constexpr int REGS = kQ8 ? 80 : 128;
+    static_assert(2 * REGS_SOFT + REGS_EPI + REGS_OTHER + (kQ8 ? 2 * REGS_CONV : 0) == THREADS / 128 * REGS, "see above");
+    static_assert(REGS_SOFT >= REGS && REGS_OTHER <= REGS && REGS_CONV <= REGS, "raised or lowered as the roles do");
     static constexpr int BN = D <= 128 ? 128 : 64;
-    // slots of the K and of the V ring, and of the ring of 8-bit tiles (K and V in turn)
-    static constexpr int KST = kQ8 ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
-    static constexpr int VST = kQ8 ? 2 : KST;
-    static constexpr int S8 = kQ8 ? (D <= 128 ? 5 : 3) : 0;
-    static constexpr int AHEAD = (S8 + 1) / 2;  // tiles whose rows are looked up before they are converted
+    // slots of the K and of the V ring
+    static constexpr int KST = kQ8 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
+    static constexpr int VST = KST;
+    static constexpr int INFO = kQ8 ? 4 : 0;  // slots of the ring of looked-up tiles
     static constexpr int NBUF = D <= 128 ? 3 : 2;
     static constexpr int BOXES = D / 64;
     static constexpr uint32_t kTileQ_B = BM * D * 2;
@@ -82,25 +86,24 @@ struct PCfg {
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = OFF_Q + kTileQ_B;
     static constexpr uint32_t OFF_V = OFF_K + KST * kTileKV_B;
-    static constexpr uint32_t kTile8_B = BN * D;
-    static constexpr uint32_t OFF_8 = OFF_V + VST * kTileKV_B;
     // float2 per row: two slots of the rows' max and sum; then a float per row that a row's two
     // softmax threads exchange
-    static constexpr uint32_t OFF_ROW = OFF_8 + S8 * kTile8_B;
+    static constexpr uint32_t OFF_ROW = OFF_V + VST * kTileKV_B;
     static constexpr uint32_t OFF_XCH = OFF_ROW + 2 * BM * 8;
-    // 8-bit caches.  Of a tile's rows: where they lie in K and V (4 slots), their exponents (2 slots);
-    // of a tile: its largest exponents by warp (2 slots) and in all (8 slots); of an item's rows: the
-    // inverse of the power of two that Q was scaled by (4 slots)
+    // 8-bit caches.  Of a looked-up tile: where its rows lie in K and in V, their exponents, words of
+    // both halves; its largest exponents for the softmax (8 slots); of an item's rows: the inverse of
+    // the power of two that Q was scaled by (4 slots)
     static constexpr uint32_t OFF_AT = OFF_XCH + BM * 4;
-    static constexpr uint32_t OFF_EXP = OFF_AT + (kQ8 ? 4 * BN * 16 : 0);
-    static constexpr uint32_t OFF_PART = OFF_EXP + (kQ8 ? 2 * BN * 2 : 0);
-    static constexpr uint32_t OFF_TOP = OFF_PART + (kQ8 ? 2 * 4 * 4 : 0);
-    static constexpr uint32_t OFF_QS = OFF_TOP + (kQ8 ? 8 * 4 : 0);
+    static constexpr uint32_t OFF_EXP = OFF_AT + INFO * BN * 16;
+    static constexpr uint32_t OFF_INFO = OFF_EXP + INFO * BN * 2;
+    static constexpr uint32_t OFF_TOP = OFF_INFO + INFO * 16;
+    static constexpr uint32_t OFF_QS = OFF_TOP + (kQ8 ? 32 : 0);
     static constexpr uint32_t OFF_BAR = OFF_QS + (kQ8 ? 4 * BM * 4 : 0);
     // V(j)'s slot is past V(j - VST) once S(j) is complete (the softmax warps' rare waits for V)
     static_assert(kQ8 || VST >= NBUF, "see above");
     // what the softmax reads of a tile's or item's slot is read before the slot is written again
-    static_assert(KST + NBUF < 8, "see above");
+    static_assert(!kQ8 || KST + NBUF < 8, "see above");
+    static_assert(OFF_AT % 16 == 0 && OFF_INFO % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
@@ -117,13 +120,17 @@ enum {
     P_ML0,                 // max and sum of an item's rows written (4 softmax warps), 2 slots
     P_MR0 = P_ML0 + 2,     // and read by the epilogue (4 warps), 2 slots
     P_SLOT0 = P_MR0 + 2    // KST "full" and KST "empty" of the K ring, VST of each of the V ring, and
-                           // for 8-bit caches: Q made fp16 (4 converting warps)
+                           // for 8-bit caches Q made fp16 (4 converting warps), then INFO "full" and
+                           // INFO "empty" of the ring of looked-up tiles
 };
 
-// Whether the converting warps arrive at barrier P_SLOT0 + i: K, V or Q is there.
+// 8-bit caches: arrivals at barrier P_SLOT0 + i.  Four converting warps make K (and Q), four V, all
+// eight free the looked-up tiles, which two warps look up.
 template <typename C>
-__device__ __forceinline__ bool conv_arrives(int i) {
-    return (i >= 0 && i < C::KST) || (i >= 2 * C::KST && i < 2 * C::KST + C::VST) || i == 2 * (C::KST + C::VST);
+__device__ __forceinline__ uint32_t q8_arrivals(int i) {
+    constexpr int q = 2 * (C::KST + C::VST);
+    if (i > q) return i <= q + C::INFO ? 2u : 8u;
+    return i < C::KST || (i >= 2 * C::KST && i < 2 * C::KST + C::VST) || i == q ? 4u : 1u;
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -210,7 +217,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
     constexpr bool kBF16 = TypeTraits<T>::kId == FA_BF16;
     constexpr bool kOpBF16 = kBF16 && !kQ8;  // operands of the products
     constexpr bool kConvQ = kBF16 && kQ8;    // Q is made fp16
-    constexpr int kNumBars = P_SLOT0 + 2 * C::KST + 2 * C::VST + (kQ8 ? 1 : 0);
+    constexpr int kNumBars = P_SLOT0 + 2 * C::KST + 2 * C::VST + (kQ8 ? 1 + 2 * C::INFO : 0);
     constexpr uint32_t OFF_MISC = C::OFF_BAR + kNumBars * 8;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
@@ -225,6 +232,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
     auto v_full = [&](int s) { return bar(P_SLOT0 + 2 * C::KST + s); };
     auto v_empty = [&](int s) { return bar(P_SLOT0 + 2 * C::KST + C::VST + s); };
     [[maybe_unused]] const uint32_t q_conv = bar(P_SLOT0 + 2 * C::KST + 2 * C::VST);
+    [[maybe_unused]] const Q8Bars<C> q8_bars = {k_full(0), k_empty(0), v_full(0), v_empty(0), bar(P_Q), q_conv, q_conv + 8u};
     const int g = a.H / a.H_kv;
     unsigned int* err = a.err;
 
@@ -233,8 +241,8 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
         *abort_flag = (sbase & 1023u) != 0;
         for (int i = 0; i < kNumBars; ++i)
             ptx::mbar_init(bar(i), i >= P_P0 && i < P_P0 + 3 ? 8u
-                                   : (i >= P_OFREE && i < P_SLOT0) || (kQ8 && conv_arrives<C>(i - P_SLOT0)) ? 4u
-                                                                                                           : 1u);
+                                   : i >= P_OFREE && i < P_SLOT0 ? 4u
+                                   : kQ8 && i >= P_SLOT0 ? q8_arrivals<C>(i - P_SLOT0) : 1u);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -265,29 +273,14 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
     if (kQ8 && warp >= kWarpConv) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
         if constexpr (kQ8) {
-            if (!(sbase & 1023u))
-                convert_tiles<C, T, D, kConvQ>(a, share, geo, smem, abort_flag, k_full(0), k_empty(0), v_full(0), v_empty(0),
-                                            bar(P_Q), q_conv);
+            if (!*abort_flag) convert_tiles<C, D, kConvQ>(a, smem, abort_flag, q8_bars);
         }
     } else if (warp >= kWarpLoadK) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (kQ8 && (warp == kWarpLoadK || warp == kWarpLoadV)) {
-        // ------------------------------------------------------------ Q tiles (8-bit caches)
-        if (warp == kWarpLoadK && !*abort_flag) {
-            int ka = 0;
-            FwdWalk w;
-            for (bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead); more; more = w.next()) {
-                if (w.tiles() == 0) continue;
-                if (lane < C::BOXES) tma_prefetch_3d(&tmQ, lane * 64, w.hd * g, w.t.q_tok);
-                if (ka > 0 && !wait_bar_warp(bar(P_QE), (ka - 1) & 1, abort_flag, err)) break;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(geo.tpt * g) * 128u * C::BOXES);
-                __syncwarp();
-                if (lane < C::BOXES)
-                    ptx::tma_load_3d(sbase + C::OFF_Q + lane * C::kBoxQ_B, &tmQ, lane * 64, w.hd * g, w.t.q_tok, bar(P_Q));
-                ++ka;
-            }
-            __syncwarp();
-            if (lane == 0 && ka > 0) drain_wait(bar(P_Q), (ka - 1) & 1);
+        // ------------------------------------------------------------ rows of K and V (8-bit caches)
+        if constexpr (kQ8) {
+            if (!*abort_flag) look_up_tiles<C>(a, share, geo, smem, abort_flag, q8_bars, warp == kWarpLoadV);
         }
         __syncwarp();
     } else
@@ -403,9 +396,18 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
             if (warp == kWarpMma) {
                 const uint64_t dQ_k = ptx::sw128_desc(sbase + C::OFF_Q, 16, 1024);
                 const uint64_t dK_k = ptx::sw128_desc(sbase + C::OFF_K, 16, kRow8);
+                [[maybe_unused]] int q_loads = 0;
                 for (; ok && more; more = w.next()) {
                     const int nt = w.tiles();
                     if (nt == 0) continue;
+                    if constexpr (kQ8) {  // no other warp loads Q
+                        if (ka > 0 && !(ok = wait_bar(bar(P_QE), (ka - 1) & 1, abort_flag, err))) break;
+                        ptx::mbar_arrive_expect_tx(bar(P_Q), (uint32_t)(geo.tpt * g) * 128u * C::BOXES);
+#pragma unroll
+                        for (int x = 0; x < C::BOXES; ++x)
+                            ptx::tma_load_3d(sbase + C::OFF_Q + x * C::kBoxQ_B, &tmQ, x * 64, w.hd * g, w.t.q_tok, bar(P_Q));
+                        q_loads = ka + 1;
+                    }
                     if (!(ok = wait_bar(kConvQ ? q_conv : bar(P_Q), ka & 1, abort_flag, err))) break;
                     for (int j = 0; j < nt; ++j, ++jg) {
                         const int s = jg % C::KST;
@@ -430,6 +432,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                 }
                 // every S product is read by a P V product, so all are complete once the other
                 // issuer has drained
+                if (kQ8 && q_loads > 0) drain_wait(bar(P_Q), (q_loads - 1) & 1);
             } else {
                 const uint64_t dV_mn = ptx::sw128_desc(sbase + C::OFF_V, kBlk, kRow8);
                 for (; ok && more; more = w.next()) {
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                         load(r);
                         exps(r);
                         __syncwarp();
-                        done = ptx::named_bar_and(pair, 64, !(row_valid && sum > kMaxSum));
+                        done = ptx::named_bar_and(pair, 64, !(row_valid && sum > (kQ8 ? kQ8MaxSum : kMaxSum)));
                     }
                     if (!done) {
                         uint32_t r[HN];
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                         __syncwarp();
                         ptx::named_bar_sync(pair, 64);
                         if (hf == 1) mx = *xch;
-                        mx = mx == -INFINITY ? -INFINITY : kQ8 ? fmaf(mx, scale_tile, v_exp) : mx * scale_log2;
+                        mx = mx == -INFINITY ? -INFINITY : kQ8 ? fmaf(mx, scale_tile, v_exp - kQ8Lift) : mx * scale_log2;
                         rescale = mx > m_run;
                         if (rescale) {
                             alpha = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - mx);
@@ -667,7 +670,10 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
         // O = acc / l and LSE = (m + log2 l) ln 2 of a whole item; of a cut one the raw
         // accumulator with (m, l), and the last part to arrive joins them.  Meanwhile the
         // softmax warps are at the next item; its first P V product waits for O to be read.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
+        if constexpr (C::REGS_EPI > C::REGS)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
         const int t = threadIdx.x - kWarpEpi * 32;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const int ti = t / g, th = t - ti * g;  // token and head of the row
@@ -798,7 +804,7 @@ bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, 
 template <typename T, int D, bool kPaged, bool kGroup, bool kTree, bool kQ8 = false>
 cudaError_t launch_t(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     using C = PCfg<D, kQ8>;
-    constexpr uint32_t kSmem = C::OFF_BAR + (P_SLOT0 + 2 * C::KST + 2 * C::VST + (kQ8 ? 1 : 0)) * 8 + 16;
+    constexpr uint32_t kSmem = C::OFF_BAR + (P_SLOT0 + 2 * C::KST + 2 * C::VST + (kQ8 ? 1 + 2 * C::INFO : 0)) * 8 + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
     const int g = a.H / a.H_kv;
     FwdGeom geo;

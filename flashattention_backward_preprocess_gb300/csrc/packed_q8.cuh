@@ -12,10 +12,12 @@
 // by a power of two to a largest magnitude in [2^14, 2^15), which leaves bf16 numbers exact down to
 // 2^-31 of it, and P has 11 bits instead of 8.
 //
-// Every thread fetches, with 16-byte asynchronous copies, the pieces that it will convert, so that
-// data needs no barrier; rows are looked up (table entry, then exponent) a tile or two ahead, one
-// thread per row, any page size.  Rows that are no key of the request (behind its last, before its
-// window, on no page) are filled with zeros.
+// Two warps look the rows up (table entry, then exponents), row by row, so any page size will do; four
+// warps for K and four for V load the numbers into registers, each piece as soon as the one before it
+// in its place is converted, and store the operands.
+// Rows that are no key of the request (behind its last, before its window, on no page) are zeros.
+// Numbers on their way to registers cost no shared memory: its bandwidth is what bounds a tile (64 KB
+// of operands written, 96 KB of them and of Q read by the products, at 128 bytes a cycle).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -26,15 +28,18 @@
 namespace fa {
 namespace {
 
-constexpr uint32_t kConvBarrierId = 6;  // the four converting warps (packed_fwd_tc.cuh has 1 to 5)
+// Words of half a looked-up tile: largest exponents of K and V in the low bytes and these bits;
+// smallest exponents (of those that are not 0).
+constexpr uint32_t kInfoValid = 1u << 16;  // there is such a tile
+constexpr uint32_t kInfoFirst = 1u << 17;  // it is the first of its item
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// 16 bytes that this kernel reads once.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
 // Two e4m3 numbers (low half of the word: lower byte first) as fp16.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -89,184 +94,221 @@ __device__ __forceinline__ float convert_q_row(uint8_t* q, int t) {
     return __int_as_float((127 - n) << 23);
 }
 
-// What the four converting warps do.  Elements of their stream: K and V of each tile in turn.
-// A timeout never leaves the loop, so that no warp is left at the barrier: all waits return at once
-// then.
-template <typename C, typename T, int D, bool kConvQ>
-__device__ __forceinline__ void convert_tiles(const PackedFwd& a, const FwdShare& share, const FwdGeom& geo, uint8_t* smem,
-                                              volatile int* abort_flag, uint32_t k_full, uint32_t k_empty, uint32_t v_full,
-                                              uint32_t v_empty, uint32_t q_full, uint32_t q_conv) {
-    constexpr int BN = C::BN, S8 = C::S8, AHEAD = C::AHEAD;
-    constexpr int CPR = D / 16;                    // 16-byte pieces of a row
-    constexpr int RSTEP = 128 / CPR, N = BN / RSTEP;  // rows between a thread's pieces, pieces per tile
-    const int t = threadIdx.x - 16 * 32, lane = t & 31, warp = t >> 5;
-    const int col = t % CPR, row0 = t / CPR;
-    const uint32_t sbase = ptx::smem_u32(smem);
-    unsigned int* err = a.err;
-    longlong2* at = reinterpret_cast<longlong2*>(smem + C::OFF_AT);
-    uint16_t* exps = reinterpret_cast<uint16_t*>(smem + C::OFF_EXP);
-    uint32_t* part = reinterpret_cast<uint32_t*>(smem + C::OFF_PART);
-    const bool col_live = col * 16 < a.d;
+// Shared-memory addresses of the barriers of the rings: the first of each.
+template <typename C>
+struct Q8Bars {
+    uint32_t k_full, k_empty, v_full, v_empty, q_full, q_conv, info;
+    __device__ __forceinline__ uint32_t info_full(int s) const { return info + 8u * s; }
+    __device__ __forceinline__ uint32_t info_empty(int s) const { return info + 8u * (C::INFO + s); }
+};
 
+// The two look-up warps, each for half of the rows of every tile of the CTA's share.  A step publishes
+// tile j (where its rows lie, their exponents), finds the rows of tile j + 1 and loads their
+// exponents, and loads the table entries of tile j + 2.  A word without the valid bit ends the stream.
+template <typename C>
+__device__ __forceinline__ void look_up_tiles(const PackedFwd& a, const FwdShare& share, const FwdGeom& geo, uint8_t* smem,
+                                              volatile int* abort_flag, const Q8Bars<C>& bars, int half) {
+    constexpr int BN = C::BN, HB = BN / 2, R = HB / 32;  // rows of the warp and of a lane
+    const int lane = threadIdx.x & 31;
+    longlong2* at = reinterpret_cast<longlong2*>(smem + C::OFF_AT) + half * HB;
+    uint16_t* exps = reinterpret_cast<uint16_t*>(smem + C::OFF_EXP) + half * HB;
+    volatile uint2* words = reinterpret_cast<volatile uint2*>(smem + C::OFF_INFO) + half;
+    const int shift = (a.page_size & (a.page_size - 1)) == 0 ? 31 - __clz(a.page_size) : -1;
     FwdWalk w;
     bool more = w.init(share, blockIdx.x, a.H_kv, geo.overhead);
     while (more && w.tiles() == 0) more = w.next();
     int j = more ? w.j0 : 0;
-    // the next tile to look up: this thread's row of it
-    int nx_entry = -1, nx_in = -1, nx_hd = 0;
-    bool nx_valid = false, nx_first = false;
-    auto look_up = [&]() {
-        nx_valid = more;
-        nx_in = -1;
-        if (!more) return;
-        const int key = (w.t.n_first + j) * BN + t;
+    int entry[R], in[R], hd = 0;  // table entries, and rows in their pages (-1: no key)
+    auto entries = [&]() -> uint32_t {
+        if (!more) return 0u;
+        const int key0 = (w.t.n_first + j) * BN + half * HB + lane;
         // keys before the window of the unit's first row may have lost their pages
         const int k_lo = a.window > 0 ? w.t.pos0 - a.window + 1 : 0;
-        if (t < BN && key < w.t.S_k && key >= k_lo) {
-            const int e = key / a.page_size;
-            nx_in = key - e * a.page_size;
-            nx_entry = e < a.max_pages ? a.table[(size_t)w.t.n * a.max_pages + e] : -1;
+        const int* row = a.table + (size_t)w.t.n * a.max_pages;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int key = key0 + 32 * i;
+            in[i] = -1;
+            if (key < w.t.S_k && key >= k_lo) {
+                const int e = shift >= 0 ? key >> shift : key / a.page_size;
+                in[i] = key - e * a.page_size;
+                entry[i] = e < a.max_pages ? row[e] : -1;
+            }
         }
-        nx_hd = w.hd;
-        nx_first = j == w.j0;
+        hd = w.hd;
+        const uint32_t f = kInfoValid | (j == w.j0 ? kInfoFirst : 0u);
         if (++j == w.j1) {
             do more = w.next();
             while (more && w.tiles() == 0);
             if (more) j = w.j0;
         }
+        return f;
     };
-    // exponents (K, V in the next byte) of this thread's row of tiles jg .. jg + AHEAD; whether each
-    // is there, and the first of its item
-    uint32_t ex[AHEAD + 1];
-    uint32_t valid = 0, first = 0;
-    // where the rows of the looked-up tile lie, to the others
-    auto enter = [&](int tile, int i) {
-        longlong2 o = make_longlong2(-1, -1);
-        ex[i] = 0;
-        if (nx_valid && nx_in >= 0) {
-            bool bad = false;
-            const long long pg = page_checked(nx_entry, a.pages, &bad);
-            if (bad) {
-                atomicOr(err, kErrPage);
-            } else {
-                o.x = pg * a.k_page + (long long)nx_in * a.k.tok + (long long)nx_hd * a.k.head;
-                o.y = pg * a.v_page + (long long)nx_in * a.v.tok + (long long)nx_hd * a.v.head;
-                const long long e = (pg * a.H_kv + nx_hd) * a.page_size + nx_in;
-                ex[i] = a.k_exp[e] | (uint32_t)a.v_exp[e] << 8;
+    long long ko[R], vo[R];  // -1: zeros
+    uint8_t ek[R], ev[R];
+    auto rows = [&]() {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            ko[i] = vo[i] = -1;
+            ek[i] = ev[i] = 0;
+            if (in[i] >= 0) {
+                bool bad = false;
+                const long long pg = page_checked(entry[i], a.pages, &bad);
+                if (bad) {
+                    atomicOr(a.err, kErrPage);
+                } else {
+                    ko[i] = pg * a.k_page + (long long)in[i] * a.k.tok + (long long)hd * a.k.head;
+                    vo[i] = pg * a.v_page + (long long)in[i] * a.v.tok + (long long)hd * a.v.head;
+                    const long long e = (pg * a.H_kv + hd) * a.page_size + in[i];
+                    ek[i] = a.k_exp[e];
+                    ev[i] = a.v_exp[e];
+                }
             }
         }
-        if (t < BN) at[(tile & 3) * BN + t] = o;
-        valid |= (uint32_t)nx_valid << i;
-        first |= (uint32_t)(nx_valid && nx_first) << i;
     };
-    // fetches element n of the stream (tile n / 2) into its slot
-    auto fetch = [&](int n, bool there) {
-        if (there && col_live) {
-            const char* base = static_cast<const char*>((n & 1) ? a.V : a.K) + col * 16;
-            const longlong2* rows = at + ((n >> 1) & 3) * BN;
-            const uint32_t dst = sbase + C::OFF_8 + (uint32_t)(n % S8) * C::kTile8_B + t * 16;
+    // false after a timeout
+    auto publish = [&](int tile, uint32_t flags) {
+        const int s = tile % C::INFO;
+        if (tile >= C::INFO && !wait_bar_warp(bars.info_empty(s), (tile / C::INFO - 1) & 1, abort_flag, a.err)) return false;
+        uint32_t mk = 0, mv = 0, lk = 255, lv = 255;
+        if (flags) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const longlong2 o2 = rows[row0 + i * RSTEP];
-                const long long o = (n & 1) ? o2.y : o2.x;
-                cp_async16(dst + i * 2048, base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
+            for (int i = 0; i < R; ++i) {
+                at[s * BN + lane + 32 * i] = make_longlong2(ko[i], vo[i]);
+                exps[s * BN + lane + 32 * i] = (uint16_t)(ek[i] | ev[i] << 8);
+                mk = max(mk, (uint32_t)ek[i]), mv = max(mv, (uint32_t)ev[i]);
+                lk = ek[i] ? min(lk, (uint32_t)ek[i]) : lk;
+                lv = ev[i] ? min(lv, (uint32_t)ev[i]) : lv;
             }
+            mk = __reduce_max_sync(0xffffffffu, mk), mv = __reduce_max_sync(0xffffffffu, mv);
+            lk = __reduce_min_sync(0xffffffffu, lk), lv = __reduce_min_sync(0xffffffffu, lv);
         }
-        cp_async_commit();
-    };
-    // makes a fetched tile an operand tile at `dst` (blocks of 64 columns, 128-byte swizzle); `sh`: the
-    // byte of the rows' exponents
-    auto convert = [&](int n, uint32_t dst, const uint16_t* rows, int sh, int top) {
-        const uint32_t src = C::OFF_8 + (uint32_t)(n % S8) * C::kTile8_B + t * 16;
-        const uint32_t out = dst + (uint32_t)(col / 4) * (BN * 128);
-        const bool odd_first = (col & 4) != 0;  // eight lanes' stores to eight different pieces of a line
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = row0 + i * RSTEP;
-            const uint4 q = col_live ? *reinterpret_cast<const uint4*>(smem + src + i * 2048) : make_uint4(0u, 0u, 0u, 0u);
-            const int by = (int)(rows[r] >> sh & 0xff) - top;  // <= 0
-            const uint32_t f = half2_pow2(by < -14 ? -14 : by);
-            uint32_t h[8];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) e4m3x4_to_f16((&q.x)[c], h[2 * c], h[2 * c + 1]);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) h[c] = hmul2(h[c], f);
-            if (by < -14) {
-                const uint32_t f2 = half2_pow2(by + 14);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) h[c] = hmul2(h[c], f2);
-            }
-            const int c0 = (col & 3) * 2;
-            uint8_t* line = smem + out + r * 128;
-            uint4* even = reinterpret_cast<uint4*>(line + ((c0 ^ (r & 7)) * 16));
-            uint4* odd = reinterpret_cast<uint4*>(line + (((c0 + 1) ^ (r & 7)) * 16));
-            const uint4 he = make_uint4(h[0], h[1], h[2], h[3]), ho = make_uint4(h[4], h[5], h[6], h[7]);
-            *(odd_first ? odd : even) = odd_first ? ho : he;
-            *(odd_first ? even : odd) = odd_first ? he : ho;
+        if (lane == 0) {
+            words[s * 2].x = mk | mv << 8 | flags;
+            words[s * 2].y = lk | lv << 8;
         }
-        ptx::fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars.info_full(s));
+        return true;
+    };
+    uint32_t now = entries();
+    if (now) rows();
+    uint32_t next = entries();
+    for (int tile = 0; publish(tile, now) && now; ++tile) {
+        if (next) rows();
+        now = next;
+        next = entries();
+    }
+}
+
+// Of a tile with exponents more than 14 below the largest: the rest of the way for those rows.
+template <typename C, int N, int RSTEP>
+__device__ __forceinline__ void shrink_rows(uint8_t* out, int other, const uint16_t* rows, int sh, int largest) {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        const uint32_t f = half2_pow2(min((int)(rows[i * RSTEP] >> sh & 0xff) - largest + 14, 0));
+        for (int x = 0; x < 2; ++x) {
+            uint4* p = reinterpret_cast<uint4*>(out + i * RSTEP * 128 + x * other);
+            const uint4 h = *p;
+            *p = make_uint4(hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
+        }
+    }
+}
+
+// The eight converting warps.  A timeout leaves the loop of every warp alike: they share no barrier
+// but those with bounded waits.
+template <typename C, int D, bool kConvQ>
+__device__ __forceinline__ void convert_tiles(const PackedFwd& a, uint8_t* smem, volatile int* abort_flag,
+                                              const Q8Bars<C>& bars) {
+    constexpr int BN = C::BN;
+    constexpr int CPR = D / 16;                       // 16-byte pieces of a row
+    constexpr int RSTEP = 128 / CPR, N = BN / RSTEP;  // rows between a thread's pieces, pieces per tile
+    static_assert(RSTEP % 8 == 0, "a thread's pieces have the same place in their lines");
+    static_assert(C::KST == C::VST, "one number of slots");
+    const bool is_v = threadIdx.x >= 20 * 32;
+    const int t = threadIdx.x & 127, lane = t & 31;
+    const int col = t % CPR, row0 = t / CPR;
+    unsigned int* err = a.err;
+    const long long* at = reinterpret_cast<const long long*>(smem + C::OFF_AT) + 2 * row0 + (is_v ? 1 : 0);
+    const uint16_t* exps = reinterpret_cast<const uint16_t*>(smem + C::OFF_EXP) + row0;
+    volatile const uint2* words = reinterpret_cast<volatile const uint2*>(smem + C::OFF_INFO);
+    const bool col_live = col * 16 < a.d;  // columns behind the head dimension are zeros
+    const char* base = static_cast<const char*>(is_v ? a.V : a.K) + (col_live ? col * 16 : 0);
+    const int sh = is_v ? 8 : 0;  // of the exponent bytes
+    const uint32_t ring = is_v ? C::OFF_V : C::OFF_K, full = is_v ? bars.v_full : bars.k_full;
+    const uint32_t empty = is_v ? bars.v_empty : bars.k_empty;
+    // where the first piece's halves go: blocks of 64 columns, 128-byte swizzle.  Eight lanes' stores go
+    // to eight different pieces of a line: half of them store the odd half first
+    const uint32_t even = (uint32_t)(((col & 3) * 2) ^ (row0 & 7)) * 16;
+    const bool odd_first = (col & 4) != 0;
+    const uint32_t out0 = (uint32_t)(col / 4) * (BN * 128) + row0 * 128 + (odd_first ? even ^ 16u : even);
+    const int other = odd_first ? (int)even - (int)(even ^ 16u) : (int)(even ^ 16u) - (int)even;
+    auto load = [&](long long o) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (o >= 0 && col_live) q = ld_once(base + o);
+        return q;
+    };
+    // whether tile j is there, once it is known
+    auto there = [&](int j) {
+        if (!wait_bar_warp(bars.info_full(j % C::INFO), (j / C::INFO) & 1, abort_flag, err)) return false;
+        const int s = j % C::INFO;
+        return (words[s * 2].x & words[s * 2 + 1].x & kInfoValid) != 0;
     };
 
-    look_up();
+    uint4 q[N];
+    bool more = there(0);
+    if (more) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-        enter(i, i);
-        look_up();
+        for (int i = 0; i < N; ++i) q[i] = load(at[i * RSTEP * 2]);
     }
-    ex[AHEAD] = 0;
-    ptx::named_bar_sync(kConvBarrierId, 128);
-#pragma unroll
-    for (int n = 0; n < S8; ++n) fetch(n, valid >> (n / 2) & 1u);
     int ka = 0;
-    for (int jg = 0; valid & 1u; ++jg) {
-        enter(jg + AHEAD, AHEAD);
-        look_up();
-        // the tile's largest exponents
-        const int s2 = jg & 1;
-        if (t < BN) exps[s2 * BN + t] = (uint16_t)ex[0];
-        const uint32_t mk = __reduce_max_sync(0xffffffffu, ex[0] & 0xffu), mv = __reduce_max_sync(0xffffffffu, ex[0] >> 8);
-        if (lane == 0) part[s2 * 4 + warp] = mk | mv << 8;
-        __syncwarp();
-        ptx::named_bar_sync(kConvBarrierId, 128);
-        uint32_t tk = 0, tv = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t p = part[s2 * 4 + i];
-            tk = max(tk, p & 0xffu);
-            tv = max(tv, p >> 8);
-        }
-        tv = max(tv, 1u);  // 2^-ev is a number
-        if (t == 0) *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4) = tk | tv << 8;
-        if (first & 1u) {
-            if constexpr (kConvQ) {
-                wait_bar_warp(q_full, ka & 1, abort_flag, err);
-                reinterpret_cast<float*>(smem + C::OFF_QS)[(ka & 3) * 128 + t] = convert_q_row<C, D>(smem + C::OFF_Q, t);
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(q_conv);
-            }
+    for (int jg = 0; more; ++jg) {
+        const int s = jg % C::INFO, slot = jg % C::KST;
+        const uint32_t w0 = words[s * 2].x, w1 = words[s * 2 + 1].x, l0 = words[s * 2].y, l1 = words[s * 2 + 1].y;
+        // the largest exponents (V's at least 1: 2^-ev is a number), and whether any is far below them
+        const uint32_t mk = max(w0 & 0xff, w1 & 0xff), mv = max(max(w0 >> 8 & 0xff, w1 >> 8 & 0xff), 1u);
+        const int largest = (int)(is_v ? mv : mk);
+        const bool far = (int)min(l0 >> sh & 0xff, l1 >> sh & 0xff) + 14 < largest;
+        if (!is_v && t == 0) *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4) = mk | mv << 8;
+        if (kConvQ && !is_v && (w0 & kInfoFirst)) {
+            if (!wait_bar_warp(bars.q_full, ka & 1, abort_flag, err)) break;
+            reinterpret_cast<float*>(smem + C::OFF_QS)[(ka & 3) * 128 + t] = convert_q_row<C, D>(smem + C::OFF_Q, t);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bars.q_conv);
             ++ka;
         }
-        // K
-        cp_async_wait<S8 - 1>();
-        const int sk = jg % C::KST, sv = jg % C::VST;
-        if (jg >= C::KST) wait_bar_warp(k_empty + 8u * sk, (jg / C::KST - 1) & 1, abort_flag, err);
-        convert(2 * jg, C::OFF_K + sk * C::kTileKV_B, exps + s2 * BN, 0, (int)tk);
-        if (lane == 0) ptx::mbar_arrive(k_full + 8u * sk);
-        fetch(2 * jg + S8, valid >> (S8 / 2) & 1u);
-        // V
-        cp_async_wait<S8 - 1>();
-        if (jg >= C::VST) wait_bar_warp(v_empty + 8u * sv, (jg / C::VST - 1) & 1, abort_flag, err);
-        convert(2 * jg + 1, C::OFF_V + sv * C::kTileKV_B, exps + s2 * BN, 8, (int)tv);
-        if (lane == 0) ptx::mbar_arrive(v_full + 8u * sv);
-        fetch(2 * jg + 1 + S8, valid >> ((S8 + 1) / 2) & 1u);
-        valid >>= 1;
-        first >>= 1;
+        more = there(jg + 1);
+        if (jg >= C::KST && !wait_bar_warp(empty + 8u * slot, (jg / C::KST - 1) & 1, abort_flag, err)) break;
+        uint8_t* out = smem + ring + slot * C::kTileKV_B + out0;
+        const uint16_t* rows = exps + s * BN;
+        const long long* from = at + (jg + 1) % C::INFO * BN * 2;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) ex[i] = ex[i + 1];
+        for (int i = 0; i < N; ++i) {
+            const int by = (int)(rows[i * RSTEP] >> sh & 0xff) - largest;  // <= 0
+            const uint32_t f = (uint32_t)max(by + 15, 1) * 0x04000400u;    // 2^by, 2^-14 at least
+            uint32_t h[8];
+            e4m3x4_to_f16(q[i].x, h[0], h[1]);
+            e4m3x4_to_f16(q[i].y, h[2], h[3]);
+            e4m3x4_to_f16(q[i].z, h[4], h[5]);
+            e4m3x4_to_f16(q[i].w, h[6], h[7]);
+            // the same piece of the next tile
+            if (more) q[i] = load(from[i * RSTEP * 2]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) h[c] = hmul2(h[c], f);
+            const uint4 he = make_uint4(h[0], h[1], h[2], h[3]), ho = make_uint4(h[4], h[5], h[6], h[7]);
+            uint8_t* line = out + i * RSTEP * 128;
+            *reinterpret_cast<uint4*>(line) = odd_first ? ho : he;
+            *reinterpret_cast<uint4*>(line + other) = odd_first ? he : ho;
+        }
+        if (far) shrink_rows<C, N, RSTEP>(out, other, rows, sh, largest);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::mbar_arrive(full + 8u * slot);
+            ptx::mbar_arrive(bars.info_empty(s));
+        }
     }
-    cp_async_wait<0>();
 }
 
 }  // namespace
