@@ -101,7 +101,7 @@ def load_library(path: str | None = None):
         lib.fa_paged_write.restype = I
         lib.fa_paged_fwd_ex.argtypes = [V] * 11 + [I] * 9 + [V, F, I, I, I, I, V, Z, V]
         lib.fa_paged_fwd_ex.restype = I
-        lib.fa_paged_workspace_bytes_ex.argtypes = [I] * 8
+        lib.fa_paged_workspace_bytes_ex.argtypes = [I] * 9
         lib.fa_paged_workspace_bytes_ex.restype = Z
         lib.fa_paged_write_q8.argtypes = lib.fa_paged_read_q8.argtypes = [V] * 7 + [I] * 5 + [V, I, V]
         lib.fa_paged_write_q8.restype = lib.fa_paged_read_q8.restype = I

@@ -512,6 +512,9 @@ cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaS
 cudaError_t launch_packed_tree(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 // packed_q8.cu: tensor cores, 8-bit cache (f16 / bf16 queries, any page size)
 cudaError_t launch_packed_q8(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
+// packed_q8.cu: the same by way of a copy of the rows in the queries' type, where that pays
+bool q8_spread(const PackedFwd& a);
+cudaError_t launch_q8_spread(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 // packed_q8_rows.cu: the same for few rows per request (few_rows)
 cudaError_t launch_q8_rows(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st);
 // packed_simt.cu: CUDA cores (f32, and layouts that TMA cannot address)

@@ -219,17 +219,19 @@ size_t fa_varlen_workspace_bytes(int N, int T_q, int T_k, int H, int H_kv, int d
     return fwd_bytes(a);
 }
 
-size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype, int quantised) {
-    if (check_common(N, H, H_kv, d, 1.f, 0, 0, 0, dtype) != FA_OK || T_q < 0 || page_size <= 0) return 0;
+size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int max_pages, int dtype,
+                                   int quantised) {
+    if (check_common(N, H, H_kv, d, 1.f, 0, 0, 0, dtype) != FA_OK || T_q < 0 || page_size <= 0 || max_pages <= 0) return 0;
     PackedFwd a = {};
     static const uint8_t some = 0;
     if (quantised) a.k_exp = a.v_exp = &some;
     a.N = N, a.T_q = T_q, a.H = H, a.H_kv = H_kv, a.d = d, a.dtype = dtype, a.page_size = page_size;
+    a.max_pages = max_pages;
     return fwd_bytes(a);
 }
 
 size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype) {
-    return fa_paged_workspace_bytes_ex(N, T_q, H, H_kv, d, page_size, dtype, 0);
+    return fa_paged_workspace_bytes_ex(N, T_q, H, H_kv, d, page_size, 1, dtype, 0);
 }
 
 int fa_varlen_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q, const int* cu_k,

@@ -5,11 +5,13 @@
 namespace fa {
 namespace {
 
-// Steps over an 8-bit cache whose requests have 16 rows (tokens x heads of a group) or fewer on
-// average, on pages of whole 16-key pieces: packed_q8_rows.cu.
+// Steps over an 8-bit cache whose requests have 32 rows (tokens x heads of a group) or fewer on
+// average, on pages of whole 16-key pieces: packed_q8_rows.cu, which reads the cache once per 16 rows
+// (32 requests over 98000 keys, 4 heads a group: 1, 4, 8 and 16 tokens each take 67, 75, 125 and 219
+// us there, 130, 131, 140 and 165 us in 128-row tiles).
 bool few_rows(const PackedFwd& a) {
     const long long g = a.H / a.H_kv;
-    return a.d <= 128 && g <= 16 && a.page_size % 16 == 0 && a.T_q * g <= 16ll * a.N;
+    return a.d <= 128 && g <= 16 && a.page_size % 16 == 0 && a.T_q * g <= 32ll * a.N;
 }
 
 template <typename T>
@@ -25,7 +27,9 @@ cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_packed_fwd(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
-    if (a.q8()) return few_rows(a) ? launch_q8_rows(a, ws, bytes, st) : launch_packed_q8(a, ws, bytes, st);
+    if (a.q8() && few_rows(a)) return launch_q8_rows(a, ws, bytes, st);
+    if (a.q8() && q8_spread(a)) return launch_q8_spread(a, ws, bytes, st);
+    if (a.q8()) return launch_packed_q8(a, ws, bytes, st);
     if (a.tree) return launch_packed_tree(a, ws, bytes, st);
     return a.dtype == FA_F16 ? launch_d<__half>(a, ws, bytes, st) : launch_d<__nv_bfloat16>(a, ws, bytes, st);
 }

@@ -1,8 +1,74 @@
-// packed_q8.cu -- the instances of the tensor-core forward (packed_fwd_tc.cuh) over 8-bit caches.
+// packed_q8.cu -- the instances of the tensor-core forward (packed_fwd_tc.cuh) over 8-bit caches, and
+// the way round them for calls of many rows.
+//
+// In the tensor-core kernel every 128-row tile of a request converts the request's keys again, and the
+// conversion is what takes its time (about 4500 cycles of a 128-key tile; the products need 1300).
+// Where requests have many such tiles (chunks of prompts), one pass makes the rows of the cache that
+// the step reads fp16 or bf16, exactly, in pages of the workspace, and the kernel for caches of that
+// type does the rest.  Chunks of up to 512 tokens over up to 8000 cached ones, 10 requests, H = 32,
+// H_kv = 8, d = 128: see q8_spread.
 #include "packed_fwd_tc.cuh"
 
 namespace fa {
 namespace {
+
+constexpr int kSpreadT = 256, kSpreadTok = 32;  // threads of a block, tokens
+
+// Tokens [kSpreadTok * blockIdx.x, ..) of request blockIdx.y, those that its new tokens may see, to pages
+// of its own: entry e of its table becomes page max_pages * n + e.
+template <typename T>
+__global__ void __launch_bounds__(kSpreadT) q8_spread_kernel(const PackedFwd a, T* K, T* V, int* table) {
+    const int n = blockIdx.y, k0 = blockIdx.x * kSpreadTok;
+    Seq s;
+    if (!seq_at(a, n, s) || s.nq == 0) return;  // the plan reports lengths that do not fit
+    for (int e = k0 / a.page_size + threadIdx.x; e < a.max_pages && (long long)e * a.page_size < k0 + kSpreadTok; e += kSpreadT)
+        if ((long long)e * a.page_size >= k0) table[(size_t)n * a.max_pages + e] = n * a.max_pages + e;
+    // whole pages from the first key that any new token sees: none of their rows may be left unset
+    int lo = a.window > 0 ? max(s.nk - s.nq - a.window + 1, 0) : 0;
+    lo -= lo % a.page_size;
+    const int hi = (int)min((long long)s.nk, table_room(a));
+    const int per = a.H_kv * (a.d / 16);
+    for (int i = threadIdx.x; i < kSpreadTok * per; i += kSpreadT) {
+        const int j = k0 + i / per, c = i % per, h = c / (a.d / 16), x = c % (a.d / 16) * 16;
+        if (j < lo || j >= hi) continue;
+        const int in = j % a.page_size;
+        bool bad = false;
+        const long long pg = page_of(a.table + (size_t)n * a.max_pages, j, a.page_size, a.max_pages, a.pages, &bad);
+        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+        float sk = 0.f, sv = 0.f;
+        if (bad) {
+            if (c == 0) atomicOr(a.err, kErrPage);
+        } else {
+            k = ld_once(static_cast<const char*>(a.K) + pg * a.k_page + in * a.k.tok + h * a.k.head + x);
+            v = ld_once(static_cast<const char*>(a.V) + pg * a.v_page + in * a.v.tok + h * a.v.head + x);
+            const long long e = (pg * a.H_kv + h) * a.page_size + in;
+            sk = exp_value(a.k_exp[e]);
+            sv = exp_value(a.v_exp[e]);
+        }
+        const long long to = (((long long)n * a.max_pages * a.page_size + j) * a.H_kv + h) * a.d + x;
+        auto put = [&](T* dst, const uint4& q, float f) {
+            uint32_t w[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t lo2, hi2;
+                e4m3x4_to_f16((&q.x)[u], lo2, hi2);
+                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
+                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
+                w[2 * u] = pack2<TypeTraits<T>::kId == FA_BF16>(p.x * f, p.y * f);
+                w[2 * u + 1] = pack2<TypeTraits<T>::kId == FA_BF16>(r.x * f, r.y * f);
+            }
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        };
+        put(K + to, k, sk);
+        put(V + to, v, sv);
+    }
+}
+
+size_t spread_cache_bytes(const PackedFwd& a) {
+    return packed_align((size_t)a.N * a.max_pages * a.page_size * a.H_kv * a.d * 2);
+}
+size_t spread_table_bytes(const PackedFwd& a) { return packed_align((size_t)a.N * a.max_pages * 4); }
 
 template <typename T, bool kTree>
 cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
@@ -18,6 +84,44 @@ cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t s
 cudaError_t launch_packed_q8(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
     if (a.dtype == FA_F16) return a.tree ? launch_d<__half, true>(a, ws, bytes, st) : launch_d<__half, false>(a, ws, bytes, st);
     return a.tree ? launch_d<__nv_bfloat16, true>(a, ws, bytes, st) : launch_d<__nv_bfloat16, false>(a, ws, bytes, st);
+}
+
+// From four 128-row tiles per request on, where the copy (of all that the tables have room for: the
+// lengths are on the device) takes 2 GB each of K and V at most, and pages that the other kernel takes.
+bool q8_spread(const PackedFwd& a) {
+    const long long g = a.H / a.H_kv;
+    const int bn = a.d == 256 ? 64 : 128;
+    const bool pages = a.page_size % 8 == 0 && (bn % a.page_size == 0 || a.page_size % bn == 0);
+    return pages && a.T_q * g >= 512ll * a.N && a.N <= 65535 &&
+           (double)a.N * a.max_pages * a.page_size * a.H_kv * a.d * 2 <= 2147483648.0;
+}
+
+cudaError_t launch_q8_spread(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
+    const size_t cache = spread_cache_bytes(a), table = spread_table_bytes(a);
+    char* base = static_cast<char*>(ws);
+    PackedFwd b = a;
+    b.k_exp = b.v_exp = nullptr;
+    b.pages = a.N * a.max_pages;
+    b.k.head = b.v.head = a.d;
+    b.k.tok = b.v.tok = (long long)a.H_kv * a.d;
+    b.k_page = b.v_page = b.k.tok * a.page_size;
+    if (ws == nullptr) {
+        const cudaError_t e = launch_packed_fwd(b, nullptr, bytes, st);
+        *bytes += 2 * cache + table;
+        return e;
+    }
+    b.K = base, b.V = base + cache;
+    int* own = reinterpret_cast<int*>(base + 2 * cache);
+    b.table = own;
+    const long long room = (long long)a.max_pages * a.page_size;
+    const dim3 grid((unsigned)((room + kSpreadTok - 1) / kSpreadTok), (unsigned)a.N);
+    if (a.dtype == FA_F16)
+        q8_spread_kernel<<<grid, kSpreadT, 0, st>>>(a, reinterpret_cast<__half*>(base), reinterpret_cast<__half*>(base + cache), own);
+    else
+        q8_spread_kernel<<<grid, kSpreadT, 0, st>>>(a, reinterpret_cast<__nv_bfloat16*>(base),
+                                                    reinterpret_cast<__nv_bfloat16*>(base + cache), own);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_packed_fwd(b, base + 2 * cache + table, bytes, st);
 }
 
 }  // namespace fa

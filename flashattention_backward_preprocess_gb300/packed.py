@@ -264,7 +264,7 @@ def fa_paged_fwd(Q, K_cache, V_cache, block_table, cu_q, seq_lens, scale: float 
     cols = _table(block_table, N)
     dt = _type(Q)
     dev = _device(Q, K_cache, V_cache, block_table, cu_q, seq_lens, O, LSE, K_exp, V_exp, tree)
-    need = _paged_ws(dev.index, N, T_q, H, H_kv, d, page, dt, int(q8))
+    need = _paged_ws(dev.index, N, T_q, H, H_kv, d, page, max(cols, 1) if q8 else 1, dt, int(q8))
 
     def body(st):
         o, lse, fill = _outputs(Q, T_q, H, O, LSE)

@@ -298,8 +298,12 @@ size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page
  *                  to its own place; tokens past 64 * tree_words are seen by none).  All tokens
  *                  before the new ones are seen.  causal must be 1 and window_size 0.
  *   tree_words   : 1 to 1024
- * A row that sees nothing gets O = 0 and LSE = -inf.  Kernels as for fa_paged_fwd; an 8-bit cache
- * runs the FFMA kernel.
+ *   K_exp, V_exp are 16-byte aligned.
+ * A row that sees nothing gets O = 0 and LSE = -inf.  F16/BF16 run tensor-core kernels, over an 8-bit
+ * cache with any page_size; F32 and wider head groups than 128 an FFMA kernel.  Where rows of an 8-bit
+ * cache are not copied they are fp16 operands, and so is Q after a scaling of each row by a power of two
+ * (exact down to 2^-31 of the row's largest element for BF16) and P: its 11 bits, with a fixed step of
+ * 2^-33 of the row's largest weight at the small end.  The result is bitwise reproducible.
  */
 int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp,
                     void* O, float* LSE, const int* block_table, const int* cu_q, const int* seq_lens,
@@ -307,8 +311,12 @@ int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, con
                     int H, int H_kv, int d, const long long* strides, float scale, int causal, int window_size, int fill,
                     int dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of fa_paged_fwd_ex (quantised: with K_exp and V_exp); 0 for arguments it refuses. */
-size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int dtype, int quantised);
+/* Workspace bytes of fa_paged_fwd_ex (quantised: with K_exp and V_exp); 0 for arguments it refuses.  A
+ * call with 512 rows (tokens x H / H_kv) or more per request over an 8-bit cache copies the rows it
+ * reads to the workspace in `dtype`: room for N * max_pages * page_size tokens, up to 2 GB each of K and
+ * V; where it would be more, and otherwise, the rows are converted in the kernel. */
+size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int max_pages, int dtype,
+                                   int quantised);
 
 /*
  * fa_page_slots -- pages and slots of a step's new tokens, on the device.
