@@ -165,14 +165,20 @@ def _setup(seed, new, ctx, H, H_kv, d, page, dtype, spread=3):
     return Q, (Kc, Vc), (Ke, Ve), table.cuda(), torch.tensor(total, dtype=torch.int32).cuda()
 
 
-def _check(O, LSE, Q, caches, exps, table, new, total, dtype, causal=True, window=0):
+def _check(O, LSE, Q, caches, exps, table, new, total, dtype, causal=True, window=0, p_step=0.0):
+    """p_step: by how much a P is off at most where that is more than u P; with the row sum at least 1 it moves
+    O by p_step times the sum of |V| over the keys that the row sees."""
     page, d = caches[0].shape[1], Q.shape[2]
     vals = [dr.values(c, e) for c, e in zip(caches, exps)]
     a = 0
     for i, (nq, nk) in enumerate(zip(new, total)):
         k, v = (ref.gather_pages(x, table[i].cpu(), nk, page) for x in vals)
         o, lse, mag, e = ref.attend(Q[a:a + nq].double().cpu(), k, v, causal, window, 1 / math.sqrt(d))
-        ref.check(f"O of request {i} ({nq} over {nk})", O[a:a + nq], o, mag, e, dtype)
+        size = torch.zeros_like(mag)
+        if p_step:
+            seen = torch.einsum("ij,jhc->ihc", ref.visible(nq, nk, causal, window).double(), v.abs())
+            size = seen.repeat_interleave(Q.shape[1] // v.shape[1], 1) * p_step / e
+        ref.check(f"O of request {i} ({nq} over {nk})", O[a:a + nq], o, mag, e, dtype, f32=mag + size)
         ref.check_lse(LSE[:, a:a + nq], lse, e)
         a += nq
 
