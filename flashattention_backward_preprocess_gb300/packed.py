@@ -427,29 +427,35 @@ def fa_paged_keep(path, count, cu_q, seq_lens, block_table, K_caches, V_caches, 
     q8 = K_exps is not None or V_exps is not None
     k0, v0 = K_caches[0], V_caches[0]
     pages, page, H_kv, d = _caches(k0, v0, _F8 if q8 else k0.dtype)
-    for name, first, ts in (("K_caches", k0, K_caches), ("V_caches", v0, V_caches)):
-        for t in ts:
-            _same(name, t, first.shape, first.dtype)
-            if t.stride() != first.stride():
-                _refuse(name, f"expected strides {first.stride()} in every layer, got {t.stride()}")
-    exps = []
+    index = path.get_device()
+
+    def pointers(name, ts, first):
+        """Device pointers of one tensor per layer, all of them like `first`."""
+        shape, dtype, stride = first.shape, first.dtype, first.stride()
+        out = (ctypes.c_void_p * layers)()
+        for n, t in enumerate(ts):
+            if t.shape != shape or t.dtype is not dtype or t.stride() != stride:
+                _refuse(name, f"expected {dtype} {tuple(shape)} with strides {stride} in every layer, got {t.dtype} "
+                              f"{tuple(t.shape)} with {t.stride()}")
+            if t.get_device() != index:
+                _refuse("tensors", f"expected one device, got {path.device} and {t.device}")
+            out[n] = t.data_ptr()
+        return out
+
+    kp, vp = pointers("K_caches", K_caches, k0), pointers("V_caches", V_caches, v0)
+    kx = vx = None
     if q8:
         if K_exps is None or V_exps is None or len(K_exps) != layers or len(V_exps) != layers:
             _refuse("K_exps", "an 8-bit cache has exponents for both K and V of every layer")
-        for a, b in zip(K_exps, V_exps):
-            _exps(a, b, k0.shape)
-        exps = [*K_exps, *V_exps]
+        _exps(K_exps[0], V_exps[0], k0.shape)
+        kx, vx = pointers("K_exps", K_exps, K_exps[0]), pointers("V_exps", V_exps, V_exps[0])
     dt = 0 if q8 else _type(k0)
-    dev = _device(path, count, cu_q, seq_lens, block_table, *K_caches, *V_caches, *exps)
-
-    def pointers(ts):
-        return (ctypes.c_void_p * layers)(*[t.data_ptr() for t in ts])
+    dev = _device(path, count, cu_q, seq_lens, block_table)
 
     def body(st):
         _check(load_library().fa_paged_keep(
             path.data_ptr(), count.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-            pointers(K_caches), pointers(V_caches), pointers(K_exps) if q8 else None, pointers(V_exps) if q8 else None,
-            layers, N, T, pages, page, cols, H_kv, d,
+            kp, vp, kx, vx, layers, N, T, pages, page, cols, H_kv, d,
             None if k0.is_contiguous() and v0.is_contiguous() else _strides(("K_caches", k0), ("V_caches", v0)), dt, st))
         return K_caches, V_caches
 
