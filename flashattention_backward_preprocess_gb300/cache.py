@@ -67,7 +67,7 @@ class PagedKVCache:
             self.lens, cu_q, self.block_table, self.free_pages, self.free_start, self.page_size, tokens)
         self.tree = None
         if parents is not None:
-            words = max(-(-int(tokens) // 64), 1) if words is None else words
+            words = min(max(-(-int(tokens) // 64), 1), 1024) if words is None else words
             self.tree, self.positions = packed.fa_tree_mask(parents, cu_q, self.lens, words)
         # in place: the replays of a captured step go on from where the last one ended
         torch._foreach_copy_([self.lens, self.free_start], [lens, start])

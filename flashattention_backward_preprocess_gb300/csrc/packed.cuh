@@ -47,7 +47,7 @@ struct PackedFwd {
     bool q8() const { return k_exp != nullptr; }
 };
 
-// Value of an exponent byte, 2^(b - 127).  (0 stands for 0; fa_paged_write_q8 writes 97 to 157.)
+// Value of an exponent byte, 2^(b - 127).  (0 comes with zeros alone; fa_paged_write_q8 writes 97 to 157.)
 __device__ __forceinline__ float exp_value(uint8_t b) { return __uint_as_float((unsigned)b << 23); }
 
 // Whether the new token in row `tok` of Q sees its request's k-th new token, k >= 0.

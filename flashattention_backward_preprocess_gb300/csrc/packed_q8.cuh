@@ -16,8 +16,9 @@
 // warps for K and four for V load the numbers into registers, each piece as soon as the one before it
 // in its place is converted, and store the operands.
 // Rows that are no key of the request (behind its last, before its window, on no page) are zeros.
-// Numbers on their way to registers cost no shared memory: its bandwidth is what bounds a tile (64 KB
-// of operands written, 96 KB of them and of Q read by the products, at 128 bytes a cycle).
+// A tile takes about 4500 cycles, of which no unit fills half (the products 1300, conversions 500, shared
+// memory's bandwidth 1300): the hand-overs between the roles do.  Staging the numbers in shared memory by
+// asynchronous copies first took as long.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -265,8 +266,9 @@ __device__ __forceinline__ void convert_tiles(const PackedFwd& a, uint8_t* smem,
     for (int jg = 0; more; ++jg) {
         const int s = jg % C::INFO, slot = jg % C::KST;
         const uint32_t w0 = words[s * 2].x, w1 = words[s * 2 + 1].x, l0 = words[s * 2].y, l1 = words[s * 2 + 1].y;
-        // the largest exponents (V's at least 1: 2^-ev is a number), and whether any is far below them
-        const uint32_t mk = max(w0 & 0xff, w1 & 0xff), mv = max(max(w0 >> 8 & 0xff, w1 >> 8 & 0xff), 1u);
+        // the largest exponents, and whether any is far below them.  Of a tile of exponents 0, zeros alone,
+        // V's is as good as any: 127 keeps P 2^ev in fp32's range
+        const uint32_t mk = max(w0 & 0xff, w1 & 0xff), mv0 = max(w0 >> 8 & 0xff, w1 >> 8 & 0xff), mv = mv0 ? mv0 : 127u;
         const int largest = (int)(is_v ? mv : mk);
         const bool far = (int)min(l0 >> sh & 0xff, l1 >> sh & 0xff) + 14 < largest;
         if (!is_v && t == 0) *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4) = mk | mv << 8;

@@ -138,3 +138,28 @@ def test_two_streams_at_once():
     for w, g in zip(want, got):
         for o, lse in g:
             assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("dtype,H,H_kv,d,page,new", [
+    ("bf16", 8, 2, 128, 16, [1] * 60), ("f16", 4, 2, 64, 16, [1, 2]), ("bf16", 8, 2, 128, 16, [30, 20]), ("f16", 4, 1, 128, 24, [1, 1]),
+    ("bf16", 8, 1, 128, 16, [100, 80]), ("f32", 4, 2, 64, 16, [1, 3]), ("bf16", 4, 2, 256, 64, [1, 2]),
+])
+def test_pages_outside_the_cache_read_as_zeros(dtype, H, H_kv, d, page, new):
+    """Keys without a page keep their place in the softmax, as keys of 0 with values of 0; so do the rows of a
+    cleared cache, whose exponents are 0."""
+    dt, ctx = DT[dtype], [(29 * i) % 70 + 300 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(9, new, ctx, H, H_kv, d, page, dt)
+    # request 0: a cleared page; request 1: pages outside the cache, one of them a whole tile of 128 keys long
+    cleared = int(table[0, 1])
+    for c, e in zip(caches, exps):
+        c.view(torch.uint8)[cleared] = 0
+        e[cleared] = 0
+    gone = list(range(128 // page, 256 // page + 1))
+    bad = table.clone()
+    bad[1, gone] = torch.tensor([-1 if i % 2 else caches[0].shape[0] + i for i in gone], dtype=torch.int32).cuda()
+    O, LSE = fa.fa_paged_fwd(Q, *caches, bad, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
+    assert "page" in _errors()
+    want = [c.clone() for c in caches]
+    for c, e in zip(want, exps):
+        c.view(torch.uint8)[table[1, gone].long()] = 0
+    _check(O, LSE, Q, want, exps, table, new, lens.tolist(), dt)
