@@ -23,8 +23,8 @@
 // item is cut into as many parts as CTAs share it, and whoever joins the parts reads them all.
 //
 // Bound by instructions (520 per warp and 16 keys, 0.4 a cycle and scheduler), then DRAM.  Measured in a
-// replayed graph, bf16, H = 32, H_kv = 8, d = 128: 64 requests, one token each, over 0.57 GB of cache 145
-// us (4.0 TB/s); one token of f16, H = 16, H_kv = 2, over 131072 keys 63 us; over 1024 keys 20 us.
+// replayed graph, bf16, H = 32, H_kv = 8, d = 128: 64 requests, one token each, over 0.57 GB of cache 141
+// us (4.1 TB/s); one token of f16, H = 16, H_kv = 2, over 131072 keys 63 us; over 1024 keys 20 us.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int RT = 16;  // rows of a tile; its keys: 16 per warp
 // Warps of a CTA, CTAs per SM and stages of the ring: many items, few items
-constexpr int kManyWarps = 4, kManyCtas = 3, kManyStages = 4;
+constexpr int kManyWarps = 4, kManyCtas = 3, kManyStages = 3;
 constexpr int kFewWarps = 12, kFewCtas = 1, kFewStages = 4;
 constexpr float kLift = 8.f, kRoom = 15.f;
 
@@ -338,19 +338,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
             const bool live = there & 1u;
             cp_async_wait<kStages - 2>();
             __syncwarp();  // also: every lane is done with the stage that is filled next
-            {
+            const uint8_t* stage = ring_p + st * kB;
+            const int fill = st == 0 ? kStages - 1 : st - 1;
+            st = st == kStages - 1 ? 0 : st + 1;
+            auto refill = [&]() {
                 const int jn = j + kStages - 1, pg = page_at(next);
                 next = entry_of(jn + 1);
                 there >>= 1;
                 if (pg >= 0) {
-                    fetch(jn, pg, st == 0 ? kStages - 1 : st - 1);
+                    fetch(jn, pg, fill);
                     there |= 1u << (kStages - 2);
                 }
                 cp_async_commit();
+            };
+            if (!live) {
+                refill();
+                continue;
             }
-            const uint8_t* stage = ring_p + st * kB;
-            st = st == kStages - 1 ? 0 : st + 1;
-            if (!live) continue;
             // ---- scores of 16 rows and 16 keys
             float c[2][4];
 #pragma unroll
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
                     }
                 }
             }
+            refill();  // here, not before the products: 141 us against 152 for the 64 requests above
             // exponents of keys 2t, 2t + 1, 2t + 8, 2t + 9
             const uint16_t* ex = reinterpret_cast<const uint16_t*>(stage + kEOff) + t;
             const uint32_t ek0 = ex[0] | (uint32_t)ex[4] << 16;
