@@ -60,8 +60,8 @@ class PagedKVCache:
 
         parents (int32 [tokens]): each request's new tokens are a tree, token i following the token
         parents[i] of the same request (an earlier one, counted from its first new token) or, at -1,
-        the cached ones; its position counts its ancestors.  words: 64 tokens of the largest tree
-        each (as many as the step's tokens may need unless given)."""
+        the cached ones; its position counts its ancestors (attend() takes no window then).  words:
+        64 tokens of the largest tree each (as many as the step's tokens may need unless given)."""
         self.cu_q = cu_q
         self.slots, self.positions, lens, start = packed.fa_page_slots(
             self.lens, cu_q, self.block_table, self.free_pages, self.free_start, self.page_size, tokens)

@@ -163,3 +163,14 @@ def test_pages_outside_the_cache_read_as_zeros(dtype, H, H_kv, d, page, new):
     for c, e in zip(want, exps):
         c.view(torch.uint8)[table[1, gone].long()] = 0
     _check(O, LSE, Q, want, exps, table, new, lens.tolist(), dt)
+
+
+@pytest.mark.parametrize("dtype,H,H_kv,d,page,N,n", [("bf16", 4, 1, 64, 16, 1000, 1), ("f16", 4, 2, 128, 32, 950, 2), ("bf16", 4, 1, 64, 16, 900, 9)])
+def test_more_requests_than_a_cta_plans_for(dtype, H, H_kv, d, page, N, n):
+    """Hundreds of requests: the plan is a kernel of its own."""
+    dt = DT[dtype]
+    new, ctx = [n if i % 9 else 0 for i in range(N)], [(7 * i) % 90 for i in range(N)]
+    Q, caches, exps, table, lens = _setup(4, new, ctx, H, H_kv, d, page, dt)
+    O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
+    assert _errors() == ""
+    _check(O, LSE, Q, caches, exps, table, new, lens.tolist(), dt)
