@@ -529,7 +529,10 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                     // K = K' 2^ek, V = V' 2^ev of the tile's operands K', V': the scores take 2^ek, and the
                     // exponentials, which stand for P 2^ev, ev
                     const uint32_t top = *reinterpret_cast<volatile const uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4);
-                    scale_tile = scale_row * __uint_as_float((top & 0xffu) << 23);
+                    // never 0, which would make NaN of the -inf of masked scores: not for a tile whose keys are
+                    // all zeros (ek is 0 - 127 then, and no float's), nor where the product falls below the
+                    // normal numbers (every score rounds to 0 either way)
+                    scale_tile = fmaxf(scale_row * __uint_as_float((top & 0xffu) << 23), 1.17549435e-38f);
                     v_exp = (float)((int)(top >> 8) - 127);
                     v_unit = __uint_as_float((254u - (top >> 8)) << 23);  // 2^-ev
                 }
