@@ -40,8 +40,9 @@ constexpr int kManyWarps = 4, kManyCtas = 3, kManyStages = 3;
 constexpr int kFewWarps = 12, kFewCtas = 1, kFewStages = 4;
 constexpr float kLift = 8.f, kRoom = 15.f;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
+// The first `live` of 16 bytes, zeros behind them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8u : 0u) : "memory");
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
                     const bool in = q + 8 * i < left && x * 64 + t * 16 < a.d;
-                    cp_async16(dst + (x * 2 + i) * 512 + lane * 16, in ? pk + x * 64 : Kb, in);
+                    cp_async16(dst + (x * 2 + i) * 512 + lane * 16, in ? pk + x * 64 : Kb, in ? 16u : 0u);
                 }
                 pk += 8 * a.k.tok;
             }
@@ -304,15 +305,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
                 const bool in = r < left && q * CH < a.d;
                 const uint32_t to = dst + kVOff + (n * 32 + lane) * CH;
                 if constexpr (CH == 16)
-                    cp_async16(to, in ? pv : Vb, in);
+                    cp_async16(to, in ? pv : Vb, in ? 16u : 0u);
                 else
                     cp_async8(to, in ? pv : Vb, in);
                 pv += n == 1 ? 7 * a.v.tok : a.v.tok;
             }
-            if (lane < 2) {
+            if (lane < 2) {  // bytes behind the last key may be anything, 255 (no float's exponent) too: zeros
                 const long long e = ((long long)pg * a.H_kv + w.hd) * a.page_size + in0;
                 const uint8_t* exps = lane ? a.v_exp : a.k_exp;
-                cp_async16(dst + kEOff + lane * 16, pg < a.pages ? exps + e : exps, pg < a.pages);
+                cp_async16(dst + kEOff + lane * 16, pg < a.pages ? exps + e : exps, (uint32_t)min(max(left, 0), 16));
             }
         };
         float o[CH][4];

@@ -88,3 +88,21 @@ def test_tiny_scale(kernel, scale):
         ref.check(f"O of request {i}", O[a:a + nq], o, mag, e, dt)
         ref.check_lse(LSE[:, a:a + nq], lse, e)
         a += nq
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 20), (False, 0)])
+def test_bytes_that_nobody_has_written(kernel, causal, window):
+    """Exponents of 255 and numbers of NaN in every slot that holds no key, those behind a last key among them."""
+    dtype, H, H_kv, d, page, new = KERNELS[kernel]
+    dt, ctx = DT[dtype], [(13 * i + 5) % 100 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(9, new, ctx, H, H_kv, d, page, dt)
+    held = torch.zeros(exps[0].shape[0], page, dtype=torch.bool)
+    for row, n in zip(table.cpu(), lens.tolist()):
+        j = torch.arange(n)
+        held[row.long()[j // page], j % page] = True
+    for e in exps:
+        e.masked_fill_(~held[:, None].cuda(), 255)
+    O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, causal=causal, window_size=window, K_exp=exps[0], V_exp=exps[1])
+    assert _errors() == ""
+    _check(O, LSE, Q, caches, exps, table, new, lens.tolist(), dt, causal, window, p_step=P_STEP.get(kernel, 0.0))
