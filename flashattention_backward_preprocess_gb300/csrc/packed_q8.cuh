@@ -34,6 +34,8 @@ namespace {
 constexpr uint32_t kInfoValid = 1u << 16;  // there is such a tile
 constexpr uint32_t kInfoFirst = 1u << 17;  // it is the first of its item
 
+constexpr uint32_t kMinExp = 97;  // smallest exponent byte of a row that was written
+
 // 16 bytes that this kernel reads once.
 __device__ __forceinline__ uint4 ld_once(const void* p) {
     uint4 v;
@@ -267,8 +269,9 @@ __device__ __forceinline__ void convert_tiles(const PackedFwd& a, uint8_t* smem,
         const int s = jg % C::INFO, slot = jg % C::KST;
         const uint32_t w0 = words[s * 2].x, w1 = words[s * 2 + 1].x, l0 = words[s * 2].y, l1 = words[s * 2 + 1].y;
         // the largest exponents, and whether any is far below them.  Of a tile of exponents 0, zeros alone,
-        // V's is as good as any: 127 keeps P 2^ev in fp32's range
-        const uint32_t mk = max(w0 & 0xff, w1 & 0xff), mv0 = max(w0 >> 8 & 0xff, w1 >> 8 & 0xff), mv = mv0 ? mv0 : 127u;
+        // V's is the smallest there is: a larger one would lift the softmax's reference above tiles whose
+        // values count and cost their P its bits
+        const uint32_t mk = max(w0 & 0xff, w1 & 0xff), mv = max(max(w0 >> 8 & 0xff, w1 >> 8 & 0xff), kMinExp);
         const int largest = (int)(is_v ? mv : mk);
         const bool far = (int)min(l0 >> sh & 0xff, l1 >> sh & 0xff) + 14 < largest;
         if (!is_v && t == 0) *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4) = mk | mv << 8;

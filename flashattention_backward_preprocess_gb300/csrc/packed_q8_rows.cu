@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
             const uint16_t* ex = reinterpret_cast<const uint16_t*>(stage + kEOff) + t;
             const uint32_t ek0 = ex[0] | (uint32_t)ex[4] << 16;
             uint32_t ev0 = ex[8] | (uint32_t)ex[12] << 16;
-            // an exponent 0, zeros alone, is as good as any: 127 keeps P' and its sum in fp32's range
-            ev0 |= __vcmpeq4(ev0, 0u) & 0x7f7f7f7fu;
+            // an exponent 0 comes with zeros alone: the smallest there is, for a larger one would lift m above
+            // the keys whose values count and cost their P' its bits
+            ev0 |= __vcmpeq4(ev0, 0u) & (kMinExp * 0x01010101u);
             // ---- weights.  c[i][2h + b]: row q + 8h, key 8i + 2t + b
             {
                 const bool full = key0 >= all_lo && key0 + 16 <= all_hi;

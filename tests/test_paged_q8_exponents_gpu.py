@@ -106,3 +106,22 @@ def test_bytes_that_nobody_has_written(kernel, causal, window):
     O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, causal=causal, window_size=window, K_exp=exps[0], V_exp=exps[1])
     assert _errors() == ""
     _check(O, LSE, Q, caches, exps, table, new, lens.tolist(), dt, causal, window, p_step=P_STEP.get(kernel, 0.0))
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tiles", "tiles_256", "copy", "simt"])
+@pytest.mark.parametrize("exponent", [97, 142, 157])
+def test_zeros_beside_values_of_one_size(kernel, exponent):
+    """Cleared pages and pages outside the cache beside values that are all small, or all large: the zeros do not
+    cost the others' weights their bits."""
+    dtype, H, H_kv, d, page, new = KERNELS[kernel]
+    dt, ctx = DT[dtype], [(29 * i) % 70 + 300 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(9, new, ctx, H, H_kv, d, page, dt)
+    exps[1].fill_(exponent)
+    asked = table.clone()
+    for n in range(len(new)):
+        for col in [1, 3, *range(128 // page, 256 // page)]:  # two pages of a tile, and a whole one
+            _zero(caches, exps, int(table[n, col]))
+        asked[n, 3] = -1
+    O, LSE = fa.fa_paged_fwd(Q, *caches, asked, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
+    assert "page" in _errors()
+    _check(O, LSE, Q, caches, exps, table, new, lens.tolist(), dt)
