@@ -91,19 +91,20 @@ struct PCfg {
     static constexpr uint32_t OFF_ROW = OFF_V + VST * kTileKV_B;
     static constexpr uint32_t OFF_XCH = OFF_ROW + 2 * BM * 8;
     // 8-bit caches.  Of a looked-up tile: where its rows lie in K and in V, their exponents, words of
-    // both halves; its largest exponents for the softmax (8 slots); of an item's rows: the inverse of
-    // the power of two that Q was scaled by (4 slots)
+    // both halves; for the softmax its largest exponents and, where they are needed, all of them (8 slots
+    // each); of an item's rows: the inverse of the power of two that Q was scaled by (4 slots)
     static constexpr uint32_t OFF_AT = OFF_XCH + BM * 4;
     static constexpr uint32_t OFF_EXP = OFF_AT + INFO * BN * 16;
     static constexpr uint32_t OFF_INFO = OFF_EXP + INFO * BN * 2;
     static constexpr uint32_t OFF_TOP = OFF_INFO + INFO * 16;
     static constexpr uint32_t OFF_QS = OFF_TOP + (kQ8 ? 32 : 0);
-    static constexpr uint32_t OFF_BAR = OFF_QS + (kQ8 ? 4 * BM * 4 : 0);
+    static constexpr uint32_t OFF_FAR = OFF_QS + (kQ8 ? 4 * BM * 4 : 0);
+    static constexpr uint32_t OFF_BAR = OFF_FAR + (kQ8 ? 8 * BN * 2 : 0);
     // V(j)'s slot is past V(j - VST) once S(j) is complete (the softmax warps' rare waits for V)
     static_assert(kQ8 || VST >= NBUF, "see above");
     // what the softmax reads of a tile's or item's slot is read before the slot is written again
     static_assert(!kQ8 || KST + NBUF < 8, "see above");
-    static_assert(OFF_AT % 16 == 0 && OFF_INFO % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
+    static_assert(OFF_AT % 16 == 0 && OFF_INFO % 8 == 0 && OFF_FAR % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
     static constexpr uint32_t TM_S = 0, TM_O = 128 * NBUF;
     static_assert(TM_O + D <= 512, "TMEM columns");
 };
@@ -176,6 +177,52 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
+}
+
+// A thread's N scores of a far tile (packed_q8.cuh), in TMEM from `buf` on: the operands hold K's and V's numbers
+// as they are, so a key's own exponents go to its score and to its P.  exps: the keys' exponent bytes, K's in
+// the low ones.
+// Scores s to y = scale 2^ek s + ev, -inf in the columns without see(column); returns the largest.
+template <int N, typename See>
+__device__ __forceinline__ float far_scores(uint32_t buf, const uint16_t* exps, float scale, See see) {
+    float most = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < N; c += 32) {
+        uint32_t y[32];
+        ptx::tmem_ld32p(buf + c, y);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t e = exps[c + i];
+            const float ev = (float)((int)max(e >> 8, kMinExp) - 127);
+            const float x = fmaf(__uint_as_float(y[i]), scale * __uint_as_float((e & 0xff) << 23), ev);
+            y[i] = __float_as_uint(see(c + i) ? x : -INFINITY);
+            most = fmaxf(most, __uint_as_float(y[i]));
+        }
+        ptx::tmem_st32(buf + c, y);
+    }
+    ptx::tmem_wait_st();
+    return most;
+}
+// y to P 2^ev = 2^(y - m), packed into the first half of the columns; returns the sum of P.
+template <int N, bool kBF16>
+__device__ __forceinline__ float far_weights(uint32_t buf, const uint16_t* exps, float m) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < N; c += 32) {
+        uint32_t y[32], p[16];
+        ptx::tmem_ld32p(buf + c, y);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float p0 = ptx::ex2(__uint_as_float(y[i]) - m), p1 = ptx::ex2(__uint_as_float(y[i + 1]) - m);
+            sum = fmaf(p0, __uint_as_float((254u - max((uint32_t)exps[c + i] >> 8, kMinExp)) << 23), sum);
+            sum = fmaf(p1, __uint_as_float((254u - max((uint32_t)exps[c + i + 1] >> 8, kMinExp)) << 23), sum);
+            p[i / 2] = pack2<kBF16>(p0, p1);
+        }
+        ptx::tmem_st16(buf + c / 2, p);
+    }
+    return sum;
 }
 
 // 32 bytes per thread (32-byte aligned): a row per thread makes every store of a warp touch 32
@@ -522,6 +569,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                     if (treed) see = tree_columns<HN>(sees, a.tree_words, n0 + hf * HN - ctx);
                 wait_bar_warp(bar(P_S0 + jg % NB), (jg / NB) & 1, abort_flag, err);
                 [[maybe_unused]] float scale_tile = 0.f, v_exp = 0.f, v_unit = 1.f;
+                [[maybe_unused]] bool far = false;
                 if constexpr (kQ8) {
                     // what Q's row was multiplied by is taken out of the scores again
                     if (kConvQ && j == 0)
@@ -533,8 +581,9 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                     // all zeros (ek is 0 - 127 then, and no float's), nor where the product falls below the
                     // normal numbers (every score rounds to 0 either way)
                     scale_tile = fmaxf(scale_row * __uint_as_float((top & 0xffu) << 23), 1.17549435e-38f);
-                    v_exp = (float)((int)(top >> 8) - 127);
-                    v_unit = __uint_as_float((254u - (top >> 8)) << 23);  // 2^-ev
+                    v_exp = (float)((int)(top >> 8 & 0xffu) - 127);
+                    v_unit = __uint_as_float((254u - (top >> 8 & 0xffu)) << 23);  // 2^-ev
+                    far = (top & kTopFar) != 0;
                 }
                 if (!kQ8 && k_live < BN) {
                     // V rows behind the last key: zeros, once the loads have landed
@@ -591,27 +640,8 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                         const float2 s2 = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
                         sum = s2.x + s2.y;
                     };
-                    bool done = false;
-                    // both threads of a row have the same m, so both warps decide alike
-                    if (j > 0 && !__any_sync(0xffffffffu, row_valid && m_run == -INFINITY)) {
-                        uint32_t r[HN];
-                        load(r);
-                        exps(r);
-                        __syncwarp();
-                        done = ptx::named_bar_and(pair, 64, !(row_valid && sum > (kQ8 ? kQ8MaxSum : kMaxSum)));
-                    }
-                    if (!done) {
-                        uint32_t r[HN];
-                        load(r);
-                        float mx8[8];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
-#pragma unroll
-                        for (int c = 0; c < HN; c += 2)
-                            mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-                        float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-                        // the max of both halves, by way of the second half's thread
+                    // the max of both halves, by way of the second half's thread
+                    auto both_halves = [&](float mx) {
                         if (hf == 1) *xch = mx;
                         __syncwarp();
                         ptx::named_bar_sync(pair, 64);
@@ -619,17 +649,50 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
                         __syncwarp();
                         ptx::named_bar_sync(pair, 64);
                         if (hf == 1) mx = *xch;
-                        mx = mx == -INFINITY ? -INFINITY : kQ8 ? fmaf(mx, scale_tile, v_exp - kQ8Lift) : mx * scale_log2;
+                        return mx;
+                    };
+                    auto refer_to = [&](float mx) {
                         rescale = mx > m_run;
                         if (rescale) {
                             alpha = m_run == -INFINITY ? 0.f : ptx::ex2(m_run - mx);
                             m_run = mx;
                         }
-                        exps(r);
-                    }
-                    l_run = l_run * alpha + (kQ8 ? sum * v_unit : sum);
+                    };
+                    if (kQ8 && far) {
+                        const uint16_t* own = reinterpret_cast<const uint16_t*>(smem + C::OFF_FAR) + (jg & 7) * BN + hf * HN;
+                        refer_to(both_halves(far_scores<HN>(buf, own, scale_row, [&](int c) {
+                                     return (unsigned)(c - c_lo) < c_span && (!treed || (see >> c & 1ull));
+                                 })) - kQ8Lift);
+                        l_run = l_run * alpha + far_weights<HN, kOpBF16>(buf, own, m_run == -INFINITY ? 0.f : m_run);
+                    } else {
+                        bool done = false;
+                        // both threads of a row have the same m, so both warps decide alike
+                        if (j > 0 && !__any_sync(0xffffffffu, row_valid && m_run == -INFINITY)) {
+                            uint32_t r[HN];
+                            load(r);
+                            exps(r);
+                            __syncwarp();
+                            done = ptx::named_bar_and(pair, 64, !(row_valid && sum > (kQ8 ? kQ8MaxSum : kMaxSum)));
+                        }
+                        if (!done) {
+                            uint32_t r[HN];
+                            load(r);
+                            float mx8[8];
 #pragma unroll
-                    for (int c = 0; c < HN / 2; c += 16) ptx::tmem_st16(buf + c, *reinterpret_cast<uint32_t(*)[16]>(Pp + c));
+                            for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < HN; c += 2)
+                                mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                            float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                             fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                            mx = both_halves(mx);
+                            refer_to(mx == -INFINITY ? -INFINITY : kQ8 ? fmaf(mx, scale_tile, v_exp - kQ8Lift) : mx * scale_log2);
+                            exps(r);
+                        }
+                        l_run = l_run * alpha + (kQ8 ? sum * v_unit : sum);
+#pragma unroll
+                        for (int c = 0; c < HN / 2; c += 16) ptx::tmem_st16(buf + c, *reinterpret_cast<uint32_t(*)[16]>(Pp + c));
+                    }
                     // rescale the O row before the next P V product accumulates into it (each
                     // thread half of the columns)
                     if (j > 0 && __any_sync(0xffffffffu, rescale)) {

@@ -6,9 +6,14 @@
 //   K' = number * 2^(e - E),  so K = K' 2^E,  V alike,
 // so the softmax needs one factor per tile instead of one per key: 2^E_k goes into the scale of the
 // scores, E_v into the exponent of P (P' = P 2^E_v), and the row sum takes 2^-E_v of a tile's sum.
-// A number times a power of two is exact in fp16 down to 2^-24, so only rows whose values lie below
-// 2^-33 of the tile's largest number lose bits.  fp16 is the operand type for bf16 queries as well
-// (an e4m3 pair is one conversion away from fp16, five instructions from bf16): a row of Q is scaled
+// A number times a power of two is exact in fp16 down to 2^-24, so 2^(e - E) loses nothing from
+// 2^-14 on (e4m3 starts at 2^-9).  A tile with an exponent further below its largest ("far") keeps its
+// numbers as they are, and the softmax takes each key's own exponents to its score and its P (far_scores,
+// far_weights in packed_fwd_tc.cuh): one row far larger than the rest, which may be hidden or without
+// weight, would otherwise cost all others their bits.  The 32 trees of packed_q8.cu take 481 us with such
+// a row in every tile, 261 without.
+// fp16 is the operand type for bf16 queries as well (an e4m3 pair is one conversion away from fp16, five
+// instructions from bf16): a row of Q is scaled
 // by a power of two to a largest magnitude in [2^14, 2^15), which leaves bf16 numbers exact down to
 // 2^-31 of it, and P has 11 bits instead of 8.
 //
@@ -29,10 +34,12 @@
 namespace fa {
 namespace {
 
-// Words of half a looked-up tile: largest exponents of K and V in the low bytes and these bits;
+// Words of half a looked-up tile: largest exponents of K and V in the low bytes and the first two bits;
 // smallest exponents (of those that are not 0).
 constexpr uint32_t kInfoValid = 1u << 16;  // there is such a tile
 constexpr uint32_t kInfoFirst = 1u << 17;  // it is the first of its item
+
+constexpr uint32_t kTopFar = 1u << 16;     // with a tile's largest exponents: its keys' own ones are to be taken
 
 constexpr uint32_t kMinExp = 97;  // smallest exponent byte of a row that was written
 
@@ -55,12 +62,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// 2^n as two equal halves, n <= 0; 0 below fp16's range.
-__device__ __forceinline__ uint32_t half2_pow2(int n) {
-    const uint32_t h = n >= -14 ? (uint32_t)(n + 15) << 10 : n >= -24 ? 1u << (n + 24) : 0u;
-    return h | (h << 16);
-}
-
 // Row t of the Q tile (128-byte swizzled blocks of 64 bf16 columns) to fp16, scaled; returns the
 // inverse of the scale.
 template <typename C, int D>
@@ -204,20 +205,6 @@ __device__ __forceinline__ void look_up_tiles(const PackedFwd& a, const FwdShare
     }
 }
 
-// Of a tile with exponents more than 14 below the largest: the rest of the way for those rows.
-template <typename C, int N, int RSTEP>
-__device__ __forceinline__ void shrink_rows(uint8_t* out, int other, const uint16_t* rows, int sh, int largest) {
-#pragma unroll 1
-    for (int i = 0; i < N; ++i) {
-        const uint32_t f = half2_pow2(min((int)(rows[i * RSTEP] >> sh & 0xff) - largest + 14, 0));
-        for (int x = 0; x < 2; ++x) {
-            uint4* p = reinterpret_cast<uint4*>(out + i * RSTEP * 128 + x * other);
-            const uint4 h = *p;
-            *p = make_uint4(hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
-        }
-    }
-}
-
 // The eight converting warps.  A timeout leaves the loop of every warp alike: they share no barrier
 // but those with bounded waits.
 template <typename C, int D, bool kConvQ>
@@ -268,13 +255,17 @@ __device__ __forceinline__ void convert_tiles(const PackedFwd& a, uint8_t* smem,
     for (int jg = 0; more; ++jg) {
         const int s = jg % C::INFO, slot = jg % C::KST;
         const uint32_t w0 = words[s * 2].x, w1 = words[s * 2 + 1].x, l0 = words[s * 2].y, l1 = words[s * 2 + 1].y;
-        // the largest exponents, and whether any is far below them.  Of a tile of exponents 0, zeros alone,
+        // the largest exponents, and whether any is far below them (in K or in V: both are left as they are then).  Of a tile of exponents 0, zeros alone,
         // V's is the smallest there is: a larger one would lift the softmax's reference above tiles whose
         // values count and cost their P its bits
         const uint32_t mk = max(w0 & 0xff, w1 & 0xff), mv = max(max(w0 >> 8 & 0xff, w1 >> 8 & 0xff), kMinExp);
         const int largest = (int)(is_v ? mv : mk);
-        const bool far = (int)min(l0 >> sh & 0xff, l1 >> sh & 0xff) + 14 < largest;
-        if (!is_v && t == 0) *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4) = mk | mv << 8;
+        const bool far = min(l0 & 0xff, l1 & 0xff) + 14 < mk || min(l0 >> 8 & 0xff, l1 >> 8 & 0xff) + 14 < mv;
+        if (!is_v && t == 0)
+            *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TOP + (jg & 7) * 4) = mk | mv << 8 | (far ? kTopFar : 0u);
+        if (far && !is_v && t < BN)
+            reinterpret_cast<uint16_t*>(smem + C::OFF_FAR)[(jg & 7) * BN + t] =
+                reinterpret_cast<const uint16_t*>(smem + C::OFF_EXP)[s * BN + t];
         if (kConvQ && !is_v && (w0 & kInfoFirst)) {
             if (!wait_bar_warp(bars.q_full, ka & 1, abort_flag, err)) break;
             reinterpret_cast<float*>(smem + C::OFF_QS)[(ka & 3) * 128 + t] = convert_q_row<C, D>(smem + C::OFF_Q, t);
@@ -287,11 +278,12 @@ __device__ __forceinline__ void convert_tiles(const PackedFwd& a, uint8_t* smem,
         if (jg >= C::KST && !wait_bar_warp(empty + 8u * slot, (jg / C::KST - 1) & 1, abort_flag, err)) break;
         uint8_t* out = smem + ring + slot * C::kTileKV_B + out0;
         const uint16_t* rows = exps + s * BN;
+        const int least = far ? 15 : 1;  // f is 2^by, 2^-14 at least (less than that: zeros); 1 in a far tile
         const long long* from = at + (jg + 1) % C::INFO * BN * 2;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int by = (int)(rows[i * RSTEP] >> sh & 0xff) - largest;  // <= 0
-            const uint32_t f = (uint32_t)max(by + 15, 1) * 0x04000400u;    // 2^by, 2^-14 at least
+            const uint32_t f = (uint32_t)max(by + 15, least) * 0x04000400u;
             uint32_t h[8];
             e4m3x4_to_f16(q[i].x, h[0], h[1]);
             e4m3x4_to_f16(q[i].y, h[2], h[3]);
@@ -306,7 +298,6 @@ __device__ __forceinline__ void convert_tiles(const PackedFwd& a, uint8_t* smem,
             *reinterpret_cast<uint4*>(line) = odd_first ? ho : he;
             *reinterpret_cast<uint4*>(line + other) = odd_first ? he : ho;
         }
-        if (far) shrink_rows<C, N, RSTEP>(out, other, rows, sh, largest);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

@@ -302,8 +302,10 @@ size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page
  * A row that sees nothing gets O = 0 and LSE = -inf.  F16/BF16 run tensor-core kernels, over an 8-bit
  * cache with any page_size; F32 and wider head groups than 128 an FFMA kernel.  Where rows of an 8-bit
  * cache are not copied they are fp16 operands, and so is Q after a scaling of each row by a power of two
- * (exact down to 2^-31 of the row's largest element for BF16) and P: its 11 bits, with a fixed step of
- * 2^-33 of the row's largest weight at the small end.  The result is bitwise reproducible.
+ * (exact down to 2^-31 of the row's largest element for BF16) and P: its 11 bits, with a fixed step at the
+ * small end, 2^-33 of the row's largest product of a P and 2^e of its V (2^-19 of it where the exponents e
+ * of V differ inside a tile of keys).  Every key counts with its own exponents, whatever size those of other
+ * keys have.  The result is bitwise reproducible.
  */
 int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp,
                     void* O, float* LSE, const int* block_table, const int* cu_q, const int* seq_lens,

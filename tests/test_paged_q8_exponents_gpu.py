@@ -125,3 +125,117 @@ def test_zeros_beside_values_of_one_size(kernel, exponent):
     O, LSE = fa.fa_paged_fwd(Q, *caches, asked, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
     assert "page" in _errors()
     _check(O, LSE, Q, caches, exps, table, new, lens.tolist(), dt)
+
+
+def _check_rows(O, LSE, q, k, v, vis, scale, dtype, lift=4):
+    """packed_ref's bounds, of each row and head from the keys that it sees alone, and the fixed step of P.
+
+    A score is off by d 2^-23 scale sum |q k|, its P by the factor exp of that, x_j.  P is an fp16 operand P 2^ev,
+    ev the exponent of its key's V; the largest of them is 2^8 or more where numbers below 2^-14 are off by up to
+    2^-25: O by 2^-33 max_j(P_j 2^ev_j) sum_j |V_jc| 2^-ev_j.  With top_j = max_c |V_jc|, 224 2^ev_j < top_j <=
+    448 2^ev_j above the smallest exponent, so by 2^-32 max_j(P_j top_j) sum_j |V_jc| / top_j.  Where one factor
+    serves a tile of keys, it is up to 2^lift times theirs."""
+    nq, H, d = q.shape
+    g = H // k.shape[1]
+    for h in range(H):
+        kh, vh = k[:, h // g], v[:, h // g]
+        s = ((q[:, h] @ kh.T) * scale).masked_fill(~vis, -math.inf)
+        lse = torch.logsumexp(s, 1)
+        P = torch.exp(s - torch.where(lse == -math.inf, 0.0, lse)[:, None])
+        x = torch.expm1((d * ref.STEP * scale * (q[:, h].abs() @ kh.abs().T)).clamp(max=80.0))
+        e = len(kh) * ref.STEP + 2.0 ** -21
+        want, A = P @ vh, P @ vh.abs()
+        f32 = (P * x) @ vh.abs() + (P * x).sum(1, keepdim=True) * want.abs() + e * A
+        top = vh.abs().amax(1).clamp(min=2.0 ** -40)
+        f32 = f32 + 2.0 ** (lift - 32) * (P * top).amax(1, keepdim=True) * (vis.double() @ (vh.abs() / top[:, None]))
+        tol = ref.U[dtype] * (want.abs() + A + f32) * 1.001 + f32 + (2.0 ** -24 if dtype == torch.float16 else 1e-30)
+        worst = float(((O[:, h].double().cpu() - want).abs() / tol).max())
+        assert worst <= 1.0, f"O of head {h}: {worst:.3g} times its bound"  # NaN fails too
+        off = (LSE[h].double().cpu() - lse).abs() / ((P * x).sum(1) + e + 2.0 ** -22 * lse.abs())
+        assert float(off.max()) <= 1.0, f"LSE of head {h}: {float(off.max()):.3g} times its bound"
+
+
+def _check_requests(O, LSE, Q, caches, exps, table, lens, new, scale, dtype, sees=None, rows=lambda i: True, lift=4):
+    """_check_rows of every request, of its new tokens numbered i with rows(i)."""
+    vals, a = [dr.values(c, e) for c, e in zip(caches, exps)], 0
+    for n, (nq, nk) in enumerate(zip(new, lens.tolist())):
+        k, v = (ref.gather_pages(x, table[n].cpu(), nk, caches[0].shape[1]) for x in vals)
+        vis = ref.visible(nq, nk, True, 0)
+        if sees is not None:
+            vis[:, nk - nq:] = sees[n]
+        at = [i for i in range(nq) if rows(i)]
+        _check_rows(O[a:a + nq][at], LSE[:, a:a + nq][:, at], Q[a:a + nq][at].double().cpu(), k, v, vis[at], scale, dtype, lift)
+        a += nq
+
+
+FAR = ["rows", "rows_f16", "tiles", "tiles_f16", "tiles_64", "tiles_256", "tiles_f16_256", "copy", "simt"]
+
+
+@pytest.mark.parametrize("kernel", FAR)
+@pytest.mark.parametrize("which", ["K", "V", "KV"])
+@pytest.mark.parametrize("gap", [13, 16, 24, 34])
+def test_rows_far_larger_than_the_others_that_nobody_sees(kernel, which, gap):
+    """Drafted tokens whose K, V or both are 2^gap times everybody's and which none but themselves sees: the others'
+    results are as exact as without them."""
+    dtype, H, H_kv, d, page, new = KERNELS[kernel]
+    dt, ctx = DT[dtype], [(29 * i) % 70 + 120 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(9, new, ctx, H, H_kv, d, page, dt, spread=1)
+    ups, at = [], 0
+    for n, m in enumerate(new):
+        up, last = [], -1
+        for i in range(m):
+            up.append(last)
+            if i % 7 != 2:
+                last = i
+                continue
+            pg, row = int(table[n, (ctx[n] + i) // page]), (ctx[n] + i) % page
+            for name, e in zip("KV", exps):
+                if name in which:
+                    e[pg, :, row] = (e[pg, :, row].int() + gap).clamp(max=157).to(torch.uint8)
+            Q[at + i] = 0  # of what it sees itself every weight is alike
+        ups.append(up)
+        at += m
+    tree, _ = fa.fa_tree_mask(torch.tensor(sum(ups, []), **I32), _cu(new), torch.tensor(ctx, **I32), -(-max(new) // 64))
+    O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, tree=tree, K_exp=exps[0], V_exp=exps[1])
+    assert _errors() == ""
+    sees = [dr.ancestors(u)[0] for u in ups]
+    lift = 14 if gap < 15 else 4
+    for rows in (lambda i: i % 7 != 2, lambda i: i % 7 == 2):
+        if dtype != "f16" or rows(0):  # fp16 has no room for the large rows' own O
+            _check_requests(O, LSE, Q, caches, exps, table, lens, new, d ** -0.5, dt, sees, rows, lift)
+
+
+@pytest.mark.parametrize("kernel", FAR)
+@pytest.mark.parametrize("gap", [16, 30])
+def test_rows_far_larger_than_the_others_without_weight(kernel, gap):
+    """Cached rows of V 2^gap times the others', whose scores leave them no weight."""
+    dtype, H, H_kv, d, page, new = KERNELS[kernel]
+    dt, ctx = DT[dtype], [(29 * i) % 70 + 300 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(9, new, ctx, H, H_kv, d, page, dt, spread=1)
+    Q = -Q.abs()
+    for pg in table[:, [1, 9]].reshape(-1).tolist():
+        caches[0].view(torch.uint8)[pg, 5] = 0x7e  # 448 in every column
+        exps[0][pg, :, 5] = 123
+        exps[1][pg, :, 5] = (exps[1][pg, :, 5].int() + gap).clamp(max=157).to(torch.uint8)
+    O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
+    assert _errors() == ""
+    _check_requests(O, LSE, Q, caches, exps, table, lens, new, d ** -0.5, dt)
+
+
+@pytest.mark.parametrize("kernel", ["tiles", "tiles_64", "tiles_256", "copy", "simt", "rows"])
+def test_every_exponent_that_is_written(kernel):
+    """Exponents from end to end of what fa_paged_write_q8 writes, rows of zeros among them."""
+    dtype, H, H_kv, d, page, new = KERNELS[kernel]
+    dt, ctx = DT[dtype], [(29 * i) % 70 + 300 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(7, new, ctx, H, H_kv, d, page, dt, spread=0)
+    g = torch.Generator().manual_seed(1)
+    lo, hi = (112, 122) if dt == torch.float16 else (97, 157)
+    exps[1].copy_(torch.randint(lo, hi + 1, exps[1].shape, generator=g).to(torch.uint8))
+    exps[0].copy_(torch.randint(lo, 121, exps[0].shape, generator=g).to(torch.uint8))  # scores of moderate size
+    for c in caches:
+        c.view(torch.uint8)[c.view(torch.uint8) & 127 == 127] = 0
+    _zero(caches, exps, int(table[0, 2]))
+    Q = Q * 0.125
+    O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
+    assert _errors() == ""
+    _check_requests(O, LSE, Q, caches, exps, table, lens, new, d ** -0.5, dt, lift=14 if dt == torch.float16 else 4)
