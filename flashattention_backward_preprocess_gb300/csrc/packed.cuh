@@ -43,6 +43,10 @@ struct PackedFwd {
     // whether the new token in row t sees its request's k-th new token; null: plain causal
     const unsigned long long* tree;
     int tree_words;
+    // a word on the device that decides whether the tensor-core kernel computes anything: if it holds
+    // gate_value; null: always
+    const unsigned int* gate;
+    unsigned int gate_value;
     bool paged() const { return cu_k == nullptr; }
     bool q8() const { return k_exp != nullptr; }
 };

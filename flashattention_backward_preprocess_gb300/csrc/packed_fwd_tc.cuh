@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(PCfg<D, kQ8>::THREADS, 1)
     } else {
         share.read(plan, blockIdx.x);
     }
+    if (kPaged && a.gate != nullptr && __ldcg(a.gate) != a.gate_value) share.W = 0;  // another kernel's step
 
     // Every role walks the same segments.  Per-tile barrier phases count the key tiles of this
     // CTA (jg), per-item ones its segments with work (ka).

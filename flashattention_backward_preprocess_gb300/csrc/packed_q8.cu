@@ -5,7 +5,9 @@
 // conversion is what takes its time (about 4500 cycles of a 128-key tile; the products need 1300).
 // Where requests have many such tiles (chunks of prompts), one pass makes the rows of the cache that
 // the step reads fp16 or bf16, exactly, in pages of the workspace, and the kernel for caches of that
-// type does the rest.  10 chunks of up to 512 tokens over up to 8000 cached ones, H = 32, H_kv = 8, d =
+// type does the rest.  (Every row that fa_paged_write_q8 writes is a bf16 number; fp16 holds what was written
+// from fp16.  A row that it cannot hold is noticed by the copy, and the tensor-core kernel above does the step instead: one
+// more launch for fp16, 173 us in place of 162 for the chunks below.)  10 chunks of up to 512 tokens over up to 8000 cached ones, H = 32, H_kv = 8, d =
 // 128, bf16: 159 us (42 of them the copy of 54 MB) against 316.  32 trees of 8 to 64 tokens over 100 to
 // 6000, f16, in the converting kernel: 252 us; the copy alone would write 400 MB.
 #include "packed_fwd_tc.cuh"
@@ -17,8 +19,11 @@ constexpr int kSpreadT = 256, kSpreadTok = 32;  // threads of a block, tokens
 
 // Tokens [kSpreadTok * blockIdx.x, ..) of request blockIdx.y, those that its new tokens may see, to pages
 // of its own: entry e of its table becomes page max_pages * n + e.
+// fp16: rows of a cache that was written from a wider type may not fit.  *wide is set then (it was 0 before).
 template <typename T>
-__global__ void __launch_bounds__(kSpreadT) q8_spread_kernel(const PackedFwd a, T* K, T* V, int* table) {
+__global__ void __launch_bounds__(kSpreadT) q8_spread_kernel(const PackedFwd a, T* K, T* V, int* table, unsigned int* wide) {
+    constexpr bool kHalf = TypeTraits<T>::kId == FA_F16;
+    bool lost = false;
     const int n = blockIdx.y, k0 = blockIdx.x * kSpreadTok;
     Seq s;
     if (!seq_at(a, n, s) || s.nq == 0) return;  // the plan reports lengths that do not fit
@@ -43,8 +48,11 @@ __global__ void __launch_bounds__(kSpreadT) q8_spread_kernel(const PackedFwd a, 
             k = ld_once(static_cast<const char*>(a.K) + pg * a.k_page + in * a.k.tok + h * a.k.head + x);
             v = ld_once(static_cast<const char*>(a.V) + pg * a.v_page + in * a.v.tok + h * a.v.head + x);
             const long long e = (pg * a.H_kv + h) * a.page_size + in;
-            sk = exp_value(a.k_exp[e]);
-            sv = exp_value(a.v_exp[e]);
+            const uint8_t ek = a.k_exp[e], ev = a.v_exp[e];
+            sk = exp_value(ek);
+            sv = exp_value(ev);
+            // numbers are multiples of 2^-9, fp16's of 2^-24
+            if (kHalf) lost |= (ek != 0 && ek < 127 - 15) || (ev != 0 && ev < 127 - 15);
         }
         const long long to = (((long long)n * a.max_pages * a.page_size + j) * a.H_kv + h) * a.d + x;
         auto put = [&](T* dst, const uint4& q, float f) {
@@ -55,6 +63,7 @@ __global__ void __launch_bounds__(kSpreadT) q8_spread_kernel(const PackedFwd a, 
                 e4m3x4_to_f16((&q.x)[u], lo2, hi2);
                 const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
                 const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
+                if (kHalf) lost |= fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(r.x), fabsf(r.y))) * f > 65504.f;
                 w[2 * u] = pack2<TypeTraits<T>::kId == FA_BF16>(p.x * f, p.y * f);
                 w[2 * u + 1] = pack2<TypeTraits<T>::kId == FA_BF16>(r.x * f, r.y * f);
             }
@@ -64,12 +73,14 @@ __global__ void __launch_bounds__(kSpreadT) q8_spread_kernel(const PackedFwd a, 
         put(K + to, k, sk);
         put(V + to, v, sv);
     }
+    if (kHalf && lost) *wide = 1u;
 }
 
 size_t spread_cache_bytes(const PackedFwd& a) {
     return packed_align((size_t)a.N * a.max_pages * a.page_size * a.H_kv * a.d * 2);
 }
 size_t spread_table_bytes(const PackedFwd& a) { return packed_align((size_t)a.N * a.max_pages * 4); }
+constexpr size_t kSpreadWordBytes = 256;  // the word `wide`
 
 template <typename T, bool kTree>
 cudaError_t launch_d(const PackedFwd& a, void* ws, size_t* bytes, cudaStream_t st) {
@@ -107,22 +118,38 @@ cudaError_t launch_q8_spread(const PackedFwd& a, void* ws, size_t* bytes, cudaSt
     b.k.tok = b.v.tok = (long long)a.H_kv * a.d;
     b.k_page = b.v_page = b.k.tok * a.page_size;
     if (ws == nullptr) {
-        const cudaError_t e = launch_packed_fwd(b, nullptr, bytes, st);
-        *bytes += 2 * cache + table;
+        cudaError_t e = launch_packed_fwd(b, nullptr, bytes, st);
+        if (a.dtype == FA_F16) {
+            size_t other = 0;
+            if (e == cudaSuccess) e = launch_packed_q8(a, nullptr, &other, st);
+            *bytes = *bytes > other ? *bytes : other;
+        }
+        *bytes += 2 * cache + table + kSpreadWordBytes;
         return e;
     }
     b.K = base, b.V = base + cache;
     int* own = reinterpret_cast<int*>(base + 2 * cache);
     b.table = own;
+    unsigned int* wide = reinterpret_cast<unsigned int*>(base + 2 * cache + table);
+    char* rest = base + 2 * cache + table + kSpreadWordBytes;
     const long long room = (long long)a.max_pages * a.page_size;
     const dim3 grid((unsigned)((room + kSpreadTok - 1) / kSpreadTok), (unsigned)a.N);
-    if (a.dtype == FA_F16)
-        q8_spread_kernel<<<grid, kSpreadT, 0, st>>>(a, reinterpret_cast<__half*>(base), reinterpret_cast<__half*>(base + cache), own);
-    else
-        q8_spread_kernel<<<grid, kSpreadT, 0, st>>>(a, reinterpret_cast<__nv_bfloat16*>(base),
-                                                    reinterpret_cast<__nv_bfloat16*>(base + cache), own);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_packed_fwd(b, base + 2 * cache + table, bytes, st);
+    cudaError_t e;
+    if (a.dtype == FA_F16) {
+        if ((e = cudaMemsetAsync(wide, 0, sizeof(unsigned int), st)) != cudaSuccess) return e;
+        q8_spread_kernel<<<grid, kSpreadT, 0, st>>>(a, reinterpret_cast<__half*>(base), reinterpret_cast<__half*>(base + cache), own, wide);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        // of the two kernels one finds nothing to do; they follow each other, so the scratch is one
+        PackedFwd c = a;
+        b.gate = c.gate = wide;
+        b.gate_value = 0u, c.gate_value = 1u;
+        if ((e = launch_packed_fwd(b, rest, bytes, st)) != cudaSuccess) return e;
+        return launch_packed_q8(c, rest, bytes, st);
+    }
+    q8_spread_kernel<<<grid, kSpreadT, 0, st>>>(a, reinterpret_cast<__nv_bfloat16*>(base),
+                                                reinterpret_cast<__nv_bfloat16*>(base + cache), own, wide);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_packed_fwd(b, rest, bytes, st);
 }
 
 }  // namespace fa

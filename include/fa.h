@@ -316,7 +316,8 @@ int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, con
 /* Workspace bytes of fa_paged_fwd_ex (quantised: with K_exp and V_exp); 0 for arguments it refuses.  A
  * call with 512 rows (tokens x H / H_kv) or more per request over an 8-bit cache copies the rows it
  * reads to the workspace in `dtype`: room for N * max_pages * page_size tokens, up to 2 GB each of K and
- * V; where it would be more, and otherwise, the rows are converted in the kernel. */
+ * V; where it would be more, and otherwise, the rows are converted in the kernel.  (So they are where the
+ * copy meets a row that F16 cannot hold, of a cache that was written from another type.) */
 size_t fa_paged_workspace_bytes_ex(int N, int T_q, int H, int H_kv, int d, int page_size, int max_pages, int dtype,
                                    int quantised);
 

@@ -168,6 +168,31 @@ def _check_requests(O, LSE, Q, caches, exps, table, lens, new, scale, dtype, see
         a += nq
 
 
+@pytest.mark.parametrize("new", [[1, 3], [40, 30], [300, 220]])
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 32), (256, 16)])
+@pytest.mark.parametrize("which", ["large K", "small K", "large V"])
+def test_fp16_queries_over_rows_of_a_wider_type(new, d, page, which):
+    """A cache written from bf16 holds values above fp16's largest and below its smallest: fp16 queries see them
+    as they are, whichever kernel the number of rows chooses."""
+    H, H_kv, ctx = 8, 2, [(29 * i) % 70 + 100 for i in range(len(new))]
+    Q, caches, exps, table, lens = _setup(9, new, ctx, H, H_kv, d, page, torch.bfloat16, spread=1)
+    scale = d ** -0.5
+    if which == "large V":  # on one row of every page, whose scores leave it no weight
+        caches[0].view(torch.uint8)[:, 3] = 0x7e  # 448 in every column
+        exps[0][:, :, 3] = 127
+        exps[1][:, :, 3] = 139
+        Q = -Q.abs()
+    else:
+        up, q_up = (20, -12) if which == "large K" else (-20, 12)
+        exps[0].copy_((exps[0].int() + up).clamp(97, 157).to(torch.uint8))
+        Q = Q.float() * 2.0 ** q_up
+        scale *= 2.0 ** -(up + q_up)
+    Q = Q.to(torch.float16)
+    O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, K_exp=exps[0], V_exp=exps[1], scale=scale)
+    assert _errors() == ""
+    _check_requests(O, LSE, Q, caches, exps, table, lens, new, scale, torch.float16)
+
+
 FAR = ["rows", "rows_f16", "tiles", "tiles_f16", "tiles_64", "tiles_256", "tiles_f16_256", "copy", "simt"]
 
 
