@@ -33,7 +33,7 @@ EXPORTS = ("fa_bwd", "fa_bwd_ex", "fa_bwd_noalloc", "fa_bwd_preprocess", "fa_fwd
            "fa_last_error", "fa_shutdown", "fa_version",
            "fa_varlen_fwd", "fa_varlen_bwd", "fa_varlen_workspace_bytes", "fa_paged_fwd", "fa_paged_workspace_bytes",
            "fa_page_slots", "fa_paged_write", "fa_paged_fwd_ex", "fa_paged_workspace_bytes_ex", "fa_paged_write_q8",
-           "fa_paged_read_q8", "fa_tree_mask", "fa_paged_keep", "fa_page_trim")
+           "fa_paged_read_q8", "fa_tree_mask", "fa_paged_keep", "fa_page_trim", "fa_page_trim_ex")
 
 
 class FaError(RuntimeError):
@@ -111,6 +111,8 @@ def load_library(path: str | None = None):
         lib.fa_paged_keep.restype = I
         lib.fa_page_trim.argtypes = [V] * 8 + [I] * 4 + [V]
         lib.fa_page_trim.restype = I
+        lib.fa_page_trim_ex.argtypes = [V] * 9 + [I] * 5 + [V]
+        lib.fa_page_trim_ex.restype = I
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_version.restype = ctypes.c_char_p
         lib.fa_shutdown.restype = None

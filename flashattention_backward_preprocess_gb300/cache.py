@@ -89,12 +89,13 @@ class PagedKVCache:
     def accept(self, path, count):
         """Ends a step of drafted tokens: of request n's new tokens those numbered path[cu_q[n]] <
         path[cu_q[n] + 1] < ... (int32 [tokens], count[n] of them, from the request's first new token)
-        stay, in this order; the others' pages are free again.  The next step begins with begin()."""
+        stay, in this order; the others' pages are free again.  A request whose path or count does not fit
+        keeps all its new tokens as they are, and fa_check_device() raises.  The next step begins with begin()."""
         if self.slots is None:
             raise FaError(1, "slots: accept() before the first begin()")
         packed.fa_paged_keep(path, count, self.cu_q, self.lens, self.block_table, self.K, self.V, self.K_exp, self.V_exp)
         lens, start = packed.fa_page_trim(count, self.cu_q, self.lens, self.block_table, self.free_pages, self.free_start,
-                                          self.page_size)
+                                          self.page_size, path=path)
         torch._foreach_copy_([self.lens, self.free_start], [lens, start])
         self.slots = None
 

@@ -13,7 +13,8 @@
 // page_trim: lengths ctx + count, and the pages that only dropped tokens used back to the free
 // list, in front of its first unused entry, request after request.  The entries written are ones
 // that were used up, the table keeps its stale columns (nothing reads behind a request's last page),
-// so the call only writes what it does not read and may be run again.
+// so the call only writes what it does not read and may be run again.  By path it leaves the requests alone
+// that paged_keep leaves alone (step_fits, path_fits): their tokens all stay, the other requests are trimmed.
 //
 // All three are bound by latency, a few dependent look-ups beside the launch: masks of 32 trees of 8 to
 // 64 tokens 4 us, rows of 64 requests in 16 layers 10 us, pages of 64 requests 5 us.
@@ -70,6 +71,16 @@ __global__ void __launch_bounds__(kT) tree_mask_kernel(const TreeMask a) {
     if (wrong) atomicOr(a.err, kErrTree);
 }
 
+// Whether a request's offsets, length and number of accepted tokens fit.
+__device__ __forceinline__ bool step_fits(int c0, int c1, int T, int len, int count) {
+    return c0 >= 0 && c1 >= c0 && c1 <= T && len >= c1 - c0 && len <= (1 << 28) && count >= 0 && count <= c1 - c0;
+}
+// Whether entry i of a request's path, of `fresh` new tokens, does.
+__device__ __forceinline__ bool path_fits(const int* path, int i, int fresh) {
+    const int p = path[i];
+    return p >= 0 && p < fresh && (i == 0 || p > path[i - 1]);
+}
+
 // Block: columns [blockIdx.y * kT, + kT) of a tensor's row in layer blockIdx.z / 2, one request.
 __global__ void __launch_bounds__(kT) paged_keep_kernel(const __grid_constant__ PagedKeep a) {
     constexpr int kBatch = 4;  // rows in flight
@@ -78,16 +89,13 @@ __global__ void __launch_bounds__(kT) paged_keep_kernel(const __grid_constant__ 
     const int count = a.count[n], c0 = a.cu_q[n], c1 = a.cu_q[n + 1], len = a.seq_lens[n];
     if (count == 0) return;
     const bool first = blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0;
-    if (c0 < 0 || c1 < c0 || c1 > a.T || len < c1 - c0 || len > (1 << 28) || count < 0 || count > c1 - c0) {
+    if (!step_fits(c0, c1, a.T, len, count)) {
         if (first) atomicOr(a.err, kErrTree);
         return;
     }
     const int* path = a.path + c0;
     bool bad = false;
-    for (int i = threadIdx.x; i < count; i += kT) {
-        const int p = path[i];
-        bad |= p < 0 || p >= c1 - c0 || (i > 0 && p <= path[i - 1]);
-    }
+    for (int i = threadIdx.x; i < count; i += kT) bad |= !path_fits(path, i, c1 - c0);
     if (__syncthreads_or(bad)) {
         if (first) atomicOr(a.err, kErrTree);
         return;
@@ -137,9 +145,20 @@ __global__ void __launch_bounds__(kTrimT) page_trim_kernel(const PageTrim a) {
     __shared__ int s_sum[33];
     const int tid = threadIdx.x;
     const int start = *a.free_start;
+    // with paths: what request n keeps, all it has where its numbers do not fit
+    auto kept_alone = [&](int n) {
+        const int c0 = a.cu_q[n], c1 = a.cu_q[n + 1], len = a.seq_lens[n], count = a.count[n];
+        bool fits = step_fits(c0, c1, a.T, len, count);
+        for (int i = 0; fits && i < count; ++i) fits = path_fits(a.path + c0, i, c1 - c0);
+        if (!fits) atomicOr(a.err, kErrTree);
+        return fits ? len - (c1 - c0) + count : len;
+    };
     // columns [need, had) of request n's row are given back
     auto gone = [&](int n, int& need, int& had) {
-        const int len = a.seq_lens[n], kept = len - (a.cu_q[n + 1] - a.cu_q[n]) + a.count[n];
+        const int len = a.seq_lens[n];
+        // (the first pass has written lens, by this thread, where there are paths)
+        const int kept = a.by_path ? a.lens[n] : len - (a.cu_q[n + 1] - a.cu_q[n]) + a.count[n];
+        if (a.by_path && kept == len) return 0;
         need = min(ceil_div(kept, a.page_size), a.max_pages);
         had = min(ceil_div(len, a.page_size), a.max_pages);
         int c = 0;
@@ -148,6 +167,10 @@ __global__ void __launch_bounds__(kTrimT) page_trim_kernel(const PageTrim a) {
     };
     bool bad = false;
     for (int n = tid; n < a.N; n += kTrimT) {
+        if (a.by_path) {
+            a.lens[n] = kept_alone(n);
+            continue;
+        }
         const int c0 = a.cu_q[n], c1 = a.cu_q[n + 1], len = a.seq_lens[n], count = a.count[n];
         bad |= !(c0 >= 0 && c1 >= c0 && len >= c1 - c0 && len <= (1 << 30) && count >= 0 && count <= c1 - c0);
     }
@@ -171,7 +194,7 @@ __global__ void __launch_bounds__(kTrimT) page_trim_kernel(const PageTrim a) {
     for (int n0 = 0; n0 < a.N; n0 += kTrimT) {
         const int n = n0 + tid;
         if (bad || full) {
-            if (n < a.N) a.lens[n] = bad ? a.seq_lens[n] : a.seq_lens[n] - (a.cu_q[n + 1] - a.cu_q[n]) + a.count[n];
+            if (n < a.N && !a.by_path) a.lens[n] = bad ? a.seq_lens[n] : a.seq_lens[n] - (a.cu_q[n + 1] - a.cu_q[n]) + a.count[n];
             continue;
         }
         int need = 0, had = 0, total;
@@ -179,7 +202,7 @@ __global__ void __launch_bounds__(kTrimT) page_trim_kernel(const PageTrim a) {
         long long at = at0 + block_excl_scan(mine, s_sum, &total);
         at0 += total;
         if (n >= a.N) continue;
-        a.lens[n] = a.seq_lens[n] - (a.cu_q[n + 1] - a.cu_q[n]) + a.count[n];
+        if (!a.by_path) a.lens[n] = a.seq_lens[n] - (a.cu_q[n + 1] - a.cu_q[n]) + a.count[n];
         for (int i = need; i < had; ++i) {
             const int page = a.table[(size_t)n * a.max_pages + i];
             if (page >= 0) a.free_pages[at++] = page;

@@ -542,33 +542,51 @@ int fa_paged_keep(const int* path, const int* count, const int* cu_q, const int*
     return FA_OK;
 }
 
+static int page_trim(PageTrim a, cudaStream_t st) {
+    clear_error();
+    int rc;
+    if ((rc = check_count("N", a.N, 1, kMaxTokens)) || (rc = check_count("T", a.T, 0, kMaxTokens)) ||
+        (rc = check_count("num_free", a.n_free, 0, kMaxTokens)) ||
+        (rc = check_count("page_size", a.page_size, 1, kMaxTokens)) ||
+        (rc = check_count("max_pages", a.max_pages, 1, kMaxTokens)))
+        return rc;
+    if ((rc = check_ptr(a.count, "count", 4)) || (rc = check_ptr(a.cu_q, "cu_q", 4)) ||
+        (rc = check_ptr(a.seq_lens, "seq_lens", 4)) || (rc = check_ptr(a.table, "block_table", 4)) ||
+        (rc = check_ptr(a.free_start, "free_start", 4)) || (rc = check_ptr(a.lens, "lens", 4)) ||
+        (rc = check_ptr(a.free_next, "free_next", 4)))
+        return rc;
+    if (a.n_free > 0 && (rc = check_ptr(a.free_pages, "free_pages", 4))) return rc;
+    if (a.T > 0 && (rc = check_ptr(a.path, "path", 4))) return rc;
+    const Span in[] = {{"count", a.count, 4ll * a.N}, {"cu_q", a.cu_q, 4ll * (a.N + 1)}, {"seq_lens", a.seq_lens, 4ll * a.N},
+                       {"block_table", a.table, 4ll * a.N * a.max_pages}, {"free_start", a.free_start, 4},
+                       {"path", a.path, 4ll * a.T}};
+    const Span out[] = {{"free_pages", a.free_pages, 4ll * a.n_free}, {"lens", a.lens, 4ll * a.N}, {"free_next", a.free_next, 4}};
+    if ((rc = check_apart(in, out))) return rc;
+    if ((rc = err_word(&a.err))) return rc;
+    const cudaError_t e = launch_page_trim(a, st);
+    if (e != cudaSuccess) return cuda_bad("page_trim launch", e);
+    return FA_OK;
+}
+
 int fa_page_trim(const int* count, const int* cu_q, const int* seq_lens, const int* block_table, int* free_pages,
                  const int* free_start, int* lens, int* free_next, int N, int num_free, int page_size, int max_pages,
                  void* stream) {
-    clear_error();
-    int rc;
-    if ((rc = check_count("N", N, 1, kMaxTokens)) || (rc = check_count("num_free", num_free, 0, kMaxTokens)) ||
-        (rc = check_count("page_size", page_size, 1, kMaxTokens)) ||
-        (rc = check_count("max_pages", max_pages, 1, kMaxTokens)))
-        return rc;
-    if ((rc = check_ptr(count, "count", 4)) || (rc = check_ptr(cu_q, "cu_q", 4)) ||
-        (rc = check_ptr(seq_lens, "seq_lens", 4)) || (rc = check_ptr(block_table, "block_table", 4)) ||
-        (rc = check_ptr(free_start, "free_start", 4)) || (rc = check_ptr(lens, "lens", 4)) ||
-        (rc = check_ptr(free_next, "free_next", 4)))
-        return rc;
-    if (num_free > 0 && (rc = check_ptr(free_pages, "free_pages", 4))) return rc;
-    const Span in[] = {{"count", count, 4ll * N}, {"cu_q", cu_q, 4ll * (N + 1)}, {"seq_lens", seq_lens, 4ll * N},
-                       {"block_table", block_table, 4ll * N * max_pages}, {"free_start", free_start, 4}};
-    const Span out[] = {{"free_pages", free_pages, 4ll * num_free}, {"lens", lens, 4ll * N}, {"free_next", free_next, 4}};
-    if ((rc = check_apart(in, out))) return rc;
     PageTrim a = {};
     a.count = count, a.cu_q = cu_q, a.seq_lens = seq_lens, a.table = block_table, a.free_start = free_start;
     a.free_pages = free_pages, a.lens = lens, a.free_next = free_next;
     a.N = N, a.n_free = num_free, a.page_size = page_size, a.max_pages = max_pages;
-    if ((rc = err_word(&a.err))) return rc;
-    const cudaError_t e = launch_page_trim(a, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_bad("page_trim launch", e);
-    return FA_OK;
+    return page_trim(a, static_cast<cudaStream_t>(stream));
+}
+
+int fa_page_trim_ex(const int* path, const int* count, const int* cu_q, const int* seq_lens, const int* block_table,
+                    int* free_pages, const int* free_start, int* lens, int* free_next, int N, int T, int num_free,
+                    int page_size, int max_pages, void* stream) {
+    PageTrim a = {};
+    a.by_path = true, a.path = path, a.T = T;
+    a.count = count, a.cu_q = cu_q, a.seq_lens = seq_lens, a.table = block_table, a.free_start = free_start;
+    a.free_pages = free_pages, a.lens = lens, a.free_next = free_next;
+    a.N = N, a.n_free = num_free, a.page_size = page_size, a.max_pages = max_pages;
+    return page_trim(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

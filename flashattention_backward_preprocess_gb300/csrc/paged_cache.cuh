@@ -69,9 +69,11 @@ cudaError_t launch_paged_keep(const PagedKeep& a, cudaStream_t st);
 
 // Lengths after the step and the pages behind them.
 struct PageTrim {
+    bool by_path;     // a request that PagedKeep leaves alone keeps all tokens, the others do not mind it
+    const int* path;  // then, [T] as in PagedKeep
     const int *count, *cu_q, *seq_lens, *table, *free_start;
     int *free_pages, *lens, *free_next;
-    int N, n_free, page_size, max_pages;
+    int N, T, n_free, page_size, max_pages;
     unsigned int* err;
 };
 cudaError_t launch_page_trim(const PageTrim& a, cudaStream_t st);

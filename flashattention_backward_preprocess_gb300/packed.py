@@ -463,9 +463,10 @@ def fa_paged_keep(path, count, cu_q, seq_lens, block_table, K_caches, V_caches, 
 
 
 def fa_page_trim(count, cu_q, seq_lens, block_table, free_pages, free_start, page_size: int, lens=None, free_next=None,
-                 stream=None):
+                 stream=None, path=None):
     """(lens, free_next) once `count` of each request's new tokens are kept; the pages behind them are
-    entered into free_pages in place; see include/fa.h (fa_page_trim)."""
+    entered into free_pages in place; see include/fa.h (fa_page_trim, and with the path that fa_paged_keep was
+    given, fa_page_trim_ex)."""
     N = cu_q.numel() - 1
     _ints("cu_q", cu_q, (N + 1,))
     _ints("count", count, (N,))
@@ -479,13 +480,19 @@ def fa_page_trim(count, cu_q, seq_lens, block_table, free_pages, free_start, pag
         _ints("lens", lens, (N,))
     if free_next is not None:
         _ints("free_next", free_next, (1,))
-    dev = _device(count, cu_q, seq_lens, block_table, free_pages, free_start, lens, free_next)
+    T = 0
+    if path is not None:
+        T = path.numel()
+        _ints("path", path, (T,))
+    dev = _device(count, cu_q, seq_lens, block_table, free_pages, free_start, lens, free_next, path)
 
     def body(st):
         out = (_empty_like(seq_lens) if lens is None else lens, _empty_like(free_start) if free_next is None else free_next)
-        _check(load_library().fa_page_trim(
-            count.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
-            free_start.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), N, n_free, page_size, cols, st))
+        ptrs = [t.data_ptr() for t in (count, cu_q, seq_lens, block_table, free_pages, free_start, *out)]
+        if path is None:
+            _check(load_library().fa_page_trim(*ptrs, N, n_free, page_size, cols, st))
+        else:
+            _check(load_library().fa_page_trim_ex(path.data_ptr(), *ptrs, N, T, n_free, page_size, cols, st))
         return out
 
     return _call(dev, stream, body)

@@ -441,6 +441,16 @@ int fa_page_trim(const int* count, const int* cu_q, const int* seq_lens, const i
                  const int* free_start, int* lens, int* free_next, int N, int num_free, int page_size, int max_pages,
                  void* stream);
 
+/*
+ * fa_page_trim_ex -- fa_page_trim behind an fa_paged_keep of the same path ([T]), which leaves a request
+ * whose path, count, offsets or length do not fit alone: such a request keeps all its new tokens (lens is its
+ * seq_lens, none of its pages is given back), and the other requests are trimmed as ever.  fa_check_device
+ * reports it (FA_ERR_INVALID_ARG).
+ */
+int fa_page_trim_ex(const int* path, const int* count, const int* cu_q, const int* seq_lens, const int* block_table,
+                    int* free_pages, const int* free_start, int* lens, int* free_next, int N, int T, int num_free,
+                    int page_size, int max_pages, void* stream);
+
 /* Synchronizes `stream`, then returns FA_ERR_TIMEOUT if a kernel of this
  * library on that stream, or an fa_bwd_noalloc call on this device, recorded
  * a bounded-wait timeout since the last check (clearing the record), else

@@ -1,0 +1,29 @@
+"""Refusals of the trim that goes by the accepted tokens' path (no GPU needed)."""
+import pytest
+import torch
+
+import flashattention_backward_preprocess_gb300 as fa
+from flashattention_backward_preprocess_gb300 import build
+
+P = [0x10000 * (i + 1) for i in range(9)]  # never dereferenced: checked before anything is launched
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("kw,arg", [
+    (dict(path=None), "path"), (dict(path=P[0] + 2), "path"), (dict(T=-1), "T"), (dict(count=None), "count"), (dict(free=None), "free_pages"),
+    (dict(out=P[0] + 28), "lens"), (dict(next=P[0]), "free_next"), (dict(out=P[3]), "lens"), (dict(N=0), "N"), (dict(page=0), "page_size"),
+    (dict(cols=0), "max_pages"), (dict(n_free=-1), "num_free"),
+])
+def test_library(kw, arg):
+    build.build()
+    a = dict(path=P[0], count=P[1], cu=P[2], lens=P[3], table=P[4], free=P[5], start=P[6], out=P[7], next=P[8], N=2, T=8, n_free=10,
+             page=16, cols=2, stream=None)
+    assert set(kw) <= set(a)
+    assert fa.load_library().fa_page_trim_ex(*{**a, **kw}.values()) == 1
+    assert fa.fa_last_error().startswith(arg + ":"), fa.fa_last_error()
+
+
+@pytest.mark.parametrize("path,match", [(i32(0, 1).long(), "path"), (torch.zeros(2, 2, dtype=torch.int32)[:, 0], "path"), (i32(0), "device")])
+def test_torch_call(path, match):
+    with pytest.raises(fa.FaError, match=match):
+        fa.fa_page_trim(i32(1), i32(0, 5), i32(5), torch.zeros(1, 2, dtype=torch.int32), i32(1, 2), i32(0), 16, path=path)
