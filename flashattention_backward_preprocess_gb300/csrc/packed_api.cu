@@ -4,8 +4,11 @@
 #include <math.h>
 #include <time.h>
 
+#include <algorithm>
 #include <mutex>
+#include <new>
 #include <string>
+#include <vector>
 
 #include "packed.cuh"
 #include "paged_cache.cuh"
@@ -518,6 +521,16 @@ int fa_paged_keep(const int* path, const int* count, const int* cu_q, const int*
         if ((rc = check_ptr(K_caches[i], "K_caches", 16)) || (rc = check_ptr(V_caches[i], "V_caches", 16)) ||
             (K_exps && ((rc = check_ptr(K_exps[i], "K_exps", 16)) || (rc = check_ptr(V_exps[i], "V_exps", 16)))))
             return rc;
+    // a tensor given twice would be moved twice, by blocks that do not wait for one another
+    std::vector<const void*> all;
+    try {
+        for (void* const* list : {K_caches, V_caches, K_exps, V_exps})
+            if (list) all.insert(all.end(), list, list + layers);
+    } catch (const std::bad_alloc&) {
+        return set_error(FA_ERR_NOMEM, "layers", "out of host memory");
+    }
+    std::sort(all.begin(), all.end());
+    if (std::adjacent_find(all.begin(), all.end()) != all.end()) return bad("K_caches", "the same tensor is given twice");
     const long long kr = (long long)H_kv * d;
     const long long dense[6] = {kr * page_size, kr, d, kr * page_size, kr, d};
     const long long* s = strides ? strides : dense;

@@ -413,7 +413,8 @@ int fa_tree_mask(const int* parents, const int* cu_q, const int* ctx_lens, long 
  *   count     : [N] int32, 0 to S
  *   seq_lens  : [N] int32 tokens in the cache, the new ones included
  *   K_caches, V_caches : host arrays of `layers` device pointers, caches of one shape and stride
- *   K_exps, V_exps     : NULL, or the same of the exponents of 8-bit caches
+ *   K_exps, V_exps     : NULL, or the same of the exponents of 8-bit caches.  No two of all these
+ *                        tensors share bytes; a pointer given twice is refused
  *   strides   : {K page, K row, K head, V page, V row, V head} or NULL
  * A request whose path or count does not fit is left alone, a row on a page outside the cache stays
  * where it is; fa_check_device reports both (FA_ERR_INVALID_ARG).

@@ -1,4 +1,6 @@
-"""Refusals of the trim that goes by the accepted tokens' path (no GPU needed)."""
+"""Refusals of the calls behind PagedKVCache.accept (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -27,3 +29,17 @@ def test_library(kw, arg):
 def test_torch_call(path, match):
     with pytest.raises(fa.FaError, match=match):
         fa.fa_page_trim(i32(1), i32(0, 5), i32(5), torch.zeros(1, 2, dtype=torch.int32), i32(1, 2), i32(0), 16, path=path)
+
+
+@pytest.mark.parametrize("K,V,Ke,Ve", [
+    ((1, 2, 1), (3, 4, 5), None, None), ((1, 2, 3), (4, 2, 5), None, None), ((1, 2, 3), (4, 5, 6), (7, 8, 7), (9, 10, 11)),
+    ((1, 2, 3), (4, 5, 6), (7, 8, 9), (10, 11, 8)), ((1, 2, 3), (4, 5, 6), (7, 8, 9), (10, 11, 1)),
+])
+def test_keep_refuses_a_tensor_given_twice(K, V, Ke, Ve):
+    """Its rows would be moved by two blocks at once."""
+    build.build()
+    arr = lambda ps: None if ps is None else (ctypes.c_void_p * 3)(*(0x10000 * p for p in ps))
+    rc = fa.load_library().fa_paged_keep(P[0], P[1], P[2], P[3], P[4], arr(K), arr(V), arr(Ke), arr(Ve), 3, 2, 8, 4, 16, 2, 2, 64, None,
+                                         fa.FA_BF16, None)
+    assert rc == 1
+    assert fa.fa_last_error() == "K_caches: the same tensor is given twice"
