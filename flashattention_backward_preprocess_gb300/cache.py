@@ -62,13 +62,18 @@ class PagedKVCache:
         parents[i] of the same request (an earlier one, counted from its first new token) or, at -1,
         the cached ones; its position counts its ancestors (attend() takes no window then).  words:
         64 tokens of the largest tree each (as many as the step's tokens may need unless given)."""
-        self.cu_q = cu_q
+        # whatever is refused is refused before anything changes
+        tree = depth = None
+        if parents is not None:
+            if parents.numel() != tokens:
+                raise FaError(1, f"parents: expected one for each of {tokens} tokens, got {parents.numel()}")
+            words = min(max(-(-int(tokens) // 64), 1), 1024) if words is None else words
+            tree, depth = packed.fa_tree_mask(parents, cu_q, self.lens, words)
         self.slots, self.positions, lens, start = packed.fa_page_slots(
             self.lens, cu_q, self.block_table, self.free_pages, self.free_start, self.page_size, tokens)
-        self.tree = None
-        if parents is not None:
-            words = min(max(-(-int(tokens) // 64), 1), 1024) if words is None else words
-            self.tree, self.positions = packed.fa_tree_mask(parents, cu_q, self.lens, words)
+        self.cu_q, self.tree = cu_q, tree
+        if tree is not None:
+            self.positions = depth
         # in place: the replays of a captured step go on from where the last one ended
         torch._foreach_copy_([self.lens, self.free_start], [lens, start])
         return self.positions
@@ -76,7 +81,7 @@ class PagedKVCache:
     def attend(self, layer: int, Q, K, V, scale: float | None = None, window_size: int = 0):
         """Caches K and V [tokens, H_kv, d] of the step and returns (O, LSE) of Q [tokens, H, d]."""
         if self.slots is None:
-            raise FaError(1, "slots: attend() before the first begin()")
+            raise FaError(1, "slots: attend() outside a step, begin() comes first")
         k_exp = v_exp = None
         if self.K_exp is None:
             packed.fa_paged_write(K, V, self.slots, self.K[layer], self.V[layer])
@@ -92,7 +97,7 @@ class PagedKVCache:
         stay, in this order; the others' pages are free again.  A request whose path or count does not fit
         keeps all its new tokens as they are, and fa_check_device() raises.  The next step begins with begin()."""
         if self.slots is None:
-            raise FaError(1, "slots: accept() before the first begin()")
+            raise FaError(1, "slots: accept() outside a step, begin() comes first")
         packed.fa_paged_keep(path, count, self.cu_q, self.lens, self.block_table, self.K, self.V, self.K_exp, self.V_exp)
         lens, start = packed.fa_page_trim(count, self.cu_q, self.lens, self.block_table, self.free_pages, self.free_start,
                                           self.page_size, path=path)

@@ -43,3 +43,14 @@ def test_keep_refuses_a_tensor_given_twice(K, V, Ke, Ve):
                                          fa.FA_BF16, None)
     assert rc == 1
     assert fa.fa_last_error() == "K_caches: the same tensor is given twice"
+
+
+@pytest.mark.parametrize("parents,words,match", [
+    (i32(-1, 0, 1, 2), None, "parents"), (i32(-1, 0, 1, 2, 3, 4), None, "parents"), (i32(-1, 0, 1, 2, 3).long(), None, "parents"),
+    (i32(-1, 0, 1, 2, 3), 0, "words"),
+])
+def test_begin_refuses_parents_before_anything_else(parents, words, match):
+    cache = fa.PagedKVCache(1, 4, 16, 2, 64, 1, 4, device="cpu")
+    with pytest.raises(fa.FaError, match=match):
+        cache.begin(i32(0, 5), 5, parents=parents, words=words)
+    assert cache.slots is None and cache.cu_q is None and cache.tree is None

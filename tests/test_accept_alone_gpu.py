@@ -78,3 +78,21 @@ def test_trim_judges_a_path_as_keep_does():
     out, nxt = fa.fa_page_trim(count, torch.tensor([0, 8, 7, 11, 40], **I32), lens, table, free, start, 4, path=path)
     assert "path" in _errors()
     assert out.tolist() == [4, 12, 3, 2]
+
+
+@pytest.mark.parametrize("parents,words", [([-1, 0, 1], 1), ([-1, 0, 1, 2, 3], 1), ([-1, 0, 1, 2], 1025)])
+def test_a_refused_begin_changes_nothing(parents, words):
+    """The step before it can go on: same tables, slots and results."""
+    cache = fa.PagedKVCache(1, 8, PAGE, 2, 64, 1, 6)
+    cu, x = _cu([7]), [_rand(i, (7, h, 64), torch.bfloat16) for i, h in enumerate((4, 2, 2))]
+    cache.begin(cu, 7)
+    want = cache.attend(0, *x)
+    held = [t.clone() for t in (cache.block_table, cache.lens, cache.free_start, cache.slots, cache.positions)]
+    with pytest.raises(fa.FaError):
+        cache.begin(_cu([4]), 4, parents=torch.tensor(parents, **I32), words=words)
+    for a, b in zip(held, (cache.block_table, cache.lens, cache.free_start, cache.slots, cache.positions)):
+        assert torch.equal(a, b)
+    assert cache.tree is None and cache.cu_q is cu
+    for a, b in zip(cache.attend(0, *x), want):
+        assert torch.equal(a, b)
+    assert _errors() == ""
