@@ -368,8 +368,9 @@ int fa_paged_write(const void* K, const void* V, const long long* slots, void* K
  *             for F16)
  *   numbers : x * 2^-e rounded to nearest, halves to even; magnitudes above 448 * 2^30 (F16: 61440)
  *             become that, infinities and NaN become NaN and do not count for the exponent
- * so an element is off by 2^-4 of itself or 2^-10 * 2^e at most.  (Exponent bytes of other origin are 1
- * to 254, or 0 with numbers that are all 0, as in a cache that was cleared.)
+ * so an element is off by 2^-4 of itself or 2^-10 * 2^e at most.  (Exponent bytes of other origin are 97
+ * to 157 as these, or 0 with numbers that are all 0, as in a cache that was cleared: the attention kernels
+ * take no others.  Slots that hold no key may have any.)
  *   K_cache, V_cache : [num_pages, page_size, H_kv, d] bytes, 16-byte aligned
  *   K_exp, V_exp     : [num_pages, H_kv, page_size] bytes, dense
  *   strides          : as in fa_paged_write, the cache's in bytes
