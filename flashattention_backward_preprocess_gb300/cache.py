@@ -34,7 +34,10 @@ class PagedKVCache:
 
     quantised: the cache holds 8-bit rows (fa_paged_write_q8), K_exp and V_exp their exponents
     [num_pages, H_kv, page_size] in each layer; `dtype` is not used then, the steps' tensors have
-    their own.
+    their own.  attend() chooses its kernel by the step's tokens per row then, idle rows included, so these
+    do have a price in steps of prompts (one of 512 tokens over 8000 cached ones: 99 us with one row, 466
+    with 64), and with 512 / (heads of a group) tokens per row or more it takes scratch for all that the
+    tables have room for, 4 GB at most (fa_paged_workspace_bytes_ex).
     """
 
     def __init__(self, layers: int, num_pages: int, page_size: int, H_kv: int, d: int, rows: int, max_pages: int,
@@ -61,7 +64,8 @@ class PagedKVCache:
         parents (int32 [tokens]): each request's new tokens are a tree, token i following the token
         parents[i] of the same request (an earlier one, counted from its first new token) or, at -1,
         the cached ones; its position counts its ancestors (attend() takes no window then).  words:
-        64 tokens of the largest tree each (as many as the step's tokens may need unless given)."""
+        64 tokens of the largest tree each (as many as the step's tokens may need unless given: a token's
+        mask takes 8 bytes each, so give it where many requests share a step)."""
         # whatever is refused is refused before anything changes
         tree = depth = None
         if parents is not None:

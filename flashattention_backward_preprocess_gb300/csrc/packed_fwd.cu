@@ -6,9 +6,12 @@ namespace fa {
 namespace {
 
 // Steps over an 8-bit cache whose requests have 32 rows (tokens x heads of a group) or fewer on
-// average, on pages of whole 16-key pieces: packed_q8_rows.cu, which reads the cache once per 16 rows
-// (32 requests over 98000 keys, 4 heads a group: 1, 4, 8 and 16 tokens each take 67, 75, 125 and 219
-// us there, 130, 131, 140 and 165 us in 128-row tiles).
+// average, idle ones counted too, on pages of whole 16-key pieces: packed_q8_rows.cu, which reads the cache
+// once per 16 rows.  32 requests of 8, 16, 32, 48 and 64 rows over 98000 keys, bf16, us in a replayed graph:
+//   d = 128, H_kv = 8, 4 heads a group (1 and 8: the same)   there 78, 81, 130, 179, 226
+//                                                            in 128-row tiles 147, 148, 154, 158, 171
+//   d = 64, H_kv = 8, 4 heads    57, 58, 91, 124, 156        119, 120, 124, 128, 134
+//   d = 128, H_kv = 2, 16 heads      48, 66, 86, 105              58, 62, 65, 70
 bool few_rows(const PackedFwd& a) {
     const long long g = a.H / a.H_kv;
     return a.d <= 128 && g <= 16 && a.page_size % 16 == 0 && a.T_q * g <= 32ll * a.N;

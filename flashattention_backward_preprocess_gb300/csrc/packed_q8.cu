@@ -5,11 +5,16 @@
 // conversion is what takes its time (about 4500 cycles of a 128-key tile; the products need 1300).
 // Where requests have many such tiles (chunks of prompts), one pass makes the rows of the cache that
 // the step reads fp16 or bf16, exactly, in pages of the workspace, and the kernel for caches of that
-// type does the rest.  (Every row that fa_paged_write_q8 writes is a bf16 number; fp16 holds what was written
-// from fp16.  A row that it cannot hold is noticed by the copy, and the tensor-core kernel above does the step instead: one
-// more launch for fp16, 173 us in place of 162 for the chunks below.)  10 chunks of up to 512 tokens over up to 8000 cached ones, H = 32, H_kv = 8, d =
-// 128, bf16: 159 us (42 of them the copy of 54 MB) against 316.  32 trees of 8 to 64 tokens over 100 to
-// 6000, f16, in the converting kernel: 252 us; the copy alone would write 400 MB.
+// type does the rest.  10 chunks of up to 512 tokens over up to 8000 cached ones, H = 32, H_kv = 8, d = 128,
+// bf16: 157 us (42 of them the copy of 54 MB) against 316.  32 trees of 8 to 64 tokens over 100 to 6000,
+// f16, in the converting kernel: 256 us; the copy alone would write 400 MB.
+//
+// Every number that fa_paged_write_q8 stores is a bf16 number; fp16 holds those written from fp16.  A row that
+// it cannot hold is noticed by the copy, and the converting kernel does the step instead: one more
+// launch for fp16, 173 us in place of 162 for the ten chunks.
+//
+// A bf16 row's P has 8 bits behind the copy and 11 in the other two kernels, so a request's result may differ by
+// such roundings with the requests that share its call.
 #include "packed_fwd_tc.cuh"
 
 namespace fa {
@@ -100,6 +105,12 @@ cudaError_t launch_packed_q8(const PackedFwd& a, void* ws, size_t* bytes, cudaSt
 
 // From four 128-row tiles per request on, where the copy (of all that the tables have room for: the
 // lengths are on the device) takes 2 GB each of K and V at most, and pages that the other kernel takes.
+// Eight requests of 256, 384, 512, 768 and 1024 rows over 500 to 8000 keys, H_kv = 8, us in a replayed graph:
+//   bf16, d = 128   copied 146, 155, 185, 203, 241   converted in tiles 140, 186, 238, 337, 435
+//   f16,  d = 128          164, 164, 195, 212, 255                      129, 166, 211, 296, 382
+//   bf16, d = 64            89, 101, 117, 146, 176                      113, 150, 191, 272, 354
+// so the copy is even at about 300 rows; below 512 it would save a sixth at most (a third at d = 64), for a
+// workspace larger than the cache itself.
 bool q8_spread(const PackedFwd& a) {
     const long long g = a.H / a.H_kv;
     const int bn = a.d == 256 ? 64 : 128;

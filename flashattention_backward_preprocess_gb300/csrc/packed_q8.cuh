@@ -22,8 +22,10 @@
 // in its place is converted, and store the operands.
 // Rows that are no key of the request (behind its last, before its window, on no page) are zeros.
 // A tile takes about 4500 cycles, of which no unit fills half (the products 1300, conversions 500, shared
-// memory's bandwidth 1300): the hand-overs between the roles do.  Staging the numbers in shared memory by
-// asynchronous copies first took as long.
+// memory's bandwidth 1300): the hand-overs between the roles do, and the kernel's length, of whose 80
+// registers a thread 80 to 150 bytes are spilled besides (of 16 cycles between two instructions of a warp 4.9
+// are awaited instructions, 4.7 memory).  Staging the numbers in shared memory by asynchronous copies first
+// took as long.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -81,7 +83,8 @@ __device__ __forceinline__ float convert_q_row(uint8_t* q, int t) {
             most = fmaxf(most, hi <= 3.4e38f ? hi : 0.f);
         }
     }
-    // most * 2^n in [2^14, 2^15); n at most 100 keeps its inverse times a key's 2^e a normal number
+    // most * 2^n in [2^14, 2^15), or n = 100 for rows below 2^-86: its inverse times a key's 2^e (2^-30 at
+    // least) is above 2^-149, the smallest float
     const int n = most > 0.f ? min(100, 14 - ((__float_as_int(most) >> 23) - 127)) : 0;
     const float s = __int_as_float((n + 127) << 23);
 #pragma unroll 4

@@ -1,14 +1,14 @@
 // packed_q8_rows.cu -- attention over an 8-bit cache for steps of few rows (a token or a few for each
-// request): packed_fwd_tc.cuh's plan, items and joins, but the numbers go from memory to registers to
-// the products, with nothing in shared memory and no warp waiting for another.
+// request): packed_fwd_tc.cuh's plan, items and joins, but each warp copies, converts and multiplies its
+// own keys, with no operand in shared memory and no warp waiting for another.
 //
 // An item's rows (up to 16: tpt tokens x the g heads of a key/value head) are one 16-row operand of
 // mma.sync m16n8k16, whose fragments a thread can load for itself.  (tcgen05 reads 128 rows of which
 // such a step fills g, and takes its operands from shared memory: the 8-bit rows would have to be
-// written there as fp16 first.)  Warp w of four takes keys [16 w, 16 w + 16) of each 64-key tile, with
+// written there as fp16 first.)  Warp w of a CTA's W takes keys [16 w, 16 w + 16) of each tile of 16 W, with
 // a max, a sum and an accumulator of its own; they meet once, at the item's end.
 //   * K: the products of Q K^T run over d in an order in which a lane's operands are 16 bytes next to
-//     each other: lane (q = lane / 4, t = lane % 4) loads bytes [64 x + 16 t, + 16) of keys q and q + 8.
+//     each other: lane (q = lane / 4, t = lane % 4) takes bytes [64 x + 16 t, + 16) of keys q and q + 8.
 //   * V: the output columns are numbered so that a lane needs bytes [q D / 8, + D / 8) of its four keys
 //     2t, 2t + 1, 2t + 8, 2t + 9: whole 128-byte lines again; two bytes of two keys are paired by a
 //     byte permutation, and pairs made fp16 by one conversion.
@@ -17,14 +17,16 @@
 //     the max of y less 8, looked at anew when a y exceeds m by 15: P' <= 2^15 fits fp16, whose fixed
 //     step below 2^-14 is 2^-33 of the row's largest weight.
 //   * Q is fp16, a bf16 row times a power of two (packed_q8.cuh says why).
-// Numbers come through a ring in shared memory, kStages tiles of a warp's 4 KB, by asynchronous copies;
-// every thread copies what it will read itself, so no warp waits for another.  Twelve warps a SM: in
-// three CTAs when there are many items, whose ends then overlap; in one when there are few, since an
-// item is cut into as many parts as CTAs share it, and whoever joins the parts reads them all.
+// Bytes come through a ring in shared memory, kStages tiles of a warp's 4 KB, by asynchronous copies;
+// every thread copies the numbers that it will read itself, so no warp waits for another.  Twelve warps a
+// SM: in three CTAs of four (tiles of 64 keys) when there are many items, whose ends then overlap; in one of
+// twelve (192 keys) when there are few, since an item is cut into as many parts as CTAs share it, and
+// whoever joins the parts reads them all.
 //
-// Bound by instructions (520 per warp and 16 keys, 0.4 a cycle and scheduler), then DRAM.  Measured in a
-// replayed graph, bf16, H = 32, H_kv = 8, d = 128: 64 requests, one token each, over 0.57 GB of cache 141
-// us (4.1 TB/s); one token of f16, H = 16, H_kv = 2, over 131072 keys 63 us; over 1024 keys 20 us.
+// Bound by latency at three warps a scheduler (520 instructions per warp and 16 keys, 0.43 issued a cycle and
+// scheduler; of 6.7 cycles between two of a warp 2.0 are fixed latencies, 1.5 memory's), then DRAM.  Measured
+// in a replayed graph, bf16, H = 32, H_kv = 8, d = 128: 64 requests, one token each, over 0.57 GB of cache 141
+// us (4.1 TB/s); one token of f16, H = 16, H_kv = 2, over 131072 keys 61 us; over 1024 keys 20 us.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -79,8 +81,8 @@ __device__ __forceinline__ float minus127(uint32_t w, int n) {
 __device__ __forceinline__ float down2(uint32_t w, int n) { return __uint_as_float((254u - (w >> (8 * n) & 0xffu)) << 23); }
 
 // Joins the parts of a cut item (join_parts with few rows and many parts: one long request is cut over
-// the whole grid).  The warps take every fourth part each, 16 loads of a thread in flight, and meet in
-// s_o; joining one after another, 76 parts took 100 us.
+// the whole grid).  Of kWarps warps each takes every kWarps-th part, 16 loads of a thread in flight, and
+// they meet in s_o; joining one after another, 76 parts took 100 us.
 template <typename T, int D, int kWarps>
 __device__ __forceinline__ void join_rows(const PackedFwd& a, const FwdPlan& p, const FwdTile& tile, int head0, int g, int rows,
                                           int first, int count, float (*s_o)[RT][D + 4], float2* s_row) {
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
                 }
             }
         }
-        // ---- the four warps' parts together.  Column n of output tile f is column n CH + f of the head
+        // ---- the warps' parts together.  Column n of output tile f is column n CH + f of the head
         cp_async_wait<0>();
         __syncthreads();  // the ring is not in use any more
 #pragma unroll

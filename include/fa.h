@@ -305,7 +305,8 @@ size_t fa_paged_workspace_bytes(int N, int T_q, int H, int H_kv, int d, int page
  * (exact down to 2^-31 of the row's largest element for BF16) and P: its 11 bits, with a fixed step at the
  * small end, 2^-33 of the row's largest product of a P and 2^e of its V (2^-19 of it where the exponents e
  * of V differ inside a tile of keys).  Every key counts with its own exponents, whatever size those of other
- * keys have.  The result is bitwise reproducible.
+ * keys have.  The result is bitwise reproducible; which kernel computes it goes by the sizes of the whole
+ * call, so a request's last bits may differ with the requests that share its call.
  */
 int fa_paged_fwd_ex(const void* Q, const void* K_cache, const void* V_cache, const void* K_exp, const void* V_exp,
                     void* O, float* LSE, const int* block_table, const int* cu_q, const int* seq_lens,
@@ -417,8 +418,9 @@ int fa_tree_mask(const int* parents, const int* cu_q, const int* ctx_lens, long 
  *   K_exps, V_exps     : NULL, or the same of the exponents of 8-bit caches.  No two of all these
  *                        tensors share bytes; a pointer given twice is refused
  *   strides   : {K page, K row, K head, V page, V row, V head} or NULL
- * A request whose path or count does not fit is left alone, a row on a page outside the cache stays
- * where it is; fa_check_device reports both (FA_ERR_INVALID_ARG).
+ * A request whose path or count does not fit is left alone (fa_page_trim_ex of the same path leaves it alone
+ * as well), a row on a page outside the cache stays where it is; fa_check_device reports both
+ * (FA_ERR_INVALID_ARG).
  */
 int fa_paged_keep(const int* path, const int* count, const int* cu_q, const int* seq_lens, const int* block_table,
                   void* const* K_caches, void* const* V_caches, void* const* K_exps, void* const* V_exps, int layers,
