@@ -264,3 +264,30 @@ def test_every_exponent_that_is_written(kernel):
     O, LSE = fa.fa_paged_fwd(Q, *caches, table, _cu(new), lens, K_exp=exps[0], V_exp=exps[1])
     assert _errors() == ""
     _check_requests(O, LSE, Q, caches, exps, table, lens, new, d ** -0.5, dt, lift=14 if dt == torch.float16 else 4)
+
+
+def test_fp16_queries_in_a_replayed_graph():
+    """Each replay looks at the rows that the cache holds then: they fit fp16, do not, and do again."""
+    dtype, H, H_kv, d, page, new = KERNELS["copy_f16"]
+    Q, caches, exps, table, lens = _setup(9, new, [40, 100], H, H_kv, d, page, torch.bfloat16, spread=1)
+    Q, args = Q.half(), (*caches, table, _cu(new), lens)
+    fit = [e.clone() for e in exps]
+    wide = [(fit[0].int() - 14).clamp(min=97).to(torch.uint8), fit[1]]
+    want = []
+    for values in (fit, wide):
+        for e, x in zip(exps, values):
+            e.copy_(x)
+        want.append(fa.fa_paged_fwd(Q, *args, K_exp=exps[0], V_exp=exps[1]))
+    assert not torch.equal(want[0][0], want[1][0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        O, LSE = fa.fa_paged_fwd(Q, *args, K_exp=exps[0], V_exp=exps[1])
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        for e, x in zip(exps, (fit, wide)[i]):
+            e.copy_(x)
+        O.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(O, want[i][0]) and torch.equal(LSE, want[i][1])
+    assert _errors() == ""
